@@ -455,6 +455,128 @@ int pmoe_router_topk(const float* logits, int T, int E, int K, int renormalize,
 int pmoe_finalize(const void* z, const int32_t* row_of_route, const float* topk_w,
                   int T, int K, int H, void* out, void* stream);
 
+/* ============================================================ router, training side
+ *
+ * A token is active when one of its ids is in [0, E) and one of its logits is
+ * not -inf; a token of padding (all ids -1, say) counts nowhere and has a zero
+ * gradient. Sequence s holds the tokens seq_offsets[s] .. seq_offsets[s+1] - 1;
+ * seq_offsets is int32 [S+1] on the device, ascending, from >= 0 to <= T, or
+ * NULL for one sequence of all tokens (S = 1). Sequences may be empty; tokens
+ * before the first or behind the last belong to none. With p = softmax(logits)
+ * over all E experts, lse = log sum exp(logits), n_s the active tokens and c_se
+ * the routes of sequence s to expert e:
+ *   balance_s = E * sum_e c_se / (n_s K) * sum_t p_te / n_s   (1 at an even load)
+ *   z_s       = sum_t lse_t^2 / n_s
+ * and both are 0 when n_s = 0.
+ */
+
+#define PMOE_MAX_SEQUENCES 65536
+
+/* Device workspace of pmoe_router_balance (bytes). 0 on bad shapes. */
+size_t pmoe_router_balance_workspace_bytes(int T, int E, int K, int S);
+
+/*
+ * Expert counts, balance loss and z-loss of each sequence.
+ *   logits      : float32 [T, E];  topk_ids : [T, K] int32 or int64 (ids_type), as
+ *                 pmoe_router_topk gives them; ids outside [0, E) are no routes
+ *   counts      : int32 [S, E] out, c_se;   tokens : int32 [S] out, n_s
+ *   prob        : float32 [S, E] out, sum_t p_te (not divided by n_s, so that
+ *                 counts, tokens and prob of several ranks can be added)
+ *   balance, z  : float32 [S] out
+ * T = 0 writes zeros. Sums over tokens are taken in a fixed order: the same
+ * inputs give the same bits. 1 <= E <= 1024, 1 <= K <= min(32, E), T*K < 2^30,
+ * 1 <= S <= PMOE_MAX_SEQUENCES. Alignment: ws 16 bytes, int64 ids 8, others 4.
+ */
+int pmoe_router_balance(const float* logits, const void* topk_ids, int ids_type, int T, int K, int E,
+                        const int32_t* seq_offsets, int S,
+                        int32_t* counts, int32_t* tokens, float* prob, float* balance, float* z,
+                        void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of the logits.
+ *   counts, tokens : of pmoe_router_balance, or their sums over ranks (then p of
+ *                    this rank's tokens meets the load of all)
+ *   d_balance, d_z : float32 [S], gradients of the two losses, or NULL
+ *   d_topk_w       : float32 [T, K], gradient of the weights of pmoe_router_topk
+ *                    called with the same `renormalize`, or NULL
+ *   d_logits       : float32 [T, E] out: the sum of the gradients that are given;
+ *                    every row is written. Tokens of no sequence have no part in the
+ *                    losses, but may have one in d_topk_w.
+ * counts is needed with d_balance, tokens with d_balance or d_z. With
+ * renormalize = 1 a token whose chosen experts all have p = 0 gets no gradient
+ * from d_topk_w. d_logits may be logits itself. Limits and alignment as above.
+ */
+int pmoe_router_backward(const float* logits, const void* topk_ids, int ids_type, int T, int K, int E,
+                         int renormalize, const int32_t* seq_offsets, int S,
+                         const int32_t* counts, const int32_t* tokens,
+                         const float* d_balance, const float* d_z, const float* d_topk_w,
+                         float* d_logits, void* stream);
+
+/*
+ * Gradients of the finalize (pmoe_finalize), for the FP32 sum before its rounding:
+ *   d_topk_w[t,j]       = sum_h dout[t,h] * z[row(t,j),h]   in FP32, 0 where row(t,j) < 0
+ *   d_z[row(t,j),:]     = bf16(w[t,j] * dout[t,:])
+ *   dout : BF16 [T, H];  z, d_z : BF16 [R, H];  row_of_route : int32 [T*K], a value
+ *   outside [0, R) is no route and no row is named twice (the routing names none
+ *   twice; of a row named twice d_z holds one of the two);  topk_w, d_topk_w : float32 [T, K].
+ * Either output may be NULL; z is needed for d_topk_w, topk_w for d_z. Rows of
+ * d_z that no route names are left as they were. H must be a multiple of 8.
+ * Alignment: dout, z and d_z 16 bytes, others 4 bytes.
+ */
+int pmoe_finalize_backward(const void* dout, const void* z, const int32_t* row_of_route,
+                           const float* topk_w, int T, int K, int H, int R,
+                           float* d_topk_w, void* d_z, void* stream);
+
+/* ============================================================ adapters
+ *
+ * Low-rank adapters of many requests beside one projection x [T, H] -> [T, N]
+ * (with N = H: beside the whole routed layer). Token t uses adapter
+ * a = adapter_ids[t]; ids outside [0, n) (-1, say) mean none. Tokens of one
+ * adapter need not be neighbours.
+ *   down : BF16 [n, R, H];  up : BF16 [n, N, R];  scale : float32 [n].
+ * H and N multiples of 16 in [16, 16384], R a multiple of 8 in [8, 128] (an
+ * adapter of a smaller rank has zeros in the rest), 1 <= n <= 65535, T <= 2^24;
+ * T*H and T*N may pass 2^31. Alignment: ws 256 bytes, ids and scale their own
+ * size, everything else 16 bytes. Runs on the caller's stream alone.
+ */
+
+#define PMOE_ADAPTER_MAX 65535
+#define PMOE_ADAPTER_MAX_TOKENS (1 << 24)
+
+/* Device workspace of pmoe_adapter_forward (backward = 0) or
+ * pmoe_adapter_backward (backward = 1), in bytes. 0 on bad arguments. */
+size_t pmoe_adapter_workspace_bytes(int T, int n, int H, int N, int R, int backward);
+
+/*
+ *   v[t]   = down[a] x[t]                                (FP32; 0 without an adapter)
+ *   out[t] = bf16(base[t] + scale[a] * up[a] v[t])       (base[t] without an adapter)
+ *   x : BF16 [T, H];  base : BF16 [T, N] or NULL (zeros);  out : BF16 [T, N], may be
+ *   base itself;  v : float32 [T, R] or NULL -- pmoe_adapter_backward wants it.
+ * Products and sums are FP32; scale * v enters the second product with 16
+ * significant bits. The bits of a token depend on that token, its adapter and
+ * the shapes only, not on the other tokens of the call.
+ */
+int pmoe_adapter_forward(const void* x, const void* adapter_ids, int ids_type, int T, int n, int H, int N,
+                         int R, const void* down, const void* up, const float* scale, const void* base,
+                         void* out, float* v, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradients for the gradient dy of out, du[t] = scale[a] * up[a]^T dy[t] in FP32:
+ *   dx[t]     = bf16(base[t] + down[a]^T du[t])          (base[t] without an adapter)
+ *   d_down[a] = sum of du[t] x[t]^T over the tokens of a      float32 [n, R, H]
+ *   d_up[a]   = scale[a] * sum of dy[t] v[t]^T                float32 [n, N, R]
+ *   dy : BF16 [T, N];  x, v as in the forward call;  base : BF16 [T, H], the gradient
+ *   that dx adds to, or NULL (zeros);  dx : BF16 [T, H], may be base itself.
+ * dx may be NULL (x has no gradient), or d_down and d_up both (the adapters are
+ * not trained; x and v are then not read). d_down and d_up are written whole,
+ * zeros for adapters without tokens, and their sums over tokens are taken in a
+ * fixed order. The gradient of base is dy itself.
+ */
+int pmoe_adapter_backward(const void* dy, const void* x, const float* v, const void* adapter_ids,
+                          int ids_type, int T, int n, int H, int N, int R, const void* down,
+                          const void* up, const float* scale, const void* base, void* dx,
+                          float* d_down, float* d_up, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,6 +8,7 @@ is no fallback implementation.
 """
 import ctypes
 import os
+from collections import namedtuple
 from dataclasses import dataclass
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -66,6 +67,17 @@ _SIGNATURES = {
     "pmoe_router_topk": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp]),
     "pmoe_moe_forward": (_i, [_vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp,
                               _vp, _i, ctypes.POINTER(MoeOptions), _vp, ctypes.c_size_t, _vp, _vp]),
+    "pmoe_router_balance_workspace_bytes": (ctypes.c_size_t, [_i, _i, _i, _i]),
+    "pmoe_router_balance": (_i, [_vp, _vp, _i, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp,
+                                 ctypes.c_size_t, _vp]),
+    "pmoe_router_backward": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp,
+                                  _vp]),
+    "pmoe_finalize_backward": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "pmoe_adapter_workspace_bytes": (ctypes.c_size_t, [_i, _i, _i, _i, _i, _i]),
+    "pmoe_adapter_forward": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                  ctypes.c_size_t, _vp]),
+    "pmoe_adapter_backward": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp,
+                                   _vp, _vp, _vp, ctypes.c_size_t, _vp]),
 }
 STEP_ROUTE, STEP_FC1, STEP_REQUANT, STEP_FC2, STEP_FINALIZE = range(5)
 
@@ -460,14 +472,27 @@ def routed_moe_ex(x, x_sf, x_scale, topk_ids, topk_w, weights: PreparedWeights, 
 
 def moe_forward(x, topk_ids, topk_w, weights: PreparedWeights, recipe="per_token",
                 finalize="ordered", swiglu_limit=0.0, a1=None, a2=None, act=None, expert_offset=0,
-                workspace=None, out=None, stream=None, streams=0, step_events=None):
+                workspace=None, out=None, stream=None, streams=0, step_events=None, adapters=None,
+                adapter_ids=None, adapter_workspace=None):
     """The whole routed layer from BF16 activations x [T, H] (pmoe_moe_forward): the NVFP4
     recipes quantize x inside the call, overlapped with the routing. step_events: None or
-    STEP_EVENTS torch.cuda.Events (timing enabled) recorded around the grouped GEMMs."""
+    STEP_EVENTS torch.cuda.Events (timing enabled) recorded around the grouped GEMMs.
+    adapters = (down, up, scale) with N = H adds, after the layer, each token's own adapter
+    adapter_ids[t] beside it (adapter_forward on x with the layer's BF16 output as its base)."""
+    import torch
     T, K = topk_ids.shape
     W = weights
     act = W.act if act is None else act
     x = _bf16_storage(x.contiguous())
+    if (adapters is None) != (adapter_ids is None):
+        raise ValueError("adapters and adapter_ids are wanted both or neither")
+    if adapters is not None:            # refused before the layer is enqueued
+        _, _, aT, _, aH, aN, *_ = _adapter_args(adapter_ids, *adapters)
+        if (aT, aH, aN) != (T, W.H, W.H):
+            raise ValueError("adapters of a layer must be [n, R, H] and [n, H, R], adapter_ids [T]")
+        _bf16(x, "x", (T, W.H))
+        if out is not None:
+            _out(out, "out", torch.bfloat16, (T, W.H), x.device)
     topk_ids, ids_type, topk_w = _routing_args(topk_ids, topk_w)
     workspace, out = _moe_buffers(T, K, W, act, x.device, workspace, out)
     evs = _event_array(step_events)
@@ -480,6 +505,9 @@ def moe_forward(x, topk_ids, topk_w, weights: PreparedWeights, recipe="per_token
         _ptr(W.w1_codes), _ptr(W.w1_scales), _ptr(W.w1_alpha), _ptr(W.w2_codes), _ptr(W.w2_scales),
         _ptr(W.w2_alpha), act, ctypes.byref(opt), _ptr(workspace), workspace.numel(), _ptr(out),
         _stream(stream, x, topk_ids, topk_w, a1, a2, workspace, out, W.w1_codes, W.w1_scales, W.w1_alpha, W.w2_codes, W.w2_scales, W.w2_alpha)))
+    if adapters is not None:
+        adapter_forward(x, adapter_ids, *adapters, base=out, out=out, need_v=False,
+                        workspace=adapter_workspace, stream=stream)
     return out
 
 
@@ -512,3 +540,202 @@ def finalize(z, row_of_route, topk_w, out=None, stream=None):
     _check(lib().pmoe_finalize(_ptr(z), _ptr(row_of_route), _ptr(topk_w), T, K, H, _ptr(out),
                                _stream(stream, z, row_of_route, topk_w, out)))
     return out
+
+
+# ----------------------------------------------------------------------------- router, training side
+RouterBalance = namedtuple("RouterBalance", "counts tokens prob balance z")
+
+
+def _is(t, name, dtype, shape):
+    """Checks the dtype and shape of a device tensor argument and returns it contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}".replace("torch.", ""))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.contiguous()
+
+
+def _out(t, name, dtype, shape, device):
+    """An output: allocated if None, else checked (it is written in place)."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _is(t, name, dtype, shape)
+
+
+def _ids(t, name):
+    import torch
+    if t.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{name} must be int32 or int64")
+    return t.contiguous(), IDS_INT32 if t.dtype == torch.int32 else IDS_INT64
+
+
+def _scratch(need, workspace, device):
+    import torch
+    if workspace is None:
+        return torch.empty(max(int(need), 256), dtype=torch.uint8, device=device)
+    return workspace
+
+
+def _sequences(seq_offsets):
+    import torch
+    if seq_offsets is None:
+        return None, 1
+    if seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
+        raise ValueError("seq_offsets must be a vector of S + 1 offsets")
+    return _is(seq_offsets, "seq_offsets", torch.int32, seq_offsets.shape), seq_offsets.numel() - 1
+
+
+def _router_args(logits, topk_ids):
+    import torch
+    if logits.dim() != 2 or topk_ids.dim() != 2:
+        raise ValueError("logits must be [T, E] and topk_ids [T, K]")
+    T, E = logits.shape
+    K = topk_ids.shape[1]
+    if topk_ids.shape[0] != T:
+        raise ValueError("logits and topk_ids must have the same number of tokens")
+    ids, ids_type = _ids(topk_ids, "topk_ids")
+    return _is(logits, "logits", torch.float32, (T, E)), ids, ids_type, T, K, E
+
+
+def router_balance_workspace_bytes(T, K, E, S=1):
+    size = lib().pmoe_router_balance_workspace_bytes(T, E, K, S)
+    if size == 0:
+        raise PmoeError(3, lib().pmoe_last_error().decode())
+    return int(size)
+
+
+def router_balance(logits, topk_ids, seq_offsets=None, out=None, workspace=None, stream=None):
+    """Expert counts, balance loss and z-loss of each sequence (pmoe_router_balance).
+
+    logits float32 [T, E], topk_ids [T, K] (ids outside [0, E) are no routes), seq_offsets
+    int32 [S+1] on the device or None for one sequence. Returns RouterBalance(counts int32
+    [S, E], tokens int32 [S], prob float32 [S, E], balance float32 [S], z float32 [S])."""
+    import torch
+    logits, ids, ids_type, T, K, E = _router_args(logits, topk_ids)
+    off, S = _sequences(seq_offsets)
+    given = out if out is not None else RouterBalance(None, None, None, None, None)
+    kinds = ((torch.int32, (S, E)), (torch.int32, (S,)), (torch.float32, (S, E)), (torch.float32, (S,)),
+             (torch.float32, (S,)))
+    res = RouterBalance(*(_out(t, f"out.{name}", dt, shape, logits.device)
+                          for name, t, (dt, shape) in zip(RouterBalance._fields, given, kinds)))
+    ws = _scratch(lib().pmoe_router_balance_workspace_bytes(T, E, K, S), workspace, logits.device)
+    _check(lib().pmoe_router_balance(
+        _ptr(logits), _ptr(ids), ids_type, T, K, E, _ptr(off), S, *(_ptr(t) for t in res), _ptr(ws),
+        ws.numel(), _stream(stream, logits, ids, off, ws, *res)))
+    return res
+
+
+def router_backward(logits, topk_ids, counts=None, tokens=None, d_balance=None, d_z=None, d_topk_w=None,
+                    renormalize=False, seq_offsets=None, out=None, stream=None):
+    """Gradient of the logits (pmoe_router_backward), float32 [T, E]: from the losses of
+    router_balance (d_balance, d_z float32 [S], with its counts and tokens) and from the
+    weights of router_topk (d_topk_w float32 [T, K]); at least one of the three."""
+    import torch
+    logits, ids, ids_type, T, K, E = _router_args(logits, topk_ids)
+    off, S = _sequences(seq_offsets)
+    f32, i32 = torch.float32, torch.int32
+    out = _out(out, "out", f32, (T, E), logits.device)
+    opt = [None if t is None else _is(t, name, dt, shape)
+           for t, name, dt, shape in ((counts, "counts", i32, (S, E)), (tokens, "tokens", i32, (S,)),
+                                      (d_balance, "d_balance", f32, (S,)), (d_z, "d_z", f32, (S,)),
+                                      (d_topk_w, "d_topk_w", f32, (T, K)))]
+    _check(lib().pmoe_router_backward(
+        _ptr(logits), _ptr(ids), ids_type, T, K, E, int(bool(renormalize)), _ptr(off), S,
+        *(_ptr(t) for t in opt), _ptr(out), _stream(stream, logits, ids, off, out, *opt)))
+    return out
+
+
+def finalize_backward(dout, z, row_of_route, topk_w, need_d_topk_w=True, need_d_z=True, out=None,
+                      stream=None):
+    """Gradients of finalize (pmoe_finalize_backward): (d_topk_w float32 [T, K], d_z BF16 [R, H])
+    from dout BF16 [T, H], z BF16 [R, H], row_of_route int32 [T*K] and topk_w float32 [T, K]; None
+    in the place of one that is not needed. A fresh d_z is not initialised in rows that no route
+    names. out = (d_topk_w, d_z), either of them None, is written in place."""
+    import torch
+    T, K = topk_w.shape
+    R, H = z.shape
+    dout = _bf16(dout, "dout", (T, H))
+    z = _bf16(z, "z", (R, H))
+    row = _is(row_of_route.reshape(-1), "row_of_route", torch.int32, (T * K,))
+    topk_w = _is(topk_w, "topk_w", torch.float32, (T, K))
+    given = out if out is not None else (None, None)
+    dw = _out(given[0], "d_topk_w", torch.float32, (T, K), z.device) if need_d_topk_w else None
+    dz = _out(given[1], "d_z", torch.bfloat16, (R, H), z.device) if need_d_z else None
+    _check(lib().pmoe_finalize_backward(
+        _ptr(dout), _ptr(z), _ptr(row), _ptr(topk_w), T, K, H, R, _ptr(dw), _ptr(dz),
+        _stream(stream, dout, z, row, topk_w, dw, dz)))
+    return dw, dz
+
+
+# ----------------------------------------------------------------------------- adapters
+def _bf16(t, name, shape):
+    import torch
+    return _is(t, name, torch.bfloat16, shape)
+
+
+def _adapter_args(adapter_ids, down, up, scale):
+    import torch
+    if down.dim() != 3 or up.dim() != 3 or adapter_ids.dim() != 1:
+        raise ValueError("adapter_ids must be [T], down [n, R, H] and up [n, N, R]")
+    n, R, H = down.shape
+    N = up.shape[1]
+    ids, ids_type = _ids(adapter_ids, "adapter_ids")
+    return (ids, ids_type, ids.shape[0], n, H, N, R, _bf16(down, "down", (n, R, H)),
+            _bf16(up, "up", (n, N, R)), _is(scale, "scale", torch.float32, (n,)))
+
+
+def adapter_workspace_bytes(T, n, H, N, R, backward=False):
+    size = lib().pmoe_adapter_workspace_bytes(T, n, H, N, R, int(bool(backward)))
+    if size == 0:
+        raise PmoeError(3, lib().pmoe_last_error().decode())
+    return int(size)
+
+
+def adapter_forward(x, adapter_ids, down, up, scale, base=None, out=None, v=None, need_v=True,
+                    workspace=None, stream=None):
+    """Low-rank adapters of many requests (pmoe_adapter_forward): token t of x BF16 [T, H] uses
+    adapter adapter_ids[t] (int32 or int64, outside [0, n): none) of down BF16 [n, R, H], up BF16
+    [n, N, R] and scale float32 [n]. Returns (out, v): out BF16 [T, N] = base + scale * up(v), v
+    float32 [T, R] = down(x), which adapter_backward wants (None with need_v False). base None
+    means zeros; out may be base."""
+    import torch
+    ids, ids_type, T, n, H, N, R, down, up, scale = _adapter_args(adapter_ids, down, up, scale)
+    x = _bf16(x, "x", (T, H))
+    if base is not None:
+        base = _bf16(base, "base", (T, N))
+    out = _out(out, "out", torch.bfloat16, (T, N), x.device)
+    v = _out(v, "v", torch.float32, (T, R), x.device) if need_v else None
+    ws = _scratch(lib().pmoe_adapter_workspace_bytes(T, n, H, N, R, 0), workspace, x.device)
+    _check(lib().pmoe_adapter_forward(
+        _ptr(x), _ptr(ids), ids_type, T, n, H, N, R, _ptr(down), _ptr(up), _ptr(scale), _ptr(base),
+        _ptr(out), _ptr(v), _ptr(ws), ws.numel(), _stream(stream, x, ids, down, up, scale, base, out, v, ws)))
+    return out, v
+
+
+def adapter_backward(dy, x, v, adapter_ids, down, up, scale, base=None, need_dx=True, need_weights=True,
+                     out=None, workspace=None, stream=None):
+    """Gradients of adapter_forward (pmoe_adapter_backward) for the gradient dy BF16 [T, N] of out:
+    (dx BF16 [T, H] = base + down^T(scale * up^T(dy)), d_down float32 [n, R, H], d_up float32
+    [n, N, R]), None in the place of what is not needed. base BF16 [T, H] is the gradient that dx
+    adds to (None: zeros); out = (dx, d_down, d_up), any of them None, is written in place and
+    its dx may be base."""
+    import torch
+    ids, ids_type, T, n, H, N, R, down, up, scale = _adapter_args(adapter_ids, down, up, scale)
+    dy = _bf16(dy, "dy", (T, N))
+    x = _bf16(x, "x", (T, H)) if need_weights else None
+    v = _is(v, "v", torch.float32, (T, R)) if need_weights else None
+    if base is not None:
+        base = _bf16(base, "base", (T, H))
+    dx, d_down, d_up = out if out is not None else (None, None, None)
+    dx = _out(dx, "dx", torch.bfloat16, (T, H), dy.device) if need_dx else None
+    d_down = _out(d_down, "d_down", torch.float32, (n, R, H), dy.device) if need_weights else None
+    d_up = _out(d_up, "d_up", torch.float32, (n, N, R), dy.device) if need_weights else None
+    ws = _scratch(lib().pmoe_adapter_workspace_bytes(T, n, H, N, R, 1), workspace, dy.device)
+    _check(lib().pmoe_adapter_backward(
+        _ptr(dy), _ptr(x), _ptr(v), _ptr(ids), ids_type, T, n, H, N, R, _ptr(down), _ptr(up), _ptr(scale),
+        _ptr(base), _ptr(dx), _ptr(d_down), _ptr(d_up), _ptr(ws), ws.numel(),
+        _stream(stream, dy, x, v, ids, down, up, scale, base, dx, d_down, d_up, ws)))
+    return dx, d_down, d_up

@@ -71,6 +71,25 @@ int check_ptr(const void* p, size_t align, const char* name) {
   return PMOE_OK;
 }
 
+// check_ptr, and the memory has to be the current device's: the kernels run there.
+int check_ptr_here(const void* p, size_t align, const char* name) {
+  const int rc = check_ptr(p, align, name);
+  if (rc != PMOE_OK) return rc;
+  int dev = 0;
+  hipPointerAttribute_t attr;
+  if (hipGetDevice(&dev) == hipSuccess && hipPointerGetAttributes(&attr, p) == hipSuccess &&
+      attr.type == hipMemoryTypeDevice && attr.device != dev)
+    return fail(PMOE_ERR_POINTER, std::string(name) + " is on device " + std::to_string(attr.device) +
+                                      ", the current device is " + std::to_string(dev));
+  return PMOE_OK;
+}
+
+// Whether [a, a + a_bytes) and [b, b + b_bytes) share a byte; null shares none.
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + b_bytes && y < x + a_bytes;
+}
+
 #define PMOE_TRY(expr)          \
   do {                          \
     int _rc = (expr);           \
@@ -181,7 +200,7 @@ int check_moe_shape(int T, int K, int E, int H, int I, int act) {
 
 // ================================================================== exports
 
-PMOE_EXPORT int pmoe_version(void) { return 200; }
+PMOE_EXPORT int pmoe_version(void) { return 300; }
 
 PMOE_EXPORT const char* pmoe_last_error(void) { return g_last_error.c_str(); }
 
@@ -818,6 +837,231 @@ PMOE_EXPORT int pmoe_router_topk(const float* logits, int T, int E, int K, int r
   PMOE_TRY(check_ptr(topk_w, 4, "topk_w"));
   PMOE_HIP(launch_router_topk(logits, T, E, K, renormalize, topk_ids, topk_w,
                               static_cast<hipStream_t>(stream)));
+  return ok();
+}
+
+// ------------------------------------------------------------------ router, training side
+namespace {
+
+int check_router_shape(int T, int E, int K, int S, const void* seq_offsets) {
+  if (T < 0) return fail(PMOE_ERR_SHAPE, "T must be >= 0");
+  if (E < 1 || E > kMaxExperts) return fail(PMOE_ERR_SHAPE, "E must be in [1, 1024]");
+  if (K < 1 || K > 32 || K > E) return fail(PMOE_ERR_SHAPE, "K must be in [1, min(32, E)]");
+  if ((long long)T * K >= (1LL << 31) / 2) return fail(PMOE_ERR_SHAPE, "T*K too large");
+  if (S < 1 || S > PMOE_MAX_SEQUENCES) return fail(PMOE_ERR_SHAPE, "S must be in [1, 65536]");
+  if (seq_offsets == nullptr && S != 1) return fail(PMOE_ERR_ARG, "S must be 1 without seq_offsets");
+  return PMOE_OK;
+}
+
+int check_ids(const void* ids, int ids_type, const char* name) {
+  if (ids_type != PMOE_IDS_INT32 && ids_type != PMOE_IDS_INT64)
+    return fail(PMOE_ERR_ARG, "ids_type must be PMOE_IDS_INT32 or PMOE_IDS_INT64");
+  return check_ptr_here(ids, ids_type == PMOE_IDS_INT64 ? 8 : 4, name);
+}
+
+}  // namespace
+
+PMOE_EXPORT size_t pmoe_router_balance_workspace_bytes(int T, int E, int K, int S) {
+  if (check_router_shape(T, E, K, S, &T) != PMOE_OK) return 0;
+  ok();
+  return balance_ws_bytes(T, E, S);
+}
+
+PMOE_EXPORT int pmoe_router_balance(const float* logits, const void* topk_ids, int ids_type, int T, int K,
+                                    int E, const int32_t* seq_offsets, int S, int32_t* counts,
+                                    int32_t* tokens, float* prob, float* balance, float* z, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  PMOE_TRY(check_router_shape(T, E, K, S, seq_offsets));
+  if (ids_type != PMOE_IDS_INT32 && ids_type != PMOE_IDS_INT64)
+    return fail(PMOE_ERR_ARG, "ids_type must be PMOE_IDS_INT32 or PMOE_IDS_INT64");
+  PMOE_TRY(check_device());
+  if (T > 0) {
+    PMOE_TRY(check_ptr_here(logits, 4, "logits"));
+    PMOE_TRY(check_ids(topk_ids, ids_type, "topk_ids"));
+  }
+  if (seq_offsets) PMOE_TRY(check_ptr_here(seq_offsets, 4, "seq_offsets"));
+  PMOE_TRY(check_ptr_here(counts, 4, "counts"));
+  PMOE_TRY(check_ptr_here(tokens, 4, "tokens"));
+  PMOE_TRY(check_ptr_here(prob, 4, "prob"));
+  PMOE_TRY(check_ptr_here(balance, 4, "balance"));
+  PMOE_TRY(check_ptr_here(z, 4, "z"));
+  PMOE_TRY(check_ptr_here(ws, 16, "ws"));
+  const size_t need = balance_ws_bytes(T, E, S);
+  if (ws_bytes < need)
+    return fail(PMOE_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
+  BalanceParams p{logits, topk_ids, ids_type == PMOE_IDS_INT64, T, E, K, seq_offsets, S,
+                  counts, tokens, prob, balance, z, ws};
+  PMOE_HIP(launch_router_balance(p, static_cast<hipStream_t>(stream)));
+  return ok();
+}
+
+PMOE_EXPORT int pmoe_router_backward(const float* logits, const void* topk_ids, int ids_type, int T, int K,
+                                     int E, int renormalize, const int32_t* seq_offsets, int S,
+                                     const int32_t* counts, const int32_t* tokens,
+                                     const float* d_balance, const float* d_z, const float* d_topk_w,
+                                     float* d_logits, void* stream) {
+  PMOE_TRY(check_router_shape(T, E, K, S, seq_offsets));
+  if (ids_type != PMOE_IDS_INT32 && ids_type != PMOE_IDS_INT64)
+    return fail(PMOE_ERR_ARG, "ids_type must be PMOE_IDS_INT32 or PMOE_IDS_INT64");
+  if (renormalize != 0 && renormalize != 1) return fail(PMOE_ERR_ARG, "renormalize must be 0 or 1");
+  if (T == 0) return ok();
+  if (!d_balance && !d_z && !d_topk_w)
+    return fail(PMOE_ERR_ARG, "one of d_balance, d_z and d_topk_w is needed");
+  if (d_balance && !counts) return fail(PMOE_ERR_ARG, "d_balance needs counts");
+  if ((d_balance || d_z) && !tokens) return fail(PMOE_ERR_ARG, "d_balance and d_z need tokens");
+  PMOE_TRY(check_device());
+  PMOE_TRY(check_ptr_here(logits, 4, "logits"));
+  PMOE_TRY(check_ids(topk_ids, ids_type, "topk_ids"));
+  if (seq_offsets) PMOE_TRY(check_ptr_here(seq_offsets, 4, "seq_offsets"));
+  if (d_balance) {
+    PMOE_TRY(check_ptr_here(d_balance, 4, "d_balance"));
+    PMOE_TRY(check_ptr_here(counts, 4, "counts"));
+  }
+  if (d_z) PMOE_TRY(check_ptr_here(d_z, 4, "d_z"));
+  if (d_balance || d_z) PMOE_TRY(check_ptr_here(tokens, 4, "tokens"));
+  if (d_topk_w) PMOE_TRY(check_ptr_here(d_topk_w, 4, "d_topk_w"));
+  PMOE_TRY(check_ptr_here(d_logits, 4, "d_logits"));
+  RouterGradParams p{logits, topk_ids, ids_type == PMOE_IDS_INT64, T, E, K, renormalize, seq_offsets, S,
+                     counts, d_balance || d_z ? tokens : nullptr, d_balance, d_z, d_topk_w, d_logits};
+  PMOE_HIP(launch_router_backward(p, static_cast<hipStream_t>(stream)));
+  return ok();
+}
+
+// ------------------------------------------------------------------ finalize, gradients
+PMOE_EXPORT int pmoe_finalize_backward(const void* dout, const void* z, const int32_t* row_of_route,
+                                       const float* topk_w, int T, int K, int H, int R, float* d_topk_w,
+                                       void* d_z, void* stream) {
+  if (T < 0 || K < 1 || K > 32) return fail(PMOE_ERR_SHAPE, "need T >= 0 and 1 <= K <= 32");
+  if ((long long)T * K >= (1LL << 31) / 2) return fail(PMOE_ERR_SHAPE, "T*K too large");
+  if (H <= 0 || H % 8 != 0) return fail(PMOE_ERR_SHAPE, "H must be a positive multiple of 8");
+  if (R < 0) return fail(PMOE_ERR_SHAPE, "R must be >= 0");
+  if (T == 0 || (R == 0 && !d_topk_w)) return ok();
+  if (!d_topk_w && !d_z) return fail(PMOE_ERR_ARG, "one of d_topk_w and d_z is needed");
+  PMOE_TRY(check_device());
+  PMOE_TRY(check_ptr_here(dout, 16, "dout"));
+  PMOE_TRY(check_ptr_here(row_of_route, 4, "row_of_route"));
+  if (d_topk_w) {
+    if (R > 0) PMOE_TRY(check_ptr_here(z, 16, "z"));
+    PMOE_TRY(check_ptr_here(d_topk_w, 4, "d_topk_w"));
+  }
+  if (d_z) {
+    PMOE_TRY(check_ptr_here(topk_w, 4, "topk_w"));
+    if (R > 0) PMOE_TRY(check_ptr_here(d_z, 16, "d_z"));
+    const size_t rows = (size_t)R * H * 2;
+    if (overlap(d_z, rows, z, rows) || overlap(d_z, rows, dout, (size_t)T * H * 2))
+      return fail(PMOE_ERR_ARG, "d_z overlaps an input");
+  }
+  PMOE_HIP(launch_finalize_backward(static_cast<const uint16_t*>(dout), static_cast<const uint16_t*>(z),
+                                    row_of_route, topk_w, T, K, H, R, d_topk_w,
+                                    static_cast<uint16_t*>(d_z), static_cast<hipStream_t>(stream)));
+  return ok();
+}
+
+// ------------------------------------------------------------------ adapters
+namespace {
+
+int check_adapter_shape(int T, int n, int H, int N, int R) {
+  if (T < 0 || T > PMOE_ADAPTER_MAX_TOKENS) return fail(PMOE_ERR_SHAPE, "T must be in [0, 2^24]");
+  if (n < 1 || n > PMOE_ADAPTER_MAX) return fail(PMOE_ERR_SHAPE, "n must be in [1, 65535]");
+  if (!dim_ok(H)) return fail(PMOE_ERR_SHAPE, "H" PMOE_DIM_RULE);
+  if (!dim_ok(N)) return fail(PMOE_ERR_SHAPE, "N" PMOE_DIM_RULE);
+  if (R < 8 || R > 128 || R % 8 != 0) return fail(PMOE_ERR_SHAPE, "R must be a multiple of 8 in [8, 128]");
+  return PMOE_OK;
+}
+
+}  // namespace
+
+PMOE_EXPORT size_t pmoe_adapter_workspace_bytes(int T, int n, int H, int N, int R, int backward) {
+  if (check_adapter_shape(T, n, H, N, R) != PMOE_OK) return 0;
+  if (backward != 0 && backward != 1) {
+    fail(PMOE_ERR_ARG, "backward must be 0 or 1");
+    return 0;
+  }
+  ok();
+  return std::max<size_t>(kAlign, backward ? adapter_backward_ws_bytes(T, n, H, N, R)
+                                           : adapter_forward_ws_bytes(T, H, R));
+}
+
+PMOE_EXPORT int pmoe_adapter_forward(const void* x, const void* adapter_ids, int ids_type, int T, int n,
+                                     int H, int N, int R, const void* down, const void* up,
+                                     const float* scale, const void* base, void* out, float* v, void* ws,
+                                     size_t ws_bytes, void* stream) {
+  PMOE_TRY(check_adapter_shape(T, n, H, N, R));
+  if (ids_type != PMOE_IDS_INT32 && ids_type != PMOE_IDS_INT64)
+    return fail(PMOE_ERR_ARG, "ids_type must be PMOE_IDS_INT32 or PMOE_IDS_INT64");
+  if (T == 0) return ok();
+  PMOE_TRY(check_device());
+  PMOE_TRY(check_ptr_here(x, 16, "x"));
+  PMOE_TRY(check_ids(adapter_ids, ids_type, "adapter_ids"));
+  PMOE_TRY(check_ptr_here(down, 16, "down"));
+  PMOE_TRY(check_ptr_here(up, 16, "up"));
+  PMOE_TRY(check_ptr_here(scale, 4, "scale"));
+  if (base) PMOE_TRY(check_ptr_here(base, 16, "base"));
+  PMOE_TRY(check_ptr_here(out, 16, "out"));
+  if (v) PMOE_TRY(check_ptr_here(v, 16, "v"));
+  PMOE_TRY(check_ptr_here(ws, 256, "ws"));
+  const size_t need = adapter_forward_ws_bytes(T, H, R);
+  if (ws_bytes < need)
+    return fail(PMOE_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
+  const size_t out_bytes = (size_t)T * N * 2;
+  if ((base != out && overlap(out, out_bytes, base, out_bytes)) ||
+      overlap(out, out_bytes, x, (size_t)T * H * 2))
+    return fail(PMOE_ERR_ARG, "out may be base itself, but overlaps no other input");
+  AdapterParams p{};
+  p.x = x, p.ids = adapter_ids, p.ids64 = ids_type == PMOE_IDS_INT64;
+  p.T = T, p.n = n, p.H = H, p.N = N, p.R = R;
+  p.down = down, p.up = up, p.scale = scale, p.base = base, p.out = out, p.v_out = v, p.ws = ws;
+  PMOE_HIP(launch_adapter_forward(p, static_cast<hipStream_t>(stream)));
+  return ok();
+}
+
+PMOE_EXPORT int pmoe_adapter_backward(const void* dy, const void* x, const float* v,
+                                      const void* adapter_ids, int ids_type, int T, int n, int H, int N,
+                                      int R, const void* down, const void* up, const float* scale,
+                                      const void* base, void* dx, float* d_down, float* d_up, void* ws,
+                                      size_t ws_bytes, void* stream) {
+  PMOE_TRY(check_adapter_shape(T, n, H, N, R));
+  if (ids_type != PMOE_IDS_INT32 && ids_type != PMOE_IDS_INT64)
+    return fail(PMOE_ERR_ARG, "ids_type must be PMOE_IDS_INT32 or PMOE_IDS_INT64");
+  if ((d_down == nullptr) != (d_up == nullptr))
+    return fail(PMOE_ERR_ARG, "d_down and d_up are wanted both or neither");
+  if (T == 0 && !d_down) return ok();
+  if (!dx && !d_down) return fail(PMOE_ERR_ARG, "dx or d_down and d_up are needed");
+  if (base && !dx) return fail(PMOE_ERR_ARG, "base needs dx");
+  PMOE_TRY(check_device());
+  if (T > 0) {
+    PMOE_TRY(check_ptr_here(dy, 16, "dy"));
+    PMOE_TRY(check_ids(adapter_ids, ids_type, "adapter_ids"));
+    PMOE_TRY(check_ptr_here(up, 16, "up"));
+    if (dx) {
+      PMOE_TRY(check_ptr_here(down, 16, "down"));
+      if (base) PMOE_TRY(check_ptr_here(base, 16, "base"));
+      PMOE_TRY(check_ptr_here(dx, 16, "dx"));
+    }
+  }
+  PMOE_TRY(check_ptr_here(scale, 4, "scale"));
+  if (d_down) {
+    if (T > 0) {
+      PMOE_TRY(check_ptr_here(x, 16, "x"));
+      PMOE_TRY(check_ptr_here(v, 16, "v"));
+    }
+    PMOE_TRY(check_ptr_here(d_down, 16, "d_down"));
+    PMOE_TRY(check_ptr_here(d_up, 16, "d_up"));
+  }
+  PMOE_TRY(check_ptr_here(ws, 256, "ws"));
+  const size_t need = adapter_backward_ws_bytes(T, n, H, N, R);
+  if (ws_bytes < need)
+    return fail(PMOE_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
+  const size_t dx_bytes = (size_t)T * H * 2;
+  if ((base != dx && overlap(dx, dx_bytes, base, dx_bytes)) || overlap(dx, dx_bytes, dy, (size_t)T * N * 2) ||
+      overlap(dx, dx_bytes, x, dx_bytes))
+    return fail(PMOE_ERR_ARG, "dx may be base itself, but overlaps no other input");
+  AdapterParams p{};
+  p.x = x, p.ids = adapter_ids, p.ids64 = ids_type == PMOE_IDS_INT64;
+  p.T = T, p.n = n, p.H = H, p.N = N, p.R = R;
+  p.down = down, p.up = up, p.scale = scale, p.base = base, p.out = dx, p.dy = dy, p.v_in = v;
+  p.d_down = d_down, p.d_up = d_up, p.ws = ws;
+  PMOE_HIP(launch_adapter_backward(p, static_cast<hipStream_t>(stream)));
   return ok();
 }
 

@@ -111,9 +111,67 @@ hipError_t launch_finalize(const uint16_t* z, const int* row_of_route, const flo
 // Fused finalize: zero the FP32 accumulator [n] before FC2, round it to BF16 after.
 hipError_t launch_fill_zero(float* p, long n, hipStream_t s);
 hipError_t launch_f32_to_bf16(const float* in, long n, uint16_t* out, hipStream_t s);
+// Gradients of the finalize; d_w or d_z may be null.
+hipError_t launch_finalize_backward(const uint16_t* dout, const uint16_t* z, const int* row_of_route,
+                                    const float* w, int T, int K, int H, int R, float* d_w,
+                                    uint16_t* d_z, hipStream_t s);
 
 // ---------------------------------------------------------------- router
 hipError_t launch_router_topk(const float* logits, int T, int E, int K, int renorm, int* ids,
                               float* w, hipStream_t s);
+struct BalanceParams {
+  const float* logits;  // [T][E]
+  const void* ids;      // [T][K], int32 or int64 (ids64)
+  int ids64;
+  int T, E, K;
+  const int* offsets;   // [S+1] or null: one sequence of all T tokens
+  int S;
+  int* counts;          // [S][E]
+  int* tokens;          // [S]
+  float* prob;          // [S][E]
+  float* balance;       // [S]
+  float* z;             // [S]
+  void* ws;             // balance_ws_bytes
+};
+size_t balance_ws_bytes(int T, int E, int S);
+hipError_t launch_router_balance(const BalanceParams& p, hipStream_t s);
+struct RouterGradParams {
+  const float* logits;
+  const void* ids;
+  int ids64;
+  int T, E, K, renorm;
+  const int* offsets;
+  int S;
+  const int* counts;       // with d_balance
+  const int* tokens;       // with d_balance or d_z
+  const float* d_balance;  // [S] or null
+  const float* d_z;        // [S] or null
+  const float* d_topk_w;   // [T][K] or null
+  float* d_logits;         // [T][E]
+};
+hipError_t launch_router_backward(const RouterGradParams& p, hipStream_t s);
+
+// ---------------------------------------------------------------- adapters
+struct AdapterParams {
+  const void* x;       // BF16 [T][H]
+  const void* ids;     // [T], int32 or int64 (ids64)
+  int ids64;
+  int T, n, H, N, R;
+  const void* down;    // BF16 [n][R][H]
+  const void* up;      // BF16 [n][N][R]
+  const float* scale;  // [n]
+  const void* base;    // forward BF16 [T][N], backward [T][H]; null: zeros
+  void* out;           // BF16, as base; backward: dx, may be null
+  float* v_out;        // forward: [T][R] or null
+  const void* dy;      // backward: BF16 [T][N]
+  const float* v_in;   // backward: [T][R]
+  float* d_down;       // backward: [n][R][H] or null
+  float* d_up;         // backward: [n][N][R] or null, with d_down
+  void* ws;
+};
+size_t adapter_forward_ws_bytes(int T, int H, int R);
+size_t adapter_backward_ws_bytes(int T, int n, int H, int N, int R);
+hipError_t launch_adapter_forward(const AdapterParams& p, hipStream_t s);
+hipError_t launch_adapter_backward(const AdapterParams& p, hipStream_t s);
 
 }  // namespace pmoe
