@@ -57,7 +57,7 @@ int check_device() {
 }
 
 // ------------------------------------------------------------------ pointer check
-int check_ptr(const void* p, size_t align, const char* name) {
+int check_ptr(const void* p, size_t align, const char* name, int device = -1) {
   if (p == nullptr) return fail(PMOE_ERR_POINTER, std::string(name) + " is null");
   if (reinterpret_cast<uintptr_t>(p) % align != 0)
     return fail(PMOE_ERR_POINTER, std::string(name) + " is not " + std::to_string(align) + "-byte aligned");
@@ -68,20 +68,17 @@ int check_ptr(const void* p, size_t align, const char* name) {
   }
   if (attr.type != hipMemoryTypeDevice && attr.type != hipMemoryTypeManaged)
     return fail(PMOE_ERR_POINTER, std::string(name) + " is not device memory");
+  if (device >= 0 && attr.type == hipMemoryTypeDevice && attr.device != device)
+    return fail(PMOE_ERR_POINTER, std::string(name) + " is on device " + std::to_string(attr.device) +
+                                      ", the current device is " + std::to_string(device));
   return PMOE_OK;
 }
 
 // check_ptr, and the memory has to be the current device's: the kernels run there.
 int check_ptr_here(const void* p, size_t align, const char* name) {
-  const int rc = check_ptr(p, align, name);
-  if (rc != PMOE_OK) return rc;
-  int dev = 0;
-  hipPointerAttribute_t attr;
-  if (hipGetDevice(&dev) == hipSuccess && hipPointerGetAttributes(&attr, p) == hipSuccess &&
-      attr.type == hipMemoryTypeDevice && attr.device != dev)
-    return fail(PMOE_ERR_POINTER, std::string(name) + " is on device " + std::to_string(attr.device) +
-                                      ", the current device is " + std::to_string(dev));
-  return PMOE_OK;
+  int dev = -1;
+  (void)hipGetDevice(&dev);  // check_device has found it valid
+  return check_ptr(p, align, name, dev);
 }
 
 // Whether [a, a + a_bytes) and [b, b + b_bytes) share a byte; null shares none.
