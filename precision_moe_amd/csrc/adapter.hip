@@ -8,12 +8,14 @@
 // R is small (8 .. 128), so x, dy, base and the outputs are what has to move;
 // the matrices of one adapter stay in the caches while its tokens pass.
 //
-// Grouping. Tokens need not be sorted. A workgroup owns 64 consecutive tokens;
-// every wave finds by ballots which of them share an adapter and works on one
-// such group after the other, its rows gathered into blocks of 16 (the width of
-// one MFMA). No plan is built and nothing is kept between calls. In a prompt
-// the 64 tokens are one or two groups; in a decode step they may be 64, and
-// then gridDim.z workgroups share the groups of one block of tokens.
+// Grouping. Tokens need not be sorted, and no plan is kept between calls. The
+// first kernel of a call takes 1024 tokens (a span) at a time, puts them into an
+// order in which the tokens of an adapter are neighbours, and cuts that order into
+// units of at most 64 tokens of one adapter, whose rows are gathered into blocks of
+// 16 (the width of one MFMA). Every workgroup of the span does so for itself, in
+// LDS; one of them leaves the order and the units in the workspace for the kernels
+// that follow. Requests that are runs of tokens are taken as they stand; otherwise
+// the span is sorted.
 //
 // Bits of a token do not depend on the other tokens of the call: a column of an
 // MFMA depends on its own operand column only, and how a sum over H (or N) is
@@ -31,7 +33,10 @@ namespace pmoe {
 
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 
-constexpr int kTok = 64;  // tokens of one workgroup
+constexpr int kUnit = 64;    // tokens of one unit at most
+constexpr int kSpan = 1024;  // tokens that are grouped together
+constexpr int kNone = 0xFFFF;  // "adapter" of tokens without one (adapters are below 65535)
+constexpr int kMostRuns = 16;  // boundaries up to which a span is not sorted
 
 __device__ __forceinline__ floatx4 mfma16(bf16x8_t a, bf16x8_t b, floatx4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -44,32 +49,119 @@ __device__ __forceinline__ int adapter_of(const void* ids, int ids64, long t, in
   return id >= 0 && id < n ? (int)id : -1;
 }
 
-// The groups of a block of 64 tokens, one after the other, the same in every
-// wave. After next(): `adapter` and `count` of the group; lane m of `member`
-// holds the place (0..63) of the group's m-th token for m < count.
-struct Groups {
-  int id;          // of this lane's token; -1: none, -2: behind the last token
-  uint64_t left;   // tokens not yet handled
-  int adapter, count, member;
-  __device__ __forceinline__ Groups(const void* ids, int ids64, long t0, int T, int n, bool with_none,
-                                    int lane) {
-    id = t0 + lane < T ? adapter_of(ids, ids64, t0 + lane, n) : -2;
-    left = __ballot(id >= (with_none ? -1 : 0));
-  }
-  __device__ __forceinline__ bool next(int lane) {
-    if (left == 0) return false;
-    adapter = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-    const uint64_t match = __ballot(id == adapter);
-    left &= ~match;
-    count = __popcll(match);
-    const uint64_t below = lane == 0 ? 0ull : (~0ull >> (64 - lane));
-    // members to the front, the others behind them: every lane sends its place
-    const int in = __popcll(match & below);
-    const int to = (match >> lane) & 1 ? in : count + (lane - in);
-    member = __builtin_amdgcn_ds_permute(to * 4, lane);
-    return true;
-  }
+// Order and units of a span: unit u holds the places [start[u], start[u + 1]) of
+// the order; key = adapter << 10 | token of the span.
+struct SpanLds {
+  uint32_t key[kSpan];
+  uint16_t start[kSpan + 8];
+  int wave[2][4];
 };
+// The same in the workspace, one for each span.
+struct SpanOrder {
+  uint32_t key[kSpan];
+  uint16_t start[kSpan];
+  int units, count;
+  int pad[2];
+};
+
+__device__ __forceinline__ int wave_inclusive_sum(int v, int lane) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int y = __shfl_up(v, off, 64);
+    if (lane >= off) v += y;
+  }
+  return v;
+}
+
+// Groups the tokens [t0, t0 + count) with a workgroup of 256 threads; returns
+// the number of units. Ends with a barrier.
+__device__ __forceinline__ int group_span(const void* ids, int ids64, long t0, int count, int n, SpanLds& l) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+#pragma unroll
+  for (int j = 0; j < kSpan / 256; ++j) {
+    const int i = tid + 256 * j;
+    uint32_t k = 0xFFFFFFFFu;
+    if (i < count) {
+      const int a = adapter_of(ids, ids64, t0 + i, n);
+      k = (uint32_t)(a < 0 ? kNone : a) << 10 | (uint32_t)i;
+    }
+    l.key[i] = k;
+  }
+  __syncthreads();
+  int edges = 0;
+#pragma unroll
+  for (int j = 0; j < kSpan / 256; ++j) {
+    const int i = tid + 256 * j;
+    edges += __popcll(__ballot(i > 0 && i < count && l.key[i] >> 10 != l.key[max(i, 1) - 1] >> 10));
+  }
+  if (lane == 0) l.wave[0][wave] = edges;
+  __syncthreads();
+  if (l.wave[0][0] + l.wave[0][1] + l.wave[0][2] + l.wave[0][3] > kMostRuns) {
+    int size = 64;
+    while (size < count) size *= 2;
+    for (int k = 2; k <= size; k *= 2)
+      for (int d = k / 2; d > 0; d /= 2) {
+        for (int i = tid; i < size / 2; i += 256) {
+          const int x = (i & ~(d - 1)) * 2 + (i & (d - 1)), y = x + d;
+          const uint32_t p = l.key[x], q = l.key[y];
+          if ((p > q) == ((x & k) == 0)) {
+            l.key[x] = q;
+            l.key[y] = p;
+          }
+        }
+        __syncthreads();
+      }
+  }
+  // Units. Thread t looks at the places 4 t .. 4 t + 3.
+  const uint4 mine = *reinterpret_cast<const uint4*>(&l.key[4 * tid]);
+  const uint32_t k[5] = {tid > 0 ? l.key[4 * tid - 1] : 0xFFFFFFFFu, mine.x, mine.y, mine.z, mine.w};
+  int first[4], last = -1;  // the start of the group that a place belongs to, -1: further back
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if ((tid == 0 && j == 0) || k[j + 1] >> 10 != k[j] >> 10) last = 4 * tid + j;
+    first[j] = last;
+  }
+  int back = last;  // inclusive maximum over the threads
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) back = max(back, __shfl_up(back, off, 64));
+  if (lane == 63) l.wave[0][wave] = back;
+  back = __shfl_up(back, 1, 64);  // exclusive; lane 0 has none within the wave
+  if (lane == 0) back = -1;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) back = max(back, l.wave[0][w]);
+  int starts = 0;
+  bool is[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int at = 4 * tid + j, from = first[j] >= 0 ? first[j] : back;
+    is[j] = at < count && ((at - from) & (kUnit - 1)) == 0;
+    starts += is[j];
+  }
+  int before = wave_inclusive_sum(starts, lane);
+  if (lane == 63) l.wave[1][wave] = before;
+  before -= starts;
+  __syncthreads();
+  int units = 0;
+  for (int w = 0; w < 4; ++w) {
+    if (w < wave) before += l.wave[1][w];
+    units += l.wave[1][w];
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (is[j]) l.start[before++] = (uint16_t)(4 * tid + j);
+  if (tid == 0) l.start[units] = (uint16_t)count;
+  __syncthreads();
+  return units;
+}
+
+__device__ __forceinline__ void keep_order(const SpanLds& l, int units, int count, SpanOrder* o) {
+  for (int i = threadIdx.x; i < count; i += 256) o->key[i] = l.key[i];
+  for (int i = threadIdx.x; i < units; i += 256) o->start[i] = l.start[i];
+  if (threadIdx.x == 0) {
+    o->units = units;
+    o->count = count;
+  }
+}
 
 // ---------------------------------------------------------------- reduction over H (or N)
 // Parts of the sum over a row of D elements: gridDim.y workgroups of four waves
@@ -81,78 +173,134 @@ int adapter_parts(int D) {
 }
 static int adapter_span(int D) { return ((D + adapter_parts(D) * 4 - 1) / (adapter_parts(D) * 4) + 63) / 64 * 64; }
 
-// 16 elements of column r of W [D][R] from row k on, as the two operands that
-// belong to 16 consecutive elements of a row.
-__device__ __forceinline__ void load_column16(const uint16_t* w, int R, uint4& lo, uint4& hi) {
-  uint32_t v[8];
+// Eight rows of kCols columns each, turned: op[b] gets the eight values of
+// column b, ready as an MFMA operand. kCols is 1, 2, 4 or 8.
+template <int kCols>
+struct Rows8 {
+  static constexpr int kWords = kCols < 2 ? 1 : kCols / 2;
+  uint32_t w[8][kWords];
+  __device__ __forceinline__ void load(int j, const uint16_t* p, bool on) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = (uint32_t)w[(long)(2 * i) * R] | ((uint32_t)w[(long)(2 * i + 1) * R] << 16);
-  lo = make_uint4(v[0], v[1], v[2], v[3]);
-  hi = make_uint4(v[4], v[5], v[6], v[7]);
-}
+    for (int i = 0; i < kWords; ++i) w[j][i] = 0;
+    if (!on) return;
+    if constexpr (kCols == 1) {
+      w[j][0] = *p;
+    } else if constexpr (kCols == 2) {
+      w[j][0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (kCols == 4) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      w[j][0] = u.x, w[j][1] = u.y;
+    } else {
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      w[j][0] = u.x, w[j][1] = u.y, w[j][2] = u.z, w[j][3] = u.w;
+    }
+  }
+  __device__ __forceinline__ bf16x8_t column(int b) const {
+    const uint32_t sel = b & 1 ? 0x07060302u : 0x05040100u;
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = __builtin_amdgcn_perm(w[2 * j + 1][b / 2], w[2 * j][b / 2], sel);
+    return as_bf16x8(make_uint4(o[0], o[1], o[2], o[3]));
+  }
+};
 
 // part[y][t][r] = sum over the y-th part of in[t][k] * W_a[r][k] (kTrans: W_a[k][r]).
+// blockIdx.x is a span and one of `share` workgroups that take its units in turn.
+// Operand row i of block b is r = NR i + b, so that a lane ends with 4 NR consecutive r of
+// one token, and with kTrans a lane reads NR neighbouring columns of eight rows.
 template <int NR, bool kTrans>
 __global__ __launch_bounds__(256) void adapter_reduce_kernel(
     const uint16_t* __restrict__ in, const void* __restrict__ ids, int ids64, int T, int n, int D, int R,
-    const uint16_t* __restrict__ W, int span, float* __restrict__ part) {
+    const uint16_t* __restrict__ W, int span, int share, SpanOrder* __restrict__ orders,
+    float* __restrict__ part) {
+  constexpr int kSteps = NR <= 4 ? 2 : 1;  // steps of 64 that are loaded together
+  __shared__ __align__(16) SpanLds lds;
   __shared__ floatx4 red[4][NR][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = lane & 15, g = lane >> 4;
-  const long t0 = (long)blockIdx.x * kTok;
+  const int sp = blockIdx.x / share, mine = blockIdx.x % share;
+  const long t0 = (long)sp * kSpan;
+  const int count = (int)min((long)kSpan, T - t0);
+  const int units = group_span(ids, ids64, t0, count, n, lds);
+  if (mine == 0 && blockIdx.y == 0) keep_order(lds, units, count, orders + sp);
   const int k_begin = (blockIdx.y * 4 + wave) * span, k_end = min(D, k_begin + span);
   float* dst = part + (long)blockIdx.y * T * R;
-  Groups grp(ids, ids64, t0, T, n, false, lane);
-  for (int gi = 0; grp.next(lane); ++gi) {
-    if (gi % gridDim.z != blockIdx.z) continue;
-    const int nf = (grp.count + 15) >> 4;
+  for (int u = mine; u < units; u += share) {
+    const int at = lds.start[u], len = lds.start[u + 1] - at;
+    const int adapter = lds.key[at] >> 10;
+    if (adapter == kNone) continue;
+    const int nf = (len + 15) >> 4;
     const uint16_t* x[4];
-    bool on[4];
 #pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      const int m = 16 * f + col;
-      on[f] = m < grp.count;
-      x[f] = in + (t0 + __shfl(grp.member, on[f] ? m : 0, 64)) * D;
-    }
-    const uint16_t* w = W + (long)grp.adapter * R * D;
+    for (int f = 0; f < 4; ++f)
+      x[f] = in + (t0 + (lds.key[at + min(16 * f + col, len - 1)] & (kSpan - 1))) * D;
+    const uint16_t* w = W + (long)adapter * R * D;
     floatx4 acc[4][NR];
 #pragma unroll
     for (int f = 0; f < 4; ++f)
 #pragma unroll
       for (int c = 0; c < NR; ++c) acc[f][c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k0 = k_begin; k0 < k_end; k0 += 64) {
-      const int k = k0 + 16 * g;  // D is a multiple of 16: these 16 elements are in or out together
-      const bool in_row = k < k_end;
-      uint4 wl[NR], wh[NR];
+    const int r0 = NR * col;
+    for (int k0 = k_begin; k0 < k_end; k0 += 64 * kSteps) {
+      uint4 xv[kSteps][4][2];
 #pragma unroll
-      for (int c = 0; c < NR; ++c) {
-        const int r = 16 * c + col;
-        wl[c] = wh[c] = make_uint4(0, 0, 0, 0);
-        if (in_row && r < R) {
-          if (kTrans) {
-            load_column16(w + (long)k * R + r, R, wl[c], wh[c]);
-          } else {
-            wl[c] = *reinterpret_cast<const uint4*>(w + (long)r * D + k);
-            wh[c] = *reinterpret_cast<const uint4*>(w + (long)r * D + k + 8);
+      for (int q = 0; q < kSteps; ++q) {
+        const int k = k0 + 64 * q + 16 * g;  // D is a multiple of 16: 16 elements are in or out together
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          xv[q][f][0] = xv[q][f][1] = make_uint4(0, 0, 0, 0);
+          if (f < nf && k < k_end && 16 * f + col < len) {
+            xv[q][f][0] = *reinterpret_cast<const uint4*>(x[f] + k);
+            xv[q][f][1] = *reinterpret_cast<const uint4*>(x[f] + k + 8);
+          }
+        }
+      }
+      bf16x8_t wv[kSteps][NR][2];
+      if constexpr (kTrans) {
+        Rows8<NR> rows[kSteps][2];
+#pragma unroll
+        for (int q = 0; q < kSteps; ++q) {
+          const int k = k0 + 64 * q + 16 * g;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            rows[q][j >> 3].load(j & 7, w + (long)(k + j) * R + r0, k < k_end && r0 < R);
+        }
+#pragma unroll
+        for (int q = 0; q < kSteps; ++q)
+#pragma unroll
+          for (int c = 0; c < NR; ++c) {
+            wv[q][c][0] = rows[q][0].column(c);
+            wv[q][c][1] = rows[q][1].column(c);
+          }
+      } else {
+#pragma unroll
+        for (int q = 0; q < kSteps; ++q) {
+          const int k = k0 + 64 * q + 16 * g;
+#pragma unroll
+          for (int c = 0; c < NR; ++c) {
+            uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+            if (k < k_end && r0 + c < R) {
+              lo = *reinterpret_cast<const uint4*>(w + (long)(r0 + c) * D + k);
+              hi = *reinterpret_cast<const uint4*>(w + (long)(r0 + c) * D + k + 8);
+            }
+            wv[q][c][0] = as_bf16x8(lo);
+            wv[q][c][1] = as_bf16x8(hi);
           }
         }
       }
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        if (f >= nf) continue;
-        uint4 xl = make_uint4(0, 0, 0, 0), xh = xl;
-        if (in_row && on[f]) {
-          xl = *reinterpret_cast<const uint4*>(x[f] + k);
-          xh = *reinterpret_cast<const uint4*>(x[f] + k + 8);
-        }
+      for (int q = 0; q < kSteps; ++q)
 #pragma unroll
-        for (int c = 0; c < NR; ++c) {
-          acc[f][c] = mfma16(as_bf16x8(wl[c]), as_bf16x8(xl), acc[f][c]);
-          acc[f][c] = mfma16(as_bf16x8(wh[c]), as_bf16x8(xh), acc[f][c]);
+        for (int f = 0; f < 4; ++f) {
+          if (f >= nf) continue;
+#pragma unroll
+          for (int c = 0; c < NR; ++c) {
+            acc[f][c] = mfma16(wv[q][c][0], as_bf16x8(xv[q][f][0]), acc[f][c]);
+            acc[f][c] = mfma16(wv[q][c][1], as_bf16x8(xv[q][f][1]), acc[f][c]);
+          }
         }
-      }
     }
-    // the four waves' sums, in wave order
+    // the four waves' sums, in wave order; value (c, lane, i) is r = 4 NR g + NR i + c
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       if (f >= nf) continue;
@@ -160,11 +308,16 @@ __global__ __launch_bounds__(256) void adapter_reduce_kernel(
       for (int c = 0; c < NR; ++c) red[wave][c][lane] = acc[f][c];
       __syncthreads();
       const int m = 16 * f + col;
-      const long t = t0 + __shfl(grp.member, m, 64);
-      for (int c = wave; c < NR; c += 4) {
-        const floatx4 s = ((red[0][c][lane] + red[1][c][lane]) + red[2][c][lane]) + red[3][c][lane];
-        const int r = 16 * c + 4 * g;
-        if (m < grp.count && r < R) *reinterpret_cast<floatx4*>(dst + t * R + r) = s;
+      const long t = t0 + (lds.key[at + min(m, len - 1)] & (kSpan - 1));
+      for (int q = wave; q < NR; q += 4) {
+        floatx4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = (4 * q + e) / NR, c = (4 * q + e) % NR;
+          v[e] = ((red[0][c][lane][i] + red[1][c][lane][i]) + red[2][c][lane][i]) + red[3][c][lane][i];
+        }
+        const int r = 4 * NR * g + 4 * q;
+        if (m < len && r < R) *reinterpret_cast<floatx4*>(dst + t * R + r) = v;
       }
       __syncthreads();
     }
@@ -172,196 +325,172 @@ __global__ __launch_bounds__(256) void adapter_reduce_kernel(
 }
 
 // ---------------------------------------------------------------- expansion to N (or H)
-// x = hi + lo in BF16, 16 significant bits. An infinite x has lo = 0.
-__device__ __forceinline__ void split2(float x, uint16_t& hi, uint16_t& lo) {
-  hi = (uint16_t)f32_to_bf16(x);
-  const float rest = x - bf16_to_f32(hi);
-  lo = (uint16_t)f32_to_bf16(__builtin_fabsf(x) == __builtin_inff() ? 0.0f : rest);
+// Two values as hi + lo in BF16, 16 significant bits each. An infinite value has lo = 0.
+__device__ __forceinline__ float finite_rest(float x, float hi) {
+  return __builtin_fabsf(x) == __builtin_inff() ? 0.0f : x - hi;
+}
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = f32x2_to_bf16x2(x, y);
+  lo = f32x2_to_bf16x2(finite_rest(x, bf16_to_f32(hi & 0xFFFFu)), finite_rest(y, bf16_to_f32(hi >> 16)));
 }
 
-// Rows of the low-rank vectors of a group in LDS: the sum of the parts (in
+// Rows of the low-rank vectors of a unit in LDS: the sum of the parts (in
 // order) times the adapter's scale, as hi and lo. With R <= 16 one row holds
 // hi[16] lo[16], which fill the 32 k of one MFMA; with more, hi[] and lo[] are
 // planes of whole steps of 32 that meet the same operand of the matrix.
 template <int NR>
 struct LowRows {
   static constexpr int kSteps = NR == 1 ? 1 : NR / 2;
-  static constexpr int kWidth = NR == 1 ? 32 : 2 * 32 * kSteps;  // BF16 values of a row
-  static constexpr int kStride = kWidth + 8;
-  uint16_t v[kTok][kStride];
+  static constexpr int kLo = NR == 1 ? 16 : 32 * kSteps;  // where lo begins
+  static constexpr int kStride = 2 * kLo + 8;
+  uint16_t v[kUnit][kStride];
 };
+
+// Adds base to 16 consecutive FP32 columns of a token and stores them in BF16.
+// c[j] is column j.
+__device__ __forceinline__ void store16(uint16_t* out, const float (&c)[16], const uint4 (&base)[2]) {
+  uint32_t o[8];
+  const uint32_t b[8] = {base[0].x, base[0].y, base[0].z, base[0].w, base[1].x, base[1].y, base[1].z, base[1].w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    o[j] = f32x2_to_bf16x2(bf16_to_f32(b[j] & 0xFFFFu) + c[2 * j], bf16_to_f32(b[j] >> 16) + c[2 * j + 1]);
+  *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
+  *reinterpret_cast<uint4*>(out + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+}
 
 // out[t][c] = bf16(base[t][c] + sum_r low[t][r] W_a[c][r]) (kTrans: W_a[r][c]),
 // low = scale * (sum of the parts). Workgroups with blockIdx.y == 0 also write the sum
 // of the parts to `sums` (times the scale if scale_sums), 0 without an adapter.
+// A wave takes 64 columns at a time. Operand row i of block b is column
+// 16 (i / 4) + 4 b + i % 4, with kTrans column 4 i + b; either way a lane's four blocks end
+// as 16 consecutive columns of one token, and four lanes write a line of 128 bytes. With
+// kTrans W_a has its columns contiguous while an operand wants eight r of one column: a
+// lane reads four columns of eight rows and turns them in registers.
 template <int NR, bool kTrans>
 __global__ __launch_bounds__(256) void adapter_expand_kernel(
-    const float* __restrict__ part, int parts, const void* __restrict__ ids, int ids64, int T, int n,
+    const float* __restrict__ part, int parts, const SpanOrder* __restrict__ orders, int share, int T,
     int D, int R, const uint16_t* __restrict__ W, const float* __restrict__ scale,
     const uint16_t* base, uint16_t* out, float* __restrict__ sums, int scale_sums, int chunk) {
   using Low = LowRows<NR>;
   __shared__ __align__(16) Low low;
+  __shared__ int place[kUnit];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int col = lane & 15, g = lane >> 4;
-  const long t0 = (long)blockIdx.x * kTok;
+  const int sp = blockIdx.x / share;
+  const SpanOrder* order = orders + sp;
+  const int units = order->units;
+  const long t0 = (long)sp * kSpan;
   const int c_begin = blockIdx.y * chunk, c_end = min(D, c_begin + chunk);
   // tokens without an adapter: base, or zeros
   const bool fill = out != nullptr && base != out;
-  Groups grp(ids, ids64, t0, T, n, true, lane);
-  for (int gi = 0; grp.next(lane); ++gi) {
-    if (gi % gridDim.z != blockIdx.z) continue;
-    if (grp.adapter < 0) {
-      for (int m = 0; m < grp.count; ++m) {
-        const long t = t0 + __builtin_amdgcn_readlane(grp.member, m);
-        if (fill)
-          for (int c = c_begin + tid * 8; c < c_end; c += 2048)
-            *reinterpret_cast<uint4*>(out + t * D + c) =
-                base ? *reinterpret_cast<const uint4*>(base + t * D + c) : make_uint4(0, 0, 0, 0);
-        if (blockIdx.y == 0 && sums != nullptr)
-          for (int r = tid; r < R; r += 256) sums[t * R + r] = 0.0f;
-      }
+  for (int u = blockIdx.x % share; u < units; u += share) {
+    const int at = order->start[u], len = (u + 1 < units ? order->start[u + 1] : order->count) - at;
+    const int adapter = order->key[at] >> 10;
+    __syncthreads();  // the unit before is no longer read
+    if (tid < kUnit) place[tid] = order->key[at + min(tid, len - 1)] & (kSpan - 1);
+    __syncthreads();
+    if (adapter == kNone) {
+      if (fill)
+        for (int m = wave; m < len; m += 4) {
+          const long row = (t0 + place[m]) * D;
+          for (int c = c_begin + lane * 8; c < c_end; c += 512)
+            *reinterpret_cast<uint4*>(out + row + c) =
+                base ? *reinterpret_cast<const uint4*>(base + row + c) : make_uint4(0, 0, 0, 0);
+        }
+      if (blockIdx.y == 0 && sums != nullptr)
+        for (int i = tid; i < len * R; i += 256) sums[(t0 + place[i / R]) * R + i % R] = 0.0f;
       continue;
     }
-    const int nf = (grp.count + 15) >> 4;
-    const float s = scale[grp.adapter];
-    __syncthreads();  // the rows of the group before are no longer read
-    for (int i = tid; i < nf * 16 * (16 * NR / 4); i += 256) {
-      const int m = i / (16 * NR / 4), r = i % (16 * NR / 4) * 4;
-      const long t = t0 + __shfl(grp.member, m, 64);  // whole waves come here
+    const int nf = (len + 15) >> 4;
+    const float s = scale[adapter];
+    for (int i = tid; i < nf * 16 * (4 * NR); i += 256) {
+      const int m = i / (4 * NR), r = i % (4 * NR) * 4;
+      const long t = t0 + place[m];
       floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (m < grp.count && r < R) {
-        for (int p = 0; p < parts; ++p)
-          v += *reinterpret_cast<const floatx4*>(part + ((long)p * T + t) * R + r);
+      if (m < len && r < R) {
+        floatx4 q[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          if (p < parts) q[p] = *reinterpret_cast<const floatx4*>(part + ((long)p * T + t) * R + r);
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          if (p < parts) v += q[p];
         if (blockIdx.y == 0 && sums != nullptr)
           *reinterpret_cast<floatx4*>(sums + t * R + r) = scale_sums ? v * s : v;
       }
-      uint16_t hi[4], lo[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) split2(v[j] * s, hi[j], lo[j]);
-      const int lo_at = NR == 1 ? 16 : Low::kWidth / 2;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        low.v[m][r + j] = hi[j];
-        low.v[m][lo_at + r + j] = lo[j];
-      }
+      uint2 hi, lo;
+      split2(v[0] * s, v[1] * s, hi.x, lo.x);
+      split2(v[2] * s, v[3] * s, hi.y, lo.y);
+      *reinterpret_cast<uint2*>(&low.v[m][r]) = hi;
+      *reinterpret_cast<uint2*>(&low.v[m][Low::kLo + r]) = lo;
     }
     __syncthreads();
     if (out == nullptr) continue;
-    const uint16_t* w = W + (long)grp.adapter * R * D;
-    if (!kTrans) {
-      // 64 columns at a time: operand row i of block b is column 16 (i / 4) + 4 b + i % 4, so
-      // that a lane's four blocks end as 16 consecutive columns of one token.
-      for (int c0 = c_begin + 64 * wave; c0 < c_end; c0 += 256) {
-        uint4 wop[Low::kSteps][4];
+    const uint16_t* w = W + (long)adapter * R * D;
+    for (int c0 = c_begin + 64 * wave; c0 < c_end; c0 += 256) {
+      const int c = c0 + 16 * g;  // the lane's columns of the result
+      uint4 bv[4][2];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        bv[f][0] = bv[f][1] = make_uint4(0, 0, 0, 0);
+        if (f < nf && base && 16 * f + col < len && c < D) {
+          const uint16_t* b = base + (t0 + place[16 * f + col]) * D + c;
+          bv[f][0] = *reinterpret_cast<const uint4*>(b);
+          bv[f][1] = *reinterpret_cast<const uint4*>(b + 8);
+        }
+      }
+      bf16x8_t wop[Low::kSteps][4];
+      if constexpr (kTrans) {
+        Rows8<4> rows[Low::kSteps];
+        const int cc = c0 + 4 * col;
+#pragma unroll
+        for (int q = 0; q < Low::kSteps; ++q) {
+          const int r = NR == 1 ? 8 * (g & 1) : 32 * q + 8 * g;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) rows[q].load(j, w + (long)(r + j) * D + cc, cc < D && r < R);
+        }
+#pragma unroll
+        for (int q = 0; q < Low::kSteps; ++q)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) wop[q][b] = rows[q].column(b);
+      } else {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const int c = c0 + 16 * (col >> 2) + 4 * b + (col & 3);
+          const int cc = c0 + 16 * (col >> 2) + 4 * b + (col & 3);
 #pragma unroll
           for (int q = 0; q < Low::kSteps; ++q) {
             const int r = NR == 1 ? 8 * (g & 1) : 32 * q + 8 * g;
-            wop[q][b] = make_uint4(0, 0, 0, 0);
-            if (c < D && r < R) wop[q][b] = *reinterpret_cast<const uint4*>(w + (long)c * R + r);
-          }
-        }
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          if (f >= nf) continue;
-          floatx4 acc[4];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) acc[b] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-          const uint16_t* row = low.v[16 * f + col];
-#pragma unroll
-          for (int q = 0; q < Low::kSteps; ++q) {
-            const uint4 vh = *reinterpret_cast<const uint4*>(row + 32 * q + 8 * g);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) acc[b] = mfma16(as_bf16x8(wop[q][b]), as_bf16x8(vh), acc[b]);
-            if (NR > 1) {
-              const uint4 vl = *reinterpret_cast<const uint4*>(row + Low::kWidth / 2 + 32 * q + 8 * g);
-#pragma unroll
-              for (int b = 0; b < 4; ++b) acc[b] = mfma16(as_bf16x8(wop[q][b]), as_bf16x8(vl), acc[b]);
-            }
-          }
-          const int m = 16 * f + col, c = c0 + 16 * g;
-          const long at = (t0 + __shfl(grp.member, m, 64)) * D + c;
-          if (m < grp.count && c < D) {
-            uint32_t o[8];
-            uint32_t bv[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (base) {
-              const uint4 b0 = *reinterpret_cast<const uint4*>(base + at);
-              const uint4 b1 = *reinterpret_cast<const uint4*>(base + at + 8);
-              bv[0] = b0.x, bv[1] = b0.y, bv[2] = b0.z, bv[3] = b0.w;
-              bv[4] = b1.x, bv[5] = b1.y, bv[6] = b1.z, bv[7] = b1.w;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              o[j] = f32x2_to_bf16x2(bf16_to_f32(bv[j] & 0xFFFFu) + acc[j / 2][2 * (j & 1)],
-                                     bf16_to_f32(bv[j] >> 16) + acc[j / 2][2 * (j & 1) + 1]);
-            *reinterpret_cast<uint4*>(out + at) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(out + at + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (cc < D && r < R) v = *reinterpret_cast<const uint4*>(w + (long)cc * R + r);
+            wop[q][b] = as_bf16x8(v);
           }
         }
       }
-    } else {
-      // 128 columns at a time. W_a has its columns contiguous, an operand wants eight r of one
-      // column: lane (col, g) loads eight rows r of the columns 8 col .. 8 col + 7 and turns
-      // that 8 x 8 block in registers; operand row i of block b is column 8 i + b, so a lane
-      // ends with the 32 consecutive columns 32 g + 8 i + b of one token.
-      for (int c0 = c_begin + 128 * wave; c0 < c_end; c0 += 512) {
-        floatx4 acc[4][8];
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
+      for (int f = 0; f < 4; ++f) {
+        if (f >= nf) continue;
+        floatx4 acc[4];
 #pragma unroll
-          for (int b = 0; b < 8; ++b) acc[f][b] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-        const int c = c0 + 8 * col;
+        for (int b = 0; b < 4; ++b) acc[b] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+        const uint16_t* row = low.v[16 * f + col];
 #pragma unroll
         for (int q = 0; q < Low::kSteps; ++q) {
-          const int r0 = NR == 1 ? 8 * (g & 1) : 32 * q + 8 * g;
-          uint32_t in[8][4];
+          const uint4 vh = *reinterpret_cast<const uint4*>(row + 32 * q + 8 * g);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (c < D && r0 < R) u = *reinterpret_cast<const uint4*>(w + (long)(r0 + j) * D + c);
-            in[j][0] = u.x, in[j][1] = u.y, in[j][2] = u.z, in[j][3] = u.w;
-          }
+          for (int b = 0; b < 4; ++b) acc[b] = mfma16(wop[q][b], as_bf16x8(vh), acc[b]);
+          if (NR > 1) {
+            const uint4 vl = *reinterpret_cast<const uint4*>(row + Low::kLo + 32 * q + 8 * g);
 #pragma unroll
-          for (int b = 0; b < 8; ++b) {
-            const uint32_t sel = b & 1 ? 0x07060302u : 0x05040100u;
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = __builtin_amdgcn_perm(in[2 * j + 1][b / 2], in[2 * j][b / 2], sel);
-            const bf16x8_t wop = as_bf16x8(make_uint4(o[0], o[1], o[2], o[3]));
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              if (f >= nf) continue;
-              const uint16_t* row = low.v[16 * f + col];
-              acc[f][b] = mfma16(wop, as_bf16x8(*reinterpret_cast<const uint4*>(row + 32 * q + 8 * g)), acc[f][b]);
-              if (NR > 1)
-                acc[f][b] = mfma16(wop, as_bf16x8(*reinterpret_cast<const uint4*>(
-                                            row + Low::kWidth / 2 + 32 * q + 8 * g)), acc[f][b]);
-            }
+            for (int b = 0; b < 4; ++b) acc[b] = mfma16(wop[q][b], as_bf16x8(vl), acc[b]);
           }
         }
+        if (16 * f + col < len && c < D) {
+          float res[16];
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          if (f >= nf) continue;
-          const int m = 16 * f + col;
-          const long t = t0 + __shfl(grp.member, m, 64);
+          for (int b = 0; b < 4; ++b)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int cc = c0 + 32 * g + 8 * i;
-            if (m < grp.count && cc < D) {
-              const long at = t * D + cc;
-              uint4 bb = make_uint4(0, 0, 0, 0);
-              if (base) bb = *reinterpret_cast<const uint4*>(base + at);
-              const uint32_t bv[4] = {bb.x, bb.y, bb.z, bb.w};
-              uint32_t o[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                o[j] = f32x2_to_bf16x2(bf16_to_f32(bv[j] & 0xFFFFu) + acc[f][2 * j][i],
-                                       bf16_to_f32(bv[j] >> 16) + acc[f][2 * j + 1][i]);
-              *reinterpret_cast<uint4*>(out + at) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
-          }
+            for (int i = 0; i < 4; ++i) res[kTrans ? 4 * i + b : 4 * b + i] = acc[b][i];
+          store16(out + (t0 + place[16 * f + col]) * D + c, res, bv[f]);
         }
       }
     }
@@ -369,16 +498,19 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(
 }
 
 // ---------------------------------------------------------------- gradients of the matrices
-// x = h + m + l in BF16: all 24 bits of an FP32 value (in range; an infinite x has m = l = 0).
-__device__ __forceinline__ void split3(float x, uint32_t& h, uint32_t& m, uint32_t& l) {
-  h = f32_to_bf16(x);
-  const float r1 = __builtin_fabsf(x) == __builtin_inff() ? 0.0f : x - bf16_to_f32(h);
-  m = f32_to_bf16(r1);
-  l = f32_to_bf16(r1 - bf16_to_f32(m));
+// Two values as h + m + l in BF16: all 24 bits of an FP32 value. An infinite value has
+// m = l = 0.
+__device__ __forceinline__ void split3(float x, float y, uint32_t& h, uint32_t& m, uint32_t& l) {
+  h = f32x2_to_bf16x2(x, y);
+  const float x1 = finite_rest(x, bf16_to_f32(h & 0xFFFFu)), y1 = finite_rest(y, bf16_to_f32(h >> 16));
+  m = f32x2_to_bf16x2(x1, y1);
+  l = f32x2_to_bf16x2(x1 - bf16_to_f32(m & 0xFFFFu), y1 - bf16_to_f32(m >> 16));
 }
 
-constexpr int kSegMax = 4096;  // tokens of one segment, whose list of one adapter is kept in LDS
-constexpr int kGradCols = 128;
+constexpr int kSegMax = 4096;  // tokens of one segment at most; an adapter's are listed in LDS
+// Columns of one workgroup of adapter_grad_kernel, 16 NB: with R <= 32 NB = 8, above (where
+// there are four blocks of r) NB = 4, so that the accumulators leave room for two waves.
+static int grad_cols(int R) { return R <= 32 ? 128 : 64; }
 
 struct GradParams {
   const uint16_t* x;    // [T][H]
@@ -392,98 +524,106 @@ struct GradParams {
   float* d_up;          // [n][N][R], likewise
 };
 
-// One workgroup: adapter blockIdx.y, segment blockIdx.z, 128 columns of x (dA)
+// One workgroup: adapter blockIdx.y, segment blockIdx.z, 16 NB columns of x (dA)
 // or, behind those, of dy (dB), and 16 NR values of r (with R > 64 there are two
-// such halves: more than 4 x 8 accumulators of 4 do not fit the registers). The adapter's tokens of the segment are listed
-// in LDS, the waves take every fourth step of 32 of them. k is the token here,
-// so both operands are wanted with eight tokens of one column: x (dy) is turned
-// in registers as in the expansion, du (s v) is read column by column.
-template <int NR>
-__global__ __launch_bounds__(256) void adapter_grad_kernel(GradParams p) {
-  __shared__ int list[kSegMax + 32];
+// such halves). The
+// adapter's tokens of the segment are listed in LDS, the waves take every fourth
+// step of 32 of them, the rows of the next step on their way during one. k is the
+// token here, so both operands are wanted with eight tokens of one column: x (dy)
+// is turned in registers, du (s v) is read column by column.
+template <int NR, int NB>
+__global__ __launch_bounds__(256, 2) void adapter_grad_kernel(GradParams p) {
+  __shared__ __align__(16) int list[kSegMax + 32];
   __shared__ int wave_count[4];
-  __shared__ floatx4 red[4][8][64];
+  __shared__ floatx4 red[4][NB][64];
+  constexpr int kCols = 16 * NB;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int col = lane & 15, g = lane >> 4;
   const int a = blockIdx.y, seg0 = blockIdx.z * p.seg;
   const int seg1 = min(p.T, seg0 + p.seg);
-  const int down_chunks = (p.H + kGradCols - 1) / kGradCols;
-  const int chunks = down_chunks + (p.N + kGradCols - 1) / kGradCols;
+  const int down_chunks = (p.H + kCols - 1) / kCols;
+  const int chunks = down_chunks + (p.N + kCols - 1) / kCols;
   const int chunk = blockIdx.x % chunks, r_begin = blockIdx.x / chunks * (16 * NR);
   const bool down = chunk < down_chunks;
-  const int c0 = (down ? chunk : chunk - down_chunks) * kGradCols;
+  const int c0 = (down ? chunk : chunk - down_chunks) * kCols;
   const int D = down ? p.H : p.N, R = p.R;
   const uint16_t* in = down ? p.x : p.dy;
   const float* low = down ? p.du : p.v;
   const float s = down ? 1.0f : p.scale[a];
-  // the adapter's tokens, in order
-  int have = 0;
-  for (int b = seg0; b < seg1; b += 256) {
-    const int t = b + tid;
-    const bool mine = t < seg1 && adapter_of(p.ids, p.ids64, t, p.n) == a;
-    const uint64_t match = __ballot(mine);
-    if (lane == 0) wave_count[wave] = __popcll(match);
-    __syncthreads();
-    int at = have;
-    for (int w = 0; w < 4; ++w) {
-      if (w < wave) at += wave_count[w];
-      have += wave_count[w];
-    }
-    const uint64_t below = lane == 0 ? 0ull : (~0ull >> (64 - lane));
-    if (mine) list[at + __popcll(match & below)] = t;
-    __syncthreads();
+  // the adapter's tokens, in order: thread t looks at the t-th 16 of the segment
+  uint32_t hit = 0;
+#pragma unroll
+  for (int j = 0; j < kSegMax / 256; ++j) {
+    const int t = seg0 + tid * (kSegMax / 256) + j;
+    if (t < seg1 && adapter_of(p.ids, p.ids64, t, p.n) == a) hit |= 1u << j;
   }
+  const int incl = wave_inclusive_sum(__popc(hit), lane);
+  if (lane == 63) wave_count[wave] = incl;
+  __syncthreads();
+  int at = incl - __popc(hit), have = 0;
+  for (int w = 0; w < 4; ++w) {
+    if (w < wave) at += wave_count[w];
+    have += wave_count[w];
+  }
+#pragma unroll
+  for (int j = 0; j < kSegMax / 256; ++j)
+    if (hit >> j & 1) list[at++] = seg0 + tid * (kSegMax / 256) + j;
   if (tid < 32) list[have + tid] = -1;
   __syncthreads();
-  floatx4 acc[NR][8];
+  floatx4 acc[NR][NB];
 #pragma unroll
   for (int c = 0; c < NR; ++c)
 #pragma unroll
-    for (int b = 0; b < 8; ++b) acc[c][b] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int cc = c0 + 8 * col;
-  for (int k0 = 32 * wave; k0 < have; k0 += 128) {
-    int tok[8];
-    uint32_t q[8][4];
+    for (int b = 0; b < NB; ++b) acc[c][b] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int cc = c0 + NB * col;
+  Rows8<NB> next;
+  int tok[8];
+  const auto fetch = [&](int k0) {
+    const int4 t0 = *reinterpret_cast<const int4*>(&list[k0 + 8 * g]);
+    const int4 t1 = *reinterpret_cast<const int4*>(&list[k0 + 8 * g + 4]);
+    const int t[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      tok[j] = list[k0 + 8 * g + j];
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (tok[j] >= 0 && cc < D) u = *reinterpret_cast<const uint4*>(in + (long)tok[j] * D + cc);
-      q[j][0] = u.x, q[j][1] = u.y, q[j][2] = u.z, q[j][3] = u.w;
+      tok[j] = t[j];
+      next.load(j, in + (long)t[j] * D + cc, t[j] >= 0 && cc < D);
     }
-    bf16x8_t op[8];
+  };
+  if (32 * wave < have) fetch(32 * wave);
+  for (int k0 = 32 * wave; k0 < have; k0 += 128) {
+    bf16x8_t op[NB];
+    float lv[NR][8];
 #pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      const uint32_t sel = b & 1 ? 0x07060302u : 0x05040100u;
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = __builtin_amdgcn_perm(q[2 * j + 1][b / 2], q[2 * j][b / 2], sel);
-      op[b] = as_bf16x8(make_uint4(o[0], o[1], o[2], o[3]));
-    }
-#pragma unroll
-    for (int c = 0; c < NR; ++c) {
-      const int r = r_begin + 16 * c + col;
-      uint32_t h[8], m[8], l[8];
+    for (int c = 0; c < NR; ++c)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float f = tok[j] >= 0 && r < R ? low[(long)tok[j] * R + r] * s : 0.0f;
-        split3(f, h[j], m[j], l[j]);
+        const int r = r_begin + 16 * c + col;
+        lv[c][j] = tok[j] >= 0 && r < R ? low[(long)tok[j] * R + r] : 0.0f;
       }
-      uint4 ho, mo, lo;
-      ho = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-      mo = make_uint4(m[0] | m[1] << 16, m[2] | m[3] << 16, m[4] | m[5] << 16, m[6] | m[7] << 16);
-      lo = make_uint4(l[0] | l[1] << 16, l[2] | l[3] << 16, l[4] | l[5] << 16, l[6] | l[7] << 16);
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        if (down) {  // rows: columns of x, columns: r
-          acc[c][b] = mfma16(op[b], as_bf16x8(lo), acc[c][b]);
-          acc[c][b] = mfma16(op[b], as_bf16x8(mo), acc[c][b]);
-          acc[c][b] = mfma16(op[b], as_bf16x8(ho), acc[c][b]);
-        } else {     // rows: r, columns: columns of dy
-          acc[c][b] = mfma16(as_bf16x8(lo), op[b], acc[c][b]);
-          acc[c][b] = mfma16(as_bf16x8(mo), op[b], acc[c][b]);
-          acc[c][b] = mfma16(as_bf16x8(ho), op[b], acc[c][b]);
-        }
+    for (int b = 0; b < NB; ++b) op[b] = next.column(b);
+    if (k0 + 128 < have) fetch(k0 + 128);
+#pragma unroll
+    for (int c = 0; c < NR; ++c) {
+      uint32_t h[4], m[4], l[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split3(lv[c][2 * j] * s, lv[c][2 * j + 1] * s, h[j], m[j], l[j]);
+      const bf16x8_t ho = as_bf16x8(make_uint4(h[0], h[1], h[2], h[3]));
+      const bf16x8_t mo = as_bf16x8(make_uint4(m[0], m[1], m[2], m[3]));
+      const bf16x8_t lo = as_bf16x8(make_uint4(l[0], l[1], l[2], l[3]));
+      if (down) {  // rows: columns of x, columns: r
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[c][b] = mfma16(op[b], lo, acc[c][b]);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[c][b] = mfma16(op[b], mo, acc[c][b]);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[c][b] = mfma16(op[b], ho, acc[c][b]);
+      } else {     // rows: r, columns: columns of dy
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[c][b] = mfma16(lo, op[b], acc[c][b]);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[c][b] = mfma16(mo, op[b], acc[c][b]);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[c][b] = mfma16(ho, op[b], acc[c][b]);
       }
     }
   }
@@ -492,29 +632,26 @@ __global__ __launch_bounds__(256) void adapter_grad_kernel(GradParams p) {
 #pragma unroll
   for (int c = 0; c < NR; ++c) {
 #pragma unroll
-    for (int b = 0; b < 8; ++b) red[wave][b][lane] = acc[c][b];
+    for (int b = 0; b < NB; ++b) red[wave][b][lane] = acc[c][b];
     __syncthreads();
     if (down) {
-      // value (b, lane (col, g), i) is row r = r_begin + 16 c + col, column c0 + 32 g + 8 i + b
-      const int r16 = tid >> 4, gg = (tid & 15) >> 2, i = tid & 3;
-      const int r = r_begin + 16 * c + r16, h = c0 + 32 * gg + 8 * i;
-      float v[8];
+      // value (b, lane (col, g), i) is row r = r_begin + 16 c + col, column c0 + NB (4 g + i) + b
+      const int r16 = tid >> 4, gi = tid & 15;
+      const int r = r_begin + 16 * c + r16, h = c0 + NB * gi, ln = (gi >> 2) * 16 + r16;
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        const int ln = gg * 16 + r16;
-        v[b] = ((red[0][b][ln][i] + red[1][b][ln][i]) + red[2][b][ln][i]) + red[3][b][ln][i];
-      }
-      if (r < R && h < D) {
-        float* dst = p.d_down + (slot * R + r) * D + h;
-        *reinterpret_cast<floatx4*>(dst) = floatx4{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<floatx4*>(dst + 4) = floatx4{v[4], v[5], v[6], v[7]};
+      for (int q = 0; q < NB; q += 4) {
+        floatx4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = ((red[0][q + e][ln][gi & 3] + red[1][q + e][ln][gi & 3]) + red[2][q + e][ln][gi & 3]) +
+                 red[3][q + e][ln][gi & 3];
+        if (r < R && h < D) *reinterpret_cast<floatx4*>(p.d_down + (slot * R + r) * D + h + q) = v;
       }
     } else {
-      // value (b, lane (col, g), i) is row c0 + 8 col + b, column r = r_begin + 16 c + 4 g + i
-      const int row = tid >> 1, b = row & 7, cl = row >> 3;
+      // value (b, lane (col, g), i) is row c0 + NB col + b, column r = r_begin + 16 c + 4 g + i
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int gg = 2 * (tid & 1) + k, ln = gg * 16 + cl;
+      for (int item = tid; item < kCols * 4; item += 256) {
+        const int row = item >> 2, gg = item & 3, b = row % NB, ln = gg * 16 + row / NB;
         const floatx4 v = ((red[0][b][ln] + red[1][b][ln]) + red[2][b][ln]) + red[3][b][ln];
         const int r = r_begin + 16 * c + 4 * gg;
         if (r < R && c0 + row < D) *reinterpret_cast<floatx4*>(p.d_up + (slot * D + c0 + row) * R + r) = v;
@@ -524,13 +661,19 @@ __global__ __launch_bounds__(256) void adapter_grad_kernel(GradParams p) {
   }
 }
 
-// out[i] = sum over the segments, in order.
-__global__ __launch_bounds__(256) void adapter_sum_kernel(const floatx4* __restrict__ part, int segments,
-                                                          long n4, floatx4* __restrict__ out) {
-  for (long i = blockIdx.x * 256L + threadIdx.x; i < n4; i += (long)gridDim.x * 256) {
-    floatx4 v = part[i];
-    for (int s = 1; s < segments; ++s) v += part[s * n4 + i];
-    out[i] = v;
+// Sums over the segments, in order, for both gradients: quads [0, na4) of the one, then nb4
+// of the other.
+__global__ __launch_bounds__(256) void adapter_sum_kernel(const floatx4* __restrict__ pa, const floatx4* __restrict__ pb,
+                                                          int segments, long na4, long nb4,
+                                                          floatx4* __restrict__ oa, floatx4* __restrict__ ob) {
+  for (long i = blockIdx.x * 256L + threadIdx.x; i < na4 + nb4; i += (long)gridDim.x * 256) {
+    const bool first = i < na4;
+    const long k = first ? i : i - na4, stride = first ? na4 : nb4;
+    const floatx4* part = (first ? pa : pb) + k;
+    floatx4 v = part[0];
+#pragma unroll 4
+    for (int s = 1; s < segments; ++s) v += part[s * stride];
+    (first ? oa : ob)[k] = v;
   }
 }
 
@@ -552,130 +695,151 @@ __global__ __launch_bounds__(256) void adapter_sum_kernel(const floatx4* __restr
     }                           \
   } while (0)
 
-static int blocks_of(int T) { return (T + kTok - 1) / kTok; }
+static int spans_of(int T) { return (T + kSpan - 1) / kSpan; }
 
-// Workgroups that share the groups of a block of tokens: as many as there can
-// be groups while the launch stays within some thousand workgroups.
-static int group_split(int T, int n, int others) {
-  int most = T < kTok ? T : kTok;
-  if (n + 1 < most) most = n + 1;
-  const int room = 4096 / (blocks_of(T) * others);
+// Workgroups that share the units of a span: as many as there can be units while the launch
+// stays within some thousand workgroups.
+static int span_share(int T, int n, int others) {
+  const int tokens = T < kSpan ? T : kSpan;
+  const int most = (tokens + kUnit - 1) / kUnit + (n < tokens ? n : tokens);
+  const int room = 8192 / (spans_of(T) * others);
   return room < 1 ? 1 : (room < most ? room : most);
 }
 
-// Columns of one expanding workgroup.
-static int expand_chunk(int T, int D) {
+// Columns of one expanding workgroup: 256 at least, one pass of its four waves.
+static int expand_chunk(int T, int n, int D) {
+  const long units = (T + kUnit - 1) / kUnit + (n < T ? n : T);
   int chunk = 2048;
-  while (chunk > 512 && (long)blocks_of(T) * ((D + chunk - 1) / chunk) < 512) chunk /= 2;
+  while (chunk > 256 && units * ((D + chunk - 1) / chunk) < 1024) chunk /= 2;
   return chunk;
-}
-
-static hipError_t reduce(bool trans, const void* in, const AdapterParams& p, int D, const void* W,
-                         float* part, hipStream_t s) {
-  const int parts = adapter_parts(D);
-  const dim3 grid(blocks_of(p.T), parts, group_split(p.T, p.n, parts));
-  const int span = adapter_span(D);
-  const uint16_t* x = static_cast<const uint16_t*>(in);
-  const uint16_t* w = static_cast<const uint16_t*>(W);
-  if (trans)
-    PMOE_BY_RANK(p.R, (adapter_reduce_kernel<NR, true><<<grid, 256, 0, s>>>(x, p.ids, p.ids64, p.T, p.n, D,
-                                                                            p.R, w, span, part)));
-  else
-    PMOE_BY_RANK(p.R, (adapter_reduce_kernel<NR, false><<<grid, 256, 0, s>>>(x, p.ids, p.ids64, p.T, p.n, D,
-                                                                             p.R, w, span, part)));
-  return hipGetLastError();
-}
-
-static hipError_t expand(bool trans, const float* part, int parts, const AdapterParams& p, int D,
-                         const void* W, const void* base, void* out, float* sums, int scale_sums,
-                         hipStream_t s) {
-  const int chunk = expand_chunk(p.T, D);
-  const int chunks = out ? (D + chunk - 1) / chunk : 1;
-  const dim3 grid(blocks_of(p.T), chunks, group_split(p.T, p.n, chunks));
-  const uint16_t* w = static_cast<const uint16_t*>(W);
-  const uint16_t* b = static_cast<const uint16_t*>(base);
-  uint16_t* o = static_cast<uint16_t*>(out);
-  if (trans)
-    PMOE_BY_RANK(p.R, (adapter_expand_kernel<NR, true><<<grid, 256, 0, s>>>(
-                          part, parts, p.ids, p.ids64, p.T, p.n, D, p.R, w, p.scale, b, o, sums, scale_sums, chunk)));
-  else
-    PMOE_BY_RANK(p.R, (adapter_expand_kernel<NR, false><<<grid, 256, 0, s>>>(
-                          part, parts, p.ids, p.ids64, p.T, p.n, D, p.R, w, p.scale, b, o, sums, scale_sums, chunk)));
-  return hipGetLastError();
-}
-
-// Segments of the tokens for the gradients of the matrices: more than the list
-// in LDS allows, and enough workgroups when there are few adapters.
-static int grad_segment(int T, int n, int H, int N) {
-  const long per_segment = (long)n * ((H + kGradCols - 1) / kGradCols + (N + kGradCols - 1) / kGradCols);
-  int seg = kSegMax;
-  while (seg > 512 && per_segment * ((T + seg - 1) / seg) < 512) seg /= 2;
-  return seg;
 }
 
 namespace {
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// The workspace: the orders of the spans, the parts of the reduction, and for the backward
+// call du and the segments' gradients.
+struct AdapterLayout {
+  SpanOrder* orders;
+  float *part, *du, *d_down, *d_up;
+  size_t bytes;
+};
 }  // namespace
 
-size_t adapter_forward_ws_bytes(int T, int H, int R) {
-  return up256((size_t)adapter_parts(H) * T * R * 4);
+static int grad_segment(int T, int n, int H, int N, int R);
+
+static AdapterLayout adapter_layout(void* ws, int T, int n, int H, int N, int R, bool backward) {
+  AdapterLayout l;
+  size_t o = 0;
+  const auto take = [&](size_t bytes) {
+    char* at = static_cast<char*>(ws) + o;
+    o += up256(bytes);
+    return at;
+  };
+  l.orders = reinterpret_cast<SpanOrder*>(take(sizeof(SpanOrder) * spans_of(T)));
+  l.part = reinterpret_cast<float*>(take((size_t)adapter_parts(backward ? N : H) * T * R * 4));
+  if (backward) {
+    const int seg = grad_segment(T, n, H, N, R), segments = (T + seg - 1) / seg;
+    const size_t each = segments > 1 ? (size_t)segments * n * R * 4 : 0;
+    l.du = reinterpret_cast<float*>(take((size_t)T * R * 4));
+    l.d_down = reinterpret_cast<float*>(take(each * H));
+    l.d_up = reinterpret_cast<float*>(take(each * N));
+  }
+  l.bytes = o;
+  return l;
+}
+
+static hipError_t reduce(bool trans, const void* in, const AdapterParams& p, int D, const void* W,
+                         const AdapterLayout& l, hipStream_t s) {
+  const int parts = adapter_parts(D), share = span_share(p.T, p.n, parts);
+  const dim3 grid(spans_of(p.T) * share, parts);
+  const int span = adapter_span(D);
+  const uint16_t* x = static_cast<const uint16_t*>(in);
+  const uint16_t* w = static_cast<const uint16_t*>(W);
+  if (trans)
+    PMOE_BY_RANK(p.R, (adapter_reduce_kernel<NR, true><<<grid, 256, 0, s>>>(
+                          x, p.ids, p.ids64, p.T, p.n, D, p.R, w, span, share, l.orders, l.part)));
+  else
+    PMOE_BY_RANK(p.R, (adapter_reduce_kernel<NR, false><<<grid, 256, 0, s>>>(
+                          x, p.ids, p.ids64, p.T, p.n, D, p.R, w, span, share, l.orders, l.part)));
+  return hipGetLastError();
+}
+
+static hipError_t expand(bool trans, int parts, const AdapterParams& p, int D, const void* W,
+                         const AdapterLayout& l, float* sums, int scale_sums, hipStream_t s) {
+  const int chunk = expand_chunk(p.T, p.n, D);
+  const int chunks = p.out ? (D + chunk - 1) / chunk : 1, share = span_share(p.T, p.n, chunks);
+  const dim3 grid(spans_of(p.T) * share, chunks);
+  const uint16_t* w = static_cast<const uint16_t*>(W);
+  const uint16_t* b = static_cast<const uint16_t*>(p.base);
+  uint16_t* o = static_cast<uint16_t*>(p.out);
+  if (trans)
+    PMOE_BY_RANK(p.R, (adapter_expand_kernel<NR, true><<<grid, 256, 0, s>>>(
+                          l.part, parts, l.orders, share, p.T, D, p.R, w, p.scale, b, o, sums, scale_sums, chunk)));
+  else
+    PMOE_BY_RANK(p.R, (adapter_expand_kernel<NR, false><<<grid, 256, 0, s>>>(
+                          l.part, parts, l.orders, share, p.T, D, p.R, w, p.scale, b, o, sums, scale_sums, chunk)));
+  return hipGetLastError();
+}
+
+// Segments of the tokens for the gradients of the matrices: several where few adapters make few
+// workgroups.
+static int grad_segment(int T, int n, int H, int N, int R) {
+  const int cols = grad_cols(R);
+  const long per_segment = (long)n * ((H + cols - 1) / cols + (N + cols - 1) / cols);
+  int seg = kSegMax;
+  while (seg > 512 && per_segment * ((T + seg - 1) / seg) < 384) seg /= 2;
+  return seg;
+}
+
+size_t adapter_forward_ws_bytes(int T, int n, int H, int N, int R) {
+  return adapter_layout(nullptr, T, n, H, N, R, false).bytes;
 }
 
 size_t adapter_backward_ws_bytes(int T, int n, int H, int N, int R) {
-  const int seg = grad_segment(T, n, H, N), segments = (T + seg - 1) / seg;
-  size_t b = up256((size_t)adapter_parts(N) * T * R * 4) + up256((size_t)T * R * 4);
-  if (segments > 1) b += up256((size_t)segments * n * R * H * 4) + up256((size_t)segments * n * R * N * 4);
-  return b;
+  return adapter_layout(nullptr, T, n, H, N, R, true).bytes;
 }
 
 hipError_t launch_adapter_forward(const AdapterParams& p, hipStream_t s) {
-  float* part = static_cast<float*>(p.ws);
-  const hipError_t e = reduce(false, p.x, p, p.H, p.down, part, s);
+  const AdapterLayout l = adapter_layout(p.ws, p.T, p.n, p.H, p.N, p.R, false);
+  const hipError_t e = reduce(false, p.x, p, p.H, p.down, l, s);
   if (e != hipSuccess) return e;
-  return expand(false, part, adapter_parts(p.H), p, p.N, p.up, p.base, p.out, p.v_out, 0, s);
+  return expand(false, adapter_parts(p.H), p, p.N, p.up, l, p.v_out, 0, s);
 }
 
 hipError_t launch_adapter_backward(const AdapterParams& p, hipStream_t s) {
-  char* at = static_cast<char*>(p.ws);
-  float* part = reinterpret_cast<float*>(at);
-  at += up256((size_t)adapter_parts(p.N) * p.T * p.R * 4);
-  float* du = reinterpret_cast<float*>(at);
-  at += up256((size_t)p.T * p.R * 4);
+  const AdapterLayout l = adapter_layout(p.ws, p.T, p.n, p.H, p.N, p.R, true);
   if (p.T > 0) {
-    hipError_t e = reduce(true, p.dy, p, p.N, p.up, part, s);
+    hipError_t e = reduce(true, p.dy, p, p.N, p.up, l, s);
     if (e != hipSuccess) return e;
-    e = expand(true, part, adapter_parts(p.N), p, p.H, p.down, p.base, p.out, du, 1, s);
+    e = expand(true, adapter_parts(p.N), p, p.H, p.down, l, l.du, 1, s);
     if (e != hipSuccess) return e;
   }
   if (!p.d_down) return hipSuccess;
-  const int seg = grad_segment(p.T, p.n, p.H, p.N);
+  const int seg = grad_segment(p.T, p.n, p.H, p.N, p.R);
   const int segments = p.T > 0 ? (p.T + seg - 1) / seg : 1;
-  const size_t na = (size_t)p.n * p.R * p.H, nb = (size_t)p.n * p.R * p.N;
   GradParams q;
   q.x = static_cast<const uint16_t*>(p.x);
   q.dy = static_cast<const uint16_t*>(p.dy);
-  q.du = du;
+  q.du = l.du;
   q.v = p.v_in;
   q.scale = p.scale;
   q.ids = p.ids;
   q.ids64 = p.ids64;
   q.T = p.T, q.n = p.n, q.H = p.H, q.N = p.N, q.R = p.R, q.seg = seg;
-  q.d_down = segments > 1 ? reinterpret_cast<float*>(at) : p.d_down;
-  q.d_up = segments > 1 ? reinterpret_cast<float*>(at + up256(segments * na * 4)) : p.d_up;
-  const int chunks = (p.H + kGradCols - 1) / kGradCols + (p.N + kGradCols - 1) / kGradCols;
+  q.d_down = segments > 1 ? l.d_down : p.d_down;
+  q.d_up = segments > 1 ? l.d_up : p.d_up;
+  const int cols = grad_cols(p.R), chunks = (p.H + cols - 1) / cols + (p.N + cols - 1) / cols;
   const dim3 grid(chunks * (p.R > 64 ? 2 : 1), p.n, segments);
-  PMOE_BY_RANK(p.R, (adapter_grad_kernel<(NR < 4 ? NR : 4)><<<grid, 256, 0, s>>>(q)));
-  hipError_t e = hipGetLastError();
+  PMOE_BY_RANK(p.R, (adapter_grad_kernel<(NR < 4 ? NR : 4), (NR < 4 ? 8 : 4)><<<grid, 256, 0, s>>>(q)));
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || segments == 1) return e;
-  const auto add = [&](const float* from, size_t count, float* to) {
-    const long n4 = (long)(count / 4);
-    const long blocks = (n4 + 255) / 256;
-    adapter_sum_kernel<<<(int)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(
-        reinterpret_cast<const floatx4*>(from), segments, n4, reinterpret_cast<floatx4*>(to));
-    return hipGetLastError();
-  };
-  e = add(q.d_down, na, p.d_down);
-  return e != hipSuccess ? e : add(q.d_up, nb, p.d_up);
+  const long na4 = (long)p.n * p.R * p.H / 4, nb4 = (long)p.n * p.R * p.N / 4;
+  const long blocks = (na4 + nb4 + 255) / 256;
+  adapter_sum_kernel<<<(int)(blocks < 8192 ? blocks : 8192), 256, 0, s>>>(
+      reinterpret_cast<const floatx4*>(l.d_down), reinterpret_cast<const floatx4*>(l.d_up), segments, na4, nb4,
+      reinterpret_cast<floatx4*>(p.d_down), reinterpret_cast<floatx4*>(p.d_up));
+  return hipGetLastError();
 }
 
 }  // namespace pmoe

@@ -976,7 +976,7 @@ PMOE_EXPORT size_t pmoe_adapter_workspace_bytes(int T, int n, int H, int N, int 
   }
   ok();
   return std::max<size_t>(kAlign, backward ? adapter_backward_ws_bytes(T, n, H, N, R)
-                                           : adapter_forward_ws_bytes(T, H, R));
+                                           : adapter_forward_ws_bytes(T, n, H, N, R));
 }
 
 PMOE_EXPORT int pmoe_adapter_forward(const void* x, const void* adapter_ids, int ids_type, int T, int n,
@@ -997,7 +997,7 @@ PMOE_EXPORT int pmoe_adapter_forward(const void* x, const void* adapter_ids, int
   PMOE_TRY(check_ptr_here(out, 16, "out"));
   if (v) PMOE_TRY(check_ptr_here(v, 16, "v"));
   PMOE_TRY(check_ptr_here(ws, 256, "ws"));
-  const size_t need = adapter_forward_ws_bytes(T, H, R);
+  const size_t need = adapter_forward_ws_bytes(T, n, H, N, R);
   if (ws_bytes < need)
     return fail(PMOE_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
   const size_t out_bytes = (size_t)T * N * 2;

@@ -169,7 +169,7 @@ struct AdapterParams {
   float* d_up;         // backward: [n][N][R] or null, with d_down
   void* ws;
 };
-size_t adapter_forward_ws_bytes(int T, int H, int R);
+size_t adapter_forward_ws_bytes(int T, int n, int H, int N, int R);
 size_t adapter_backward_ws_bytes(int T, int n, int H, int N, int R);
 hipError_t launch_adapter_forward(const AdapterParams& p, hipStream_t s);
 hipError_t launch_adapter_backward(const AdapterParams& p, hipStream_t s);
