@@ -35,12 +35,25 @@ typedef float floatx4 __attribute__((ext_vector_type(4)));
 
 constexpr int kUnit = 64;    // tokens of one unit at most
 constexpr int kSpan = 1024;  // tokens that are grouped together
-constexpr int kNone = 0xFFFF;  // "adapter" of tokens without one (adapters are below 65535)
+constexpr int kNone = -1;  // adapter of a unit of tokens without one
 constexpr int kMostRuns = 16;  // boundaries up to which a span is not sorted
 
 __device__ __forceinline__ floatx4 mfma16(bf16x8_t a, bf16x8_t b, floatx4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
+
+// Loads and stores at a 32-bit byte offset from a pointer that is the same in all lanes: the
+// pointer stays in scalar registers. Offsets within a span of tokens or within one adapter's
+// matrix, and within a segment of 4096 tokens, are at most 2^27.
+template <typename V>
+__device__ __forceinline__ V load_at(const void* base, uint32_t offset) {
+  return *reinterpret_cast<const V*>(static_cast<const char*>(base) + offset);
+}
+template <typename V>
+__device__ __forceinline__ void store_at(void* base, uint32_t offset, V v) {
+  *reinterpret_cast<V*>(static_cast<char*>(base) + offset) = v;
+}
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 __device__ __forceinline__ bf16x8_t as_bf16x8(uint4 u) { return __builtin_bit_cast(bf16x8_t, u); }
 
@@ -49,129 +62,177 @@ __device__ __forceinline__ int adapter_of(const void* ids, int ids64, long t, in
   return id >= 0 && id < n ? (int)id : -1;
 }
 
+constexpr int kReduceWaves = 8;
+constexpr int kReduceThreads = 64 * kReduceWaves;
+
 // Order and units of a span: unit u holds the places [start[u], start[u + 1]) of
-// the order; key = adapter << 10 | token of the span.
+// the order; key = adapter << 10 | token of the span, adapter n for none.
+constexpr int kChunks = kSpan / 64;
 struct SpanLds {
   uint32_t key[kSpan];
   uint16_t start[kSpan + 8];
-  int wave[2][4];
+  int table[16][kChunks];  // sort: keys of a digit in a chunk of 64, then the places before them
+  int wave[2][kReduceWaves];
 };
-// The same in the workspace, one for each span.
+// The same in the workspace, one for each span: the order, and the units as
+// {first place | tokens << 16, adapter}.
 struct SpanOrder {
   uint32_t key[kSpan];
-  uint16_t start[kSpan];
-  int units, count;
-  int pad[2];
+  uint2 unit[kSpan];
+  int units;
+  int pad[3];
 };
 
-__device__ __forceinline__ int wave_inclusive_sum(int v, int lane) {
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int y = __shfl_up(v, off, 64);
-    if (lane >= off) v += y;
-  }
+// Inclusive sum and maximum over the lanes by data-parallel-primitive moves: 1, 2, 4 and 8
+// lanes up within rows of 16, then the last lane of a row into the rows above.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ int lane_move(int old, int v) {
+  return __builtin_amdgcn_update_dpp(old, v, kCtrl, kRows, 0xf, false);
+}
+__device__ __forceinline__ int wave_inclusive_sum(int v) {
+  v += lane_move<0x111, 0xf>(0, v);
+  v += lane_move<0x112, 0xf>(0, v);
+  v += lane_move<0x114, 0xf>(0, v);
+  v += lane_move<0x118, 0xf>(0, v);
+  v += lane_move<0x142, 0xa>(0, v);
+  v += lane_move<0x143, 0xc>(0, v);
+  return v;
+}
+__device__ __forceinline__ int wave_inclusive_max(int v) {
+  v = max(v, lane_move<0x111, 0xf>(v, v));
+  v = max(v, lane_move<0x112, 0xf>(v, v));
+  v = max(v, lane_move<0x114, 0xf>(v, v));
+  v = max(v, lane_move<0x118, 0xf>(v, v));
+  v = max(v, lane_move<0x142, 0xa>(v, v));
+  v = max(v, lane_move<0x143, 0xc>(v, v));
   return v;
 }
 
-// Groups the tokens [t0, t0 + count) with a workgroup of 256 threads; returns
+// Groups the tokens [t0, t0 + count) with a workgroup of kReduceThreads; returns
 // the number of units. Ends with a barrier.
 __device__ __forceinline__ int group_span(const void* ids, int ids64, long t0, int count, int n, SpanLds& l) {
+  constexpr int kPer = kSpan / kReduceThreads;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  uint32_t key[kPer];
 #pragma unroll
-  for (int j = 0; j < kSpan / 256; ++j) {
-    const int i = tid + 256 * j;
-    uint32_t k = 0xFFFFFFFFu;
+  for (int j = 0; j < kPer; ++j) {
+    const int i = tid + kReduceThreads * j;
+    key[j] = 0xFFFFFFFFu;
     if (i < count) {
       const int a = adapter_of(ids, ids64, t0 + i, n);
-      k = (uint32_t)(a < 0 ? kNone : a) << 10 | (uint32_t)i;
+      key[j] = (uint32_t)(a < 0 ? n : a) << 10 | (uint32_t)i;
     }
-    l.key[i] = k;
+    l.key[i] = key[j];
   }
   __syncthreads();
   int edges = 0;
 #pragma unroll
-  for (int j = 0; j < kSpan / 256; ++j) {
-    const int i = tid + 256 * j;
-    edges += __popcll(__ballot(i > 0 && i < count && l.key[i] >> 10 != l.key[max(i, 1) - 1] >> 10));
+  for (int j = 0; j < kPer; ++j) {
+    const int i = tid + kReduceThreads * j;
+    edges += __popcll(__ballot(i > 0 && i < count && key[j] >> 10 != l.key[max(i, 1) - 1] >> 10));
   }
   if (lane == 0) l.wave[0][wave] = edges;
   __syncthreads();
-  if (l.wave[0][0] + l.wave[0][1] + l.wave[0][2] + l.wave[0][3] > kMostRuns) {
-    int size = 64;
-    while (size < count) size *= 2;
-    for (int k = 2; k <= size; k *= 2)
-      for (int d = k / 2; d > 0; d /= 2) {
-        for (int i = tid; i < size / 2; i += 256) {
-          const int x = (i & ~(d - 1)) * 2 + (i & (d - 1)), y = x + d;
-          const uint32_t p = l.key[x], q = l.key[y];
-          if ((p > q) == ((x & k) == 0)) {
-            l.key[x] = q;
-            l.key[y] = p;
-          }
+  edges = 0;
+  for (int w = 0; w < kReduceWaves; ++w) edges += l.wave[0][w];
+  if (edges > kMostRuns) {
+    // Stable sort by adapter, four bits at a time from the lowest: a key's place is the number of
+    // keys with a smaller digit, plus those with its digit in the chunks before its own, plus
+    // those among the lanes below (found by ballots on the digit's bits).
+    const uint64_t below = lane == 0 ? 0ull : (~0ull >> (64 - lane));
+    for (int shift = 10; n >> (shift - 10) != 0; shift += 4) {
+      for (int i = tid; i < 16 * kChunks; i += kReduceThreads) (&l.table[0][0])[i] = 0;
+      __syncthreads();
+      int digit[kPer], rank[kPer];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const bool on = tid + kReduceThreads * j < count;
+        digit[j] = key[j] >> shift & 15;
+        uint64_t match = __ballot(on);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint64_t set = __ballot(digit[j] >> b & 1);
+          match &= digit[j] >> b & 1 ? set : ~set;
         }
-        __syncthreads();
+        rank[j] = __popcll(match & below);
+        if (on && rank[j] == 0) l.table[digit[j]][wave + kReduceWaves * j] = __popcll(match);
       }
-  }
-  // Units. Thread t looks at the places 4 t .. 4 t + 3.
-  const uint4 mine = *reinterpret_cast<const uint4*>(&l.key[4 * tid]);
-  const uint32_t k[5] = {tid > 0 ? l.key[4 * tid - 1] : 0xFFFFFFFFu, mine.x, mine.y, mine.z, mine.w};
-  int first[4], last = -1;  // the start of the group that a place belongs to, -1: further back
+      __syncthreads();
+      const int mine = tid < 16 * kChunks ? (&l.table[0][0])[tid] : 0;
+      const int upto = wave_inclusive_sum(mine);
+      if (lane == 63) l.wave[1][wave] = upto;
+      __syncthreads();
+      int before = upto - mine;
+      for (int w = 0; w < wave; ++w) before += l.wave[1][w];
+      if (tid < 16 * kChunks) (&l.table[0][0])[tid] = before;
+      __syncthreads();
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if ((tid == 0 && j == 0) || k[j + 1] >> 10 != k[j] >> 10) last = 4 * tid + j;
+      for (int j = 0; j < kPer; ++j)
+        if (tid + kReduceThreads * j < count)
+          l.key[l.table[digit[j]][wave + kReduceWaves * j] + rank[j]] = key[j];
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) key[j] = l.key[tid + kReduceThreads * j];
+    }
+  }
+  // Units. Thread t looks at the places kPer t .. kPer t + kPer - 1.
+  uint32_t before_key = tid > 0 ? l.key[kPer * tid - 1] : 0;
+  int first[kPer], last = -1;  // the start of the group that a place belongs to, -1: further back
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const uint32_t k = l.key[kPer * tid + j];
+    if ((tid == 0 && j == 0) || k >> 10 != before_key >> 10) last = kPer * tid + j;
     first[j] = last;
+    before_key = k;
   }
-  int back = last;  // inclusive maximum over the threads
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) back = max(back, __shfl_up(back, off, 64));
-  if (lane == 63) l.wave[0][wave] = back;
-  back = __shfl_up(back, 1, 64);  // exclusive; lane 0 has none within the wave
+  const int upto = wave_inclusive_max(last);
+  __syncthreads();  // every wave has read the edges
+  if (lane == 63) l.wave[0][wave] = upto;
+  int back = __shfl_up(upto, 1, 64);  // exclusive; lane 0 has none within the wave
   if (lane == 0) back = -1;
   __syncthreads();
   for (int w = 0; w < wave; ++w) back = max(back, l.wave[0][w]);
   int starts = 0;
-  bool is[4];
+  bool is[kPer];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int at = 4 * tid + j, from = first[j] >= 0 ? first[j] : back;
+  for (int j = 0; j < kPer; ++j) {
+    const int at = kPer * tid + j, from = first[j] >= 0 ? first[j] : back;
     is[j] = at < count && ((at - from) & (kUnit - 1)) == 0;
     starts += is[j];
   }
-  int before = wave_inclusive_sum(starts, lane);
-  if (lane == 63) l.wave[1][wave] = before;
-  before -= starts;
+  int place = wave_inclusive_sum(starts);
+  if (lane == 63) l.wave[1][wave] = place;
+  place -= starts;
   __syncthreads();
   int units = 0;
-  for (int w = 0; w < 4; ++w) {
-    if (w < wave) before += l.wave[1][w];
+  for (int w = 0; w < kReduceWaves; ++w) {
+    if (w < wave) place += l.wave[1][w];
     units += l.wave[1][w];
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (is[j]) l.start[before++] = (uint16_t)(4 * tid + j);
+  for (int j = 0; j < kPer; ++j)
+    if (is[j]) l.start[place++] = (uint16_t)(kPer * tid + j);
   if (tid == 0) l.start[units] = (uint16_t)count;
   __syncthreads();
   return units;
 }
 
-__device__ __forceinline__ void keep_order(const SpanLds& l, int units, int count, SpanOrder* o) {
-  for (int i = threadIdx.x; i < count; i += 256) o->key[i] = l.key[i];
-  for (int i = threadIdx.x; i < units; i += 256) o->start[i] = l.start[i];
-  if (threadIdx.x == 0) {
-    o->units = units;
-    o->count = count;
+__device__ __forceinline__ void keep_order(const SpanLds& l, int units, int count, int n, SpanOrder* o) {
+  for (int i = threadIdx.x; i < count; i += kReduceThreads) o->key[i] = l.key[i];
+  for (int i = threadIdx.x; i < units; i += kReduceThreads) {
+    const uint32_t at = l.start[i], len = l.start[i + 1] - at;
+    const int a = l.key[at] >> 10;
+    o->unit[i] = make_uint2(at | len << 16, a == n ? kNone : a);
   }
+  if (threadIdx.x == 0) o->units = units;
 }
 
 // ---------------------------------------------------------------- reduction over H (or N)
-// Parts of the sum over a row of D elements: gridDim.y workgroups of four waves
-// each take a span of `span` elements (a multiple of 64) per wave. Chosen from
-// D alone.
-int adapter_parts(int D) {
-  const int p = (D + 1023) / 1024;
-  return p < 8 ? p : 8;
-}
-static int adapter_span(int D) { return ((D + adapter_parts(D) * 4 - 1) / (adapter_parts(D) * 4) + 63) / 64 * 64; }
+// A sum over a row of D elements is cut into parts of adapter_part_length(D) elements (a
+// multiple of 64, at most 4096), one workgroup of eight waves each, whose waves take pieces of
+// 64 or 128 elements in turn: together they read a row in long stretches.
+int adapter_parts(int D) { return (D + 4095) / 4096; }
+static int adapter_part_length(int D) { return ((D + adapter_parts(D) - 1) / adapter_parts(D) + 63) / 64 * 64; }
 
 // Eight rows of kCols columns each, turned: op[b] gets the eight values of
 // column b, ready as an MFMA operand. kCols is 1, 2, 4 or 8.
@@ -179,19 +240,19 @@ template <int kCols>
 struct Rows8 {
   static constexpr int kWords = kCols < 2 ? 1 : kCols / 2;
   uint32_t w[8][kWords];
-  __device__ __forceinline__ void load(int j, const uint16_t* p, bool on) {
+  __device__ __forceinline__ void load(int j, const void* base, uint32_t offset, bool on) {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[j][i] = 0;
     if (!on) return;
     if constexpr (kCols == 1) {
-      w[j][0] = *p;
+      w[j][0] = load_at<uint16_t>(base, offset);
     } else if constexpr (kCols == 2) {
-      w[j][0] = *reinterpret_cast<const uint32_t*>(p);
+      w[j][0] = load_at<uint32_t>(base, offset);
     } else if constexpr (kCols == 4) {
-      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      const uint2 u = load_at<uint2>(base, offset);
       w[j][0] = u.x, w[j][1] = u.y;
     } else {
-      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      const uint4 u = load_at<uint4>(base, offset);
       w[j][0] = u.x, w[j][1] = u.y, w[j][2] = u.z, w[j][3] = u.w;
     }
   }
@@ -204,54 +265,58 @@ struct Rows8 {
   }
 };
 
-// part[y][t][r] = sum over the y-th part of in[t][k] * W_a[r][k] (kTrans: W_a[k][r]).
-// blockIdx.x is a span and one of `share` workgroups that take its units in turn.
+// part[y][place][r] = sum over the y-th part of in[t][k] * W_a[r][k] (kTrans: W_a[k][r]),
+// t the token at the place of the order. blockIdx.y is a span and one of `share`
+// workgroups that take its half units (32 tokens) in turn.
 // Operand row i of block b is r = NR i + b, so that a lane ends with 4 NR consecutive r of
 // one token, and with kTrans a lane reads NR neighbouring columns of eight rows.
 template <int NR, bool kTrans>
-__global__ __launch_bounds__(256) void adapter_reduce_kernel(
+__global__ __launch_bounds__(kReduceThreads) void adapter_reduce_kernel(
     const uint16_t* __restrict__ in, const void* __restrict__ ids, int ids64, int T, int n, int D, int R,
-    const uint16_t* __restrict__ W, int span, int share, SpanOrder* __restrict__ orders,
+    const uint16_t* __restrict__ W, int length, int share, SpanOrder* __restrict__ orders,
     float* __restrict__ part) {
-  constexpr int kSteps = NR <= 4 ? 2 : 1;  // steps of 64 that are loaded together
+  constexpr int kSteps = NR <= 2 ? 2 : 1;  // steps of 64 that are loaded together
   __shared__ __align__(16) SpanLds lds;
-  __shared__ floatx4 red[4][NR][64];
+  __shared__ floatx4 red[kReduceWaves][NR][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = lane & 15, g = lane >> 4;
-  const int sp = blockIdx.x / share, mine = blockIdx.x % share;
+  const int sp = blockIdx.y / share, mine = blockIdx.y % share;
   const long t0 = (long)sp * kSpan;
   const int count = (int)min((long)kSpan, T - t0);
   const int units = group_span(ids, ids64, t0, count, n, lds);
-  if (mine == 0 && blockIdx.y == 0) keep_order(lds, units, count, orders + sp);
-  const int k_begin = (blockIdx.y * 4 + wave) * span, k_end = min(D, k_begin + span);
-  float* dst = part + (long)blockIdx.y * T * R;
-  for (int u = mine; u < units; u += share) {
-    const int at = lds.start[u], len = lds.start[u + 1] - at;
-    const int adapter = lds.key[at] >> 10;
-    if (adapter == kNone) continue;
+  if (mine == 0 && blockIdx.x == 0) keep_order(lds, units, count, n, orders + sp);
+  const int k_begin = blockIdx.x * length + wave * 64 * kSteps, k_end = min(D, (int)(blockIdx.x + 1) * length);
+  float* dst = part + ((long)blockIdx.x * T + t0) * R;
+  const uint16_t* rows_in = in + t0 * D;
+  for (int item = mine; item < 2 * units; item += share) {  // the first halves, then the second
+    const int u = item < units ? item : item - units;
+    const int start = uniform(lds.start[u]), end = uniform(lds.start[u + 1]);
+    const int at = item < units ? start : start + 32, len = min(32, end - at);
+    const int adapter = uniform(lds.key[start] >> 10);
+    if (len <= 0 || adapter == n) continue;
     const int nf = (len + 15) >> 4;
-    const uint16_t* x[4];
+    uint32_t x[2];  // where the rows begin
 #pragma unroll
-    for (int f = 0; f < 4; ++f)
-      x[f] = in + (t0 + (lds.key[at + min(16 * f + col, len - 1)] & (kSpan - 1))) * D;
+    for (int f = 0; f < 2; ++f)
+      x[f] = (lds.key[at + min(16 * f + col, len - 1)] & (kSpan - 1)) * (uint32_t)D * 2u;
     const uint16_t* w = W + (long)adapter * R * D;
-    floatx4 acc[4][NR];
+    floatx4 acc[2][NR];
 #pragma unroll
-    for (int f = 0; f < 4; ++f)
+    for (int f = 0; f < 2; ++f)
 #pragma unroll
       for (int c = 0; c < NR; ++c) acc[f][c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     const int r0 = NR * col;
-    for (int k0 = k_begin; k0 < k_end; k0 += 64 * kSteps) {
-      uint4 xv[kSteps][4][2];
+    for (int k0 = k_begin; k0 < k_end; k0 += 64 * kSteps * kReduceWaves) {
+      uint4 xv[kSteps][2][2];
 #pragma unroll
       for (int q = 0; q < kSteps; ++q) {
-        const int k = k0 + 64 * q + 16 * g;  // D is a multiple of 16: 16 elements are in or out together
+        const int k = k0 + 64 * q + 8 * g;  // the lane's elements: k .. k + 7 and k + 32 .. k + 39
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
+        for (int f = 0; f < 2; ++f) {
           xv[q][f][0] = xv[q][f][1] = make_uint4(0, 0, 0, 0);
-          if (f < nf && k < k_end && 16 * f + col < len) {
-            xv[q][f][0] = *reinterpret_cast<const uint4*>(x[f] + k);
-            xv[q][f][1] = *reinterpret_cast<const uint4*>(x[f] + k + 8);
+          if (f < nf && 16 * f + col < len) {
+            if (k < k_end) xv[q][f][0] = load_at<uint4>(rows_in, x[f] + 2u * k);
+            if (k + 32 < k_end) xv[q][f][1] = load_at<uint4>(rows_in, x[f] + 2u * k + 64u);
           }
         }
       }
@@ -260,10 +325,12 @@ __global__ __launch_bounds__(256) void adapter_reduce_kernel(
         Rows8<NR> rows[kSteps][2];
 #pragma unroll
         for (int q = 0; q < kSteps; ++q) {
-          const int k = k0 + 64 * q + 16 * g;
+          const int k = k0 + 64 * q + 8 * g;
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            rows[q][j >> 3].load(j & 7, w + (long)(k + j) * R + r0, k < k_end && r0 < R);
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              rows[q][h].load(j, w + (32 * h + j) * R, ((uint32_t)k * R + r0) * 2u, k + 32 * h < k_end && r0 < R);
         }
 #pragma unroll
         for (int q = 0; q < kSteps; ++q)
@@ -275,13 +342,14 @@ __global__ __launch_bounds__(256) void adapter_reduce_kernel(
       } else {
 #pragma unroll
         for (int q = 0; q < kSteps; ++q) {
-          const int k = k0 + 64 * q + 16 * g;
+          const int k = k0 + 64 * q + 8 * g;
 #pragma unroll
           for (int c = 0; c < NR; ++c) {
             uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-            if (k < k_end && r0 + c < R) {
-              lo = *reinterpret_cast<const uint4*>(w + (long)(r0 + c) * D + k);
-              hi = *reinterpret_cast<const uint4*>(w + (long)(r0 + c) * D + k + 8);
+            if (r0 + c < R) {
+              const uint32_t o = ((uint32_t)(r0 + c) * D + k) * 2u;
+              if (k < k_end) lo = load_at<uint4>(w, o);
+              if (k + 32 < k_end) hi = load_at<uint4>(w, o + 64u);
             }
             wv[q][c][0] = as_bf16x8(lo);
             wv[q][c][1] = as_bf16x8(hi);
@@ -291,7 +359,7 @@ __global__ __launch_bounds__(256) void adapter_reduce_kernel(
 #pragma unroll
       for (int q = 0; q < kSteps; ++q)
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
+        for (int f = 0; f < 2; ++f) {
           if (f >= nf) continue;
 #pragma unroll
           for (int c = 0; c < NR; ++c) {
@@ -300,24 +368,26 @@ __global__ __launch_bounds__(256) void adapter_reduce_kernel(
           }
         }
     }
-    // the four waves' sums, in wave order; value (c, lane, i) is r = 4 NR g + NR i + c
+    // the waves' sums, in wave order; value (c, lane, i) is r = 4 NR g + NR i + c
 #pragma unroll
-    for (int f = 0; f < 4; ++f) {
+    for (int f = 0; f < 2; ++f) {
       if (f >= nf) continue;
 #pragma unroll
       for (int c = 0; c < NR; ++c) red[wave][c][lane] = acc[f][c];
       __syncthreads();
       const int m = 16 * f + col;
-      const long t = t0 + (lds.key[at + min(m, len - 1)] & (kSpan - 1));
-      for (int q = wave; q < NR; q += 4) {
+      for (int q = wave; q < NR; q += kReduceWaves) {
         floatx4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = (4 * q + e) / NR, c = (4 * q + e) % NR;
-          v[e] = ((red[0][c][lane][i] + red[1][c][lane][i]) + red[2][c][lane][i]) + red[3][c][lane][i];
+          float sum = red[0][c][lane][i];
+#pragma unroll
+          for (int y = 1; y < kReduceWaves; ++y) sum += red[y][c][lane][i];
+          v[e] = sum;
         }
         const int r = 4 * NR * g + 4 * q;
-        if (m < len && r < R) *reinterpret_cast<floatx4*>(dst + t * R + r) = v;
+        if (m < len && r < R) store_at<floatx4>(dst, (uint32_t)((at + m) * R + r) * 4u, v);
       }
       __syncthreads();
     }
@@ -346,77 +416,126 @@ struct LowRows {
   uint16_t v[kUnit][kStride];
 };
 
-// Adds base to 16 consecutive FP32 columns of a token and stores them in BF16.
-// c[j] is column j.
-__device__ __forceinline__ void store16(uint16_t* out, const float (&c)[16], const uint4 (&base)[2]) {
+// Adds base to 16 FP32 columns of a token, c[0 .. 7] at `offset` and c[8 .. 15] 32 columns
+// further, and stores them in BF16. Four lanes then write 64 bytes at a stretch.
+__device__ __forceinline__ void store16(uint16_t* out, uint32_t offset, bool first, bool second,
+                                        const float (&c)[16], const uint4 (&base)[2]) {
   uint32_t o[8];
   const uint32_t b[8] = {base[0].x, base[0].y, base[0].z, base[0].w, base[1].x, base[1].y, base[1].z, base[1].w};
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     o[j] = f32x2_to_bf16x2(bf16_to_f32(b[j] & 0xFFFFu) + c[2 * j], bf16_to_f32(b[j] >> 16) + c[2 * j + 1]);
-  *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
-  *reinterpret_cast<uint4*>(out + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+  if (first) store_at<uint4>(out, offset, make_uint4(o[0], o[1], o[2], o[3]));
+  if (second) store_at<uint4>(out, offset + 64u, make_uint4(o[4], o[5], o[6], o[7]));
 }
 
 // out[t][c] = bf16(base[t][c] + sum_r low[t][r] W_a[c][r]) (kTrans: W_a[r][c]),
-// low = scale * (sum of the parts). Workgroups with blockIdx.y == 0 also write the sum
-// of the parts to `sums` (times the scale if scale_sums), 0 without an adapter.
-// A wave takes 64 columns at a time. Operand row i of block b is column
-// 16 (i / 4) + 4 b + i % 4, with kTrans column 4 i + b; either way a lane's four blocks end
-// as 16 consecutive columns of one token, and four lanes write a line of 128 bytes. With
-// kTrans W_a has its columns contiguous while an operand wants eight r of one column: a
-// lane reads four columns of eight rows and turns them in registers.
+// low = scale * (sum of the parts). blockIdx.x is a block of 256 columns, 64 for each wave,
+// so that neighbouring workgroups write neighbouring pieces of the same tokens; blockIdx.y
+// is a span and one of `share` workgroups that take its units in turn. Workgroups with
+// blockIdx.x == 0 also write the sum of the parts to `sums` (times the scale if scale_sums),
+// 0 without an adapter.
+// Operand row i of block b is column 32 (b / 2) + 8 (i / 4) + 4 (b % 2) + i % 4, with kTrans
+// 32 (i / 2 % 2) + 8 (i / 4) + 4 (i % 2) + b; either way a lane's four blocks end as the
+// columns 8 g .. 8 g + 7 and 32 further of one token, so that four lanes read and write 64
+// bytes at a stretch. With kTrans W_a has its columns contiguous while an operand wants eight
+// r of one column: a lane reads four columns of eight rows and turns them in registers.
 template <int NR, bool kTrans>
 __global__ __launch_bounds__(256) void adapter_expand_kernel(
     const float* __restrict__ part, int parts, const SpanOrder* __restrict__ orders, int share, int T,
     int D, int R, const uint16_t* __restrict__ W, const float* __restrict__ scale,
-    const uint16_t* base, uint16_t* out, float* __restrict__ sums, int scale_sums, int chunk) {
+    const uint16_t* base, uint16_t* out, float* __restrict__ sums, int scale_sums) {
   using Low = LowRows<NR>;
   __shared__ __align__(16) Low low;
   __shared__ int place[kUnit];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int col = lane & 15, g = lane >> 4;
-  const int sp = blockIdx.x / share;
+  const int sp = blockIdx.y / share;
   const SpanOrder* order = orders + sp;
   const int units = order->units;
   const long t0 = (long)sp * kSpan;
-  const int c_begin = blockIdx.y * chunk, c_end = min(D, c_begin + chunk);
+  const int c0 = blockIdx.x * 256 + 64 * wave;
+  const int c = c0 + 8 * g;  // the lane's columns of the result: c .. c + 7 and c + 32 .. c + 39
   // tokens without an adapter: base, or zeros
   const bool fill = out != nullptr && base != out;
-  for (int u = blockIdx.x % share; u < units; u += share) {
-    const int at = order->start[u], len = (u + 1 < units ? order->start[u + 1] : order->count) - at;
-    const int adapter = order->key[at] >> 10;
+  if (base) base += t0 * D;
+  if (out) out += t0 * D;
+  const bool keep_sums = sums != nullptr && blockIdx.x == 0;
+  if (sums) sums += t0 * R;
+  part += t0 * R;
+  for (int u = blockIdx.y % share; u < units; u += share) {
+    const uint2 unit = order->unit[u];
+    const int at = uniform(unit.x & 0xFFFFu), len = uniform(unit.x >> 16), adapter = uniform(unit.y);
     __syncthreads();  // the unit before is no longer read
     if (tid < kUnit) place[tid] = order->key[at + min(tid, len - 1)] & (kSpan - 1);
-    __syncthreads();
     if (adapter == kNone) {
+      __syncthreads();
       if (fill)
-        for (int m = wave; m < len; m += 4) {
-          const long row = (t0 + place[m]) * D;
-          for (int c = c_begin + lane * 8; c < c_end; c += 512)
-            *reinterpret_cast<uint4*>(out + row + c) =
-                base ? *reinterpret_cast<const uint4*>(base + row + c) : make_uint4(0, 0, 0, 0);
+        for (int m = tid >> 5; m < len; m += 8) {
+          const int cn = blockIdx.x * 256 + (tid & 31) * 8;
+          const uint32_t o = (place[m] * (uint32_t)D + cn) * 2u;
+          if (cn < D) store_at<uint4>(out, o, base ? load_at<uint4>(base, o) : make_uint4(0, 0, 0, 0));
         }
-      if (blockIdx.y == 0 && sums != nullptr)
-        for (int i = tid; i < len * R; i += 256) sums[(t0 + place[i / R]) * R + i % R] = 0.0f;
+      if (keep_sums)
+        for (int i = tid; i < len * R; i += 256) sums[place[i / R] * R + i % R] = 0.0f;
       continue;
     }
     const int nf = (len + 15) >> 4;
     const float s = scale[adapter];
+    const uint16_t* w = W + (long)adapter * R * D;
+    bf16x8_t wop[Low::kSteps][4];
+    if constexpr (kTrans) {
+      Rows8<4> rows[Low::kSteps];
+      const int cc = c0 + 8 * (col >> 2) + 4 * (col & 1) + 16 * (col & 2);
+#pragma unroll
+      for (int q = 0; q < Low::kSteps; ++q) {
+        const int rg = NR == 1 ? 8 * (g & 1) : 8 * g;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          rows[q].load(j, w + (long)(32 * q + j) * D, ((uint32_t)rg * D + cc) * 2u, cc < D && 32 * q + rg < R);
+      }
+#pragma unroll
+      for (int q = 0; q < Low::kSteps; ++q)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) wop[q][b] = rows[q].column(b);
+    } else {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int cc = c0 + 32 * (b >> 1) + 8 * (col >> 2) + 4 * (b & 1) + (col & 3);
+#pragma unroll
+        for (int q = 0; q < Low::kSteps; ++q) {
+          const int r = NR == 1 ? 8 * (g & 1) : 32 * q + 8 * g;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (cc < D && r < R) v = load_at<uint4>(w, ((uint32_t)cc * R + r) * 2u);
+          wop[q][b] = as_bf16x8(v);
+        }
+      }
+    }
+    __syncthreads();  // place
+    uint4 bv[4][2];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      bv[f][0] = bv[f][1] = make_uint4(0, 0, 0, 0);
+      if (f < nf && base && 16 * f + col < len) {
+        const uint32_t b = (place[16 * f + col] * (uint32_t)D + c) * 2u;
+        if (c < D) bv[f][0] = load_at<uint4>(base, b);
+        if (c + 32 < D) bv[f][1] = load_at<uint4>(base, b + 64u);
+      }
+    }
+#pragma unroll 1
     for (int i = tid; i < nf * 16 * (4 * NR); i += 256) {
       const int m = i / (4 * NR), r = i % (4 * NR) * 4;
-      const long t = t0 + place[m];
       floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
       if (m < len && r < R) {
-        floatx4 q[8];
+        const uint32_t o = (uint32_t)((at + m) * R + r) * 4u;
+        floatx4 q[4];
 #pragma unroll
-        for (int p = 0; p < 8; ++p)
-          if (p < parts) q[p] = *reinterpret_cast<const floatx4*>(part + ((long)p * T + t) * R + r);
+        for (int p = 0; p < 4; ++p) q[p] = load_at<floatx4>(part + (long)min(p, parts - 1) * T * R, o);
+        v = q[0];
 #pragma unroll
-        for (int p = 0; p < 8; ++p)
+        for (int p = 1; p < 4; ++p)
           if (p < parts) v += q[p];
-        if (blockIdx.y == 0 && sums != nullptr)
-          *reinterpret_cast<floatx4*>(sums + t * R + r) = scale_sums ? v * s : v;
+        if (keep_sums) store_at<floatx4>(sums, (place[m] * (uint32_t)R + r) * 4u, scale_sums ? v * s : v);
       }
       uint2 hi, lo;
       split2(v[0] * s, v[1] * s, hi.x, lo.x);
@@ -425,73 +544,32 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(
       *reinterpret_cast<uint2*>(&low.v[m][Low::kLo + r]) = lo;
     }
     __syncthreads();
-    if (out == nullptr) continue;
-    const uint16_t* w = W + (long)adapter * R * D;
-    for (int c0 = c_begin + 64 * wave; c0 < c_end; c0 += 256) {
-      const int c = c0 + 16 * g;  // the lane's columns of the result
-      uint4 bv[4][2];
+    if (out == nullptr || c0 >= D) continue;
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        bv[f][0] = bv[f][1] = make_uint4(0, 0, 0, 0);
-        if (f < nf && base && 16 * f + col < len && c < D) {
-          const uint16_t* b = base + (t0 + place[16 * f + col]) * D + c;
-          bv[f][0] = *reinterpret_cast<const uint4*>(b);
-          bv[f][1] = *reinterpret_cast<const uint4*>(b + 8);
+    for (int f = 0; f < 4; ++f) {
+      if (f >= nf) continue;
+      floatx4 acc[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) acc[b] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+      const uint16_t* row = low.v[16 * f + col];
+#pragma unroll
+      for (int q = 0; q < Low::kSteps; ++q) {
+        const uint4 vh = *reinterpret_cast<const uint4*>(row + 32 * q + 8 * g);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) acc[b] = mfma16(wop[q][b], as_bf16x8(vh), acc[b]);
+        if (NR > 1) {
+          const uint4 vl = *reinterpret_cast<const uint4*>(row + Low::kLo + 32 * q + 8 * g);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) acc[b] = mfma16(wop[q][b], as_bf16x8(vl), acc[b]);
         }
       }
-      bf16x8_t wop[Low::kSteps][4];
-      if constexpr (kTrans) {
-        Rows8<4> rows[Low::kSteps];
-        const int cc = c0 + 4 * col;
+      if (16 * f + col < len) {
+        float res[16];
 #pragma unroll
-        for (int q = 0; q < Low::kSteps; ++q) {
-          const int r = NR == 1 ? 8 * (g & 1) : 32 * q + 8 * g;
+        for (int b = 0; b < 4; ++b)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) rows[q].load(j, w + (long)(r + j) * D + cc, cc < D && r < R);
-        }
-#pragma unroll
-        for (int q = 0; q < Low::kSteps; ++q)
-#pragma unroll
-          for (int b = 0; b < 4; ++b) wop[q][b] = rows[q].column(b);
-      } else {
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int cc = c0 + 16 * (col >> 2) + 4 * b + (col & 3);
-#pragma unroll
-          for (int q = 0; q < Low::kSteps; ++q) {
-            const int r = NR == 1 ? 8 * (g & 1) : 32 * q + 8 * g;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (cc < D && r < R) v = *reinterpret_cast<const uint4*>(w + (long)cc * R + r);
-            wop[q][b] = as_bf16x8(v);
-          }
-        }
-      }
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        if (f >= nf) continue;
-        floatx4 acc[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) acc[b] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-        const uint16_t* row = low.v[16 * f + col];
-#pragma unroll
-        for (int q = 0; q < Low::kSteps; ++q) {
-          const uint4 vh = *reinterpret_cast<const uint4*>(row + 32 * q + 8 * g);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) acc[b] = mfma16(wop[q][b], as_bf16x8(vh), acc[b]);
-          if (NR > 1) {
-            const uint4 vl = *reinterpret_cast<const uint4*>(row + Low::kLo + 32 * q + 8 * g);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) acc[b] = mfma16(wop[q][b], as_bf16x8(vl), acc[b]);
-          }
-        }
-        if (16 * f + col < len && c < D) {
-          float res[16];
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) res[kTrans ? 4 * i + b : 4 * b + i] = acc[b][i];
-          store16(out + (t0 + place[16 * f + col]) * D + c, res, bv[f]);
-        }
+          for (int i = 0; i < 4; ++i) res[kTrans ? 4 * i + b : 4 * b + i] = acc[b][i];
+        store16(out, (place[16 * f + col] * (uint32_t)D + c) * 2u, c < D, c + 32 < D, res, bv[f]);
       }
     }
   }
@@ -547,8 +625,8 @@ __global__ __launch_bounds__(256, 2) void adapter_grad_kernel(GradParams p) {
   const bool down = chunk < down_chunks;
   const int c0 = (down ? chunk : chunk - down_chunks) * kCols;
   const int D = down ? p.H : p.N, R = p.R;
-  const uint16_t* in = down ? p.x : p.dy;
-  const float* low = down ? p.du : p.v;
+  const uint16_t* in = (down ? p.x : p.dy) + (long)seg0 * D;  // tokens count from the segment's first
+  const float* low = (down ? p.du : p.v) + (long)seg0 * R;
   const float s = down ? 1.0f : p.scale[a];
   // the adapter's tokens, in order: thread t looks at the t-th 16 of the segment
   uint32_t hit = 0;
@@ -557,7 +635,7 @@ __global__ __launch_bounds__(256, 2) void adapter_grad_kernel(GradParams p) {
     const int t = seg0 + tid * (kSegMax / 256) + j;
     if (t < seg1 && adapter_of(p.ids, p.ids64, t, p.n) == a) hit |= 1u << j;
   }
-  const int incl = wave_inclusive_sum(__popc(hit), lane);
+  const int incl = wave_inclusive_sum(__popc(hit));
   if (lane == 63) wave_count[wave] = incl;
   __syncthreads();
   int at = incl - __popc(hit), have = 0;
@@ -567,7 +645,7 @@ __global__ __launch_bounds__(256, 2) void adapter_grad_kernel(GradParams p) {
   }
 #pragma unroll
   for (int j = 0; j < kSegMax / 256; ++j)
-    if (hit >> j & 1) list[at++] = seg0 + tid * (kSegMax / 256) + j;
+    if (hit >> j & 1) list[at++] = tid * (kSegMax / 256) + j;
   if (tid < 32) list[have + tid] = -1;
   __syncthreads();
   floatx4 acc[NR][NB];
@@ -585,7 +663,7 @@ __global__ __launch_bounds__(256, 2) void adapter_grad_kernel(GradParams p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       tok[j] = t[j];
-      next.load(j, in + (long)t[j] * D + cc, t[j] >= 0 && cc < D);
+      next.load(j, in, ((uint32_t)t[j] * D + cc) * 2u, t[j] >= 0 && cc < D);
     }
   };
   if (32 * wave < have) fetch(32 * wave);
@@ -597,7 +675,7 @@ __global__ __launch_bounds__(256, 2) void adapter_grad_kernel(GradParams p) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int r = r_begin + 16 * c + col;
-        lv[c][j] = tok[j] >= 0 && r < R ? low[(long)tok[j] * R + r] : 0.0f;
+        lv[c][j] = tok[j] >= 0 && r < R ? load_at<float>(low, ((uint32_t)tok[j] * R + r) * 4u) : 0.0f;
       }
 #pragma unroll
     for (int b = 0; b < NB; ++b) op[b] = next.column(b);
@@ -697,21 +775,13 @@ __global__ __launch_bounds__(256) void adapter_sum_kernel(const floatx4* __restr
 
 static int spans_of(int T) { return (T + kSpan - 1) / kSpan; }
 
-// Workgroups that share the units of a span: as many as there can be units while the launch
-// stays within some thousand workgroups.
-static int span_share(int T, int n, int others) {
+// Workgroups that share the units (of `size` tokens at most) of a span: as many as there can
+// be while the launch stays within some thousand workgroups.
+static int span_share(int T, int n, int size, int others) {
   const int tokens = T < kSpan ? T : kSpan;
-  const int most = (tokens + kUnit - 1) / kUnit + (n < tokens ? n : tokens);
+  const int most = (tokens + size - 1) / size + (n < tokens ? n : tokens);
   const int room = 8192 / (spans_of(T) * others);
   return room < 1 ? 1 : (room < most ? room : most);
-}
-
-// Columns of one expanding workgroup: 256 at least, one pass of its four waves.
-static int expand_chunk(int T, int n, int D) {
-  const long units = (T + kUnit - 1) / kUnit + (n < T ? n : T);
-  int chunk = 2048;
-  while (chunk > 256 && units * ((D + chunk - 1) / chunk) < 1024) chunk /= 2;
-  return chunk;
 }
 
 namespace {
@@ -751,34 +821,33 @@ static AdapterLayout adapter_layout(void* ws, int T, int n, int H, int N, int R,
 
 static hipError_t reduce(bool trans, const void* in, const AdapterParams& p, int D, const void* W,
                          const AdapterLayout& l, hipStream_t s) {
-  const int parts = adapter_parts(D), share = span_share(p.T, p.n, parts);
-  const dim3 grid(spans_of(p.T) * share, parts);
-  const int span = adapter_span(D);
+  const int parts = adapter_parts(D), share = span_share(p.T, p.n, kUnit / 2, parts);
+  const dim3 grid(parts, spans_of(p.T) * share);
+  const int length = adapter_part_length(D);
   const uint16_t* x = static_cast<const uint16_t*>(in);
   const uint16_t* w = static_cast<const uint16_t*>(W);
   if (trans)
-    PMOE_BY_RANK(p.R, (adapter_reduce_kernel<NR, true><<<grid, 256, 0, s>>>(
-                          x, p.ids, p.ids64, p.T, p.n, D, p.R, w, span, share, l.orders, l.part)));
+    PMOE_BY_RANK(p.R, (adapter_reduce_kernel<NR, true><<<grid, kReduceThreads, 0, s>>>(
+                          x, p.ids, p.ids64, p.T, p.n, D, p.R, w, length, share, l.orders, l.part)));
   else
-    PMOE_BY_RANK(p.R, (adapter_reduce_kernel<NR, false><<<grid, 256, 0, s>>>(
-                          x, p.ids, p.ids64, p.T, p.n, D, p.R, w, span, share, l.orders, l.part)));
+    PMOE_BY_RANK(p.R, (adapter_reduce_kernel<NR, false><<<grid, kReduceThreads, 0, s>>>(
+                          x, p.ids, p.ids64, p.T, p.n, D, p.R, w, length, share, l.orders, l.part)));
   return hipGetLastError();
 }
 
 static hipError_t expand(bool trans, int parts, const AdapterParams& p, int D, const void* W,
                          const AdapterLayout& l, float* sums, int scale_sums, hipStream_t s) {
-  const int chunk = expand_chunk(p.T, p.n, D);
-  const int chunks = p.out ? (D + chunk - 1) / chunk : 1, share = span_share(p.T, p.n, chunks);
-  const dim3 grid(spans_of(p.T) * share, chunks);
+  const int chunks = p.out ? (D + 255) / 256 : 1, share = span_share(p.T, p.n, kUnit, chunks);
+  const dim3 grid(chunks, spans_of(p.T) * share);
   const uint16_t* w = static_cast<const uint16_t*>(W);
   const uint16_t* b = static_cast<const uint16_t*>(p.base);
   uint16_t* o = static_cast<uint16_t*>(p.out);
   if (trans)
     PMOE_BY_RANK(p.R, (adapter_expand_kernel<NR, true><<<grid, 256, 0, s>>>(
-                          l.part, parts, l.orders, share, p.T, D, p.R, w, p.scale, b, o, sums, scale_sums, chunk)));
+                          l.part, parts, l.orders, share, p.T, D, p.R, w, p.scale, b, o, sums, scale_sums)));
   else
     PMOE_BY_RANK(p.R, (adapter_expand_kernel<NR, false><<<grid, 256, 0, s>>>(
-                          l.part, parts, l.orders, share, p.T, D, p.R, w, p.scale, b, o, sums, scale_sums, chunk)));
+                          l.part, parts, l.orders, share, p.T, D, p.R, w, p.scale, b, o, sums, scale_sums)));
   return hipGetLastError();
 }
 
