@@ -229,9 +229,9 @@ __device__ __forceinline__ void keep_order(const SpanLds& l, int units, int coun
 
 // ---------------------------------------------------------------- reduction over H (or N)
 // A sum over a row of D elements is cut into parts of adapter_part_length(D) elements (a
-// multiple of 64, at most 4096), one workgroup of eight waves each, whose waves take pieces of
-// 64 or 128 elements in turn: together they read a row in long stretches.
-int adapter_parts(int D) { return (D + 4095) / 4096; }
+// multiple of 64, at most 2048), one workgroup of eight waves each, whose waves take pieces of
+// 64 elements in turn: together they read a row in long stretches.
+int adapter_parts(int D) { return (D + 2047) / 2048; }
 static int adapter_part_length(int D) { return ((D + adapter_parts(D) - 1) / adapter_parts(D) + 63) / 64 * 64; }
 
 // Eight rows of kCols columns each, turned: op[b] gets the eight values of
@@ -265,112 +265,117 @@ struct Rows8 {
   }
 };
 
+// A block of 16 rows x 64 elements on its way to the MFMA operands. An operand wants lane
+// (col, g) to hold eight elements of row col, which would make every lane of a load its own
+// cache access. So eight neighbouring lanes load the 128 bytes of a row (16 bytes each), and
+// the block is turned through 2 KB of LDS that belong to the wave alone (its LDS operations
+// stay in order); chunk c of row r lies at chunk c ^ (r & 7), which keeps both sides free of
+// bank conflicts.
+struct Block16 {
+  uint4 v[2];  // rows 8 j + lane / 8
+  __device__ __forceinline__ void load(int j, const void* base, uint32_t offset, bool on) {
+    v[j] = make_uint4(0, 0, 0, 0);
+    if (on) v[j] = load_at<uint4>(base, offset);
+  }
+  // lo: elements 8 g .. 8 g + 7 of row col, hi: 32 elements further
+  __device__ __forceinline__ void turn(uint4* lds, int lane, bf16x8_t& lo, bf16x8_t& hi) const {
+    const int row = lane >> 3, at = row * 8 + ((lane & 7) ^ row);
+    lds[at] = v[0];
+    lds[at + 64] = v[1];
+    const int col = lane & 15, g = lane >> 4, swap = col & 7;
+    lo = as_bf16x8(lds[col * 8 + (g ^ swap)]);
+    hi = as_bf16x8(lds[col * 8 + ((g + 4) ^ swap)]);
+  }
+};
+
 // part[y][place][r] = sum over the y-th part of in[t][k] * W_a[r][k] (kTrans: W_a[k][r]),
 // t the token at the place of the order. blockIdx.y is a span and one of `share`
-// workgroups that take its half units (32 tokens) in turn.
+// workgroups that take its units (with R > 64 its half units) in turn.
 // Operand row i of block b is r = NR i + b, so that a lane ends with 4 NR consecutive r of
 // one token, and with kTrans a lane reads NR neighbouring columns of eight rows.
 template <int NR, bool kTrans>
-__global__ __launch_bounds__(kReduceThreads) void adapter_reduce_kernel(
+__global__ __launch_bounds__(kReduceThreads, NR <= 2 ? 4 : 2) void adapter_reduce_kernel(
     const uint16_t* __restrict__ in, const void* __restrict__ ids, int ids64, int T, int n, int D, int R,
     const uint16_t* __restrict__ W, int length, int share, SpanOrder* __restrict__ orders,
     float* __restrict__ part) {
-  constexpr int kSteps = NR <= 2 ? 2 : 1;  // steps of 64 that are loaded together
+  constexpr int NF = NR <= 4 ? 4 : 2;      // row blocks of an item: a unit, or half a unit
   __shared__ __align__(16) SpanLds lds;
+  __shared__ uint4 turn[kReduceWaves][2][128];
   __shared__ floatx4 red[kReduceWaves][NR][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col = lane & 15, g = lane >> 4;
+  const int col = lane & 15, g = lane >> 4, row8 = lane >> 3, chunk = lane & 7;
   const int sp = blockIdx.y / share, mine = blockIdx.y % share;
   const long t0 = (long)sp * kSpan;
   const int count = (int)min((long)kSpan, T - t0);
   const int units = group_span(ids, ids64, t0, count, n, lds);
   if (mine == 0 && blockIdx.x == 0) keep_order(lds, units, count, n, orders + sp);
-  const int k_begin = blockIdx.x * length + wave * 64 * kSteps, k_end = min(D, (int)(blockIdx.x + 1) * length);
+  const int k_begin = blockIdx.x * length + wave * 64, k_end = min(D, (int)(blockIdx.x + 1) * length);
   float* dst = part + ((long)blockIdx.x * T + t0) * R;
   const uint16_t* rows_in = in + t0 * D;
-  for (int item = mine; item < 2 * units; item += share) {  // the first halves, then the second
+  for (int item = mine; item < units * (4 / NF); item += share) {  // first halves before second
     const int u = item < units ? item : item - units;
     const int start = uniform(lds.start[u]), end = uniform(lds.start[u + 1]);
-    const int at = item < units ? start : start + 32, len = min(32, end - at);
+    const int at = item < units ? start : start + 16 * NF, len = min(16 * NF, end - at);
     const int adapter = uniform(lds.key[start] >> 10);
     if (len <= 0 || adapter == n) continue;
     const int nf = (len + 15) >> 4;
-    uint32_t x[2];  // where the rows begin
+    uint32_t x[2 * NF];  // where row 8 j + lane / 8 begins
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
-      x[f] = (lds.key[at + min(16 * f + col, len - 1)] & (kSpan - 1)) * (uint32_t)D * 2u;
+    for (int j = 0; j < 2 * NF; ++j)
+      x[j] = (lds.key[at + min(8 * j + row8, len - 1)] & (kSpan - 1)) * (uint32_t)D * 2u;
     const uint16_t* w = W + (long)adapter * R * D;
-    floatx4 acc[2][NR];
+    floatx4 acc[NF][NR];
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+    for (int f = 0; f < NF; ++f)
 #pragma unroll
       for (int c = 0; c < NR; ++c) acc[f][c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int r0 = NR * col;
-    for (int k0 = k_begin; k0 < k_end; k0 += 64 * kSteps * kReduceWaves) {
-      uint4 xv[kSteps][2][2];
+    for (int k0 = k_begin; k0 < k_end; k0 += 64 * kReduceWaves) {
+      Block16 xb[NF];
+      const int kc = k0 + 8 * chunk;
 #pragma unroll
-      for (int q = 0; q < kSteps; ++q) {
-        const int k = k0 + 64 * q + 8 * g;  // the lane's elements: k .. k + 7 and k + 32 .. k + 39
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          xv[q][f][0] = xv[q][f][1] = make_uint4(0, 0, 0, 0);
-          if (f < nf && 16 * f + col < len) {
-            if (k < k_end) xv[q][f][0] = load_at<uint4>(rows_in, x[f] + 2u * k);
-            if (k + 32 < k_end) xv[q][f][1] = load_at<uint4>(rows_in, x[f] + 2u * k + 64u);
-          }
-        }
-      }
-      bf16x8_t wv[kSteps][NR][2];
+      for (int j = 0; j < 2 * NF; ++j)
+        xb[j >> 1].load(j & 1, rows_in, x[j] + 2u * kc, 8 * j + row8 < len && kc < k_end);
+      bf16x8_t wv[NR][2];
       if constexpr (kTrans) {
-        Rows8<NR> rows[kSteps][2];
+        Rows8<NR> rows[2];
+        const int r0 = NR * col, k = k0 + 8 * g;
 #pragma unroll
-        for (int q = 0; q < kSteps; ++q) {
-          const int k = k0 + 64 * q + 8 * g;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int j = 0; j < 8; ++j)
+            rows[h].load(j, w + (32 * h + j) * R, ((uint32_t)k * R + r0) * 2u, k + 32 * h < k_end && r0 < R);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              rows[q][h].load(j, w + (32 * h + j) * R, ((uint32_t)k * R + r0) * 2u, k + 32 * h < k_end && r0 < R);
+        for (int c = 0; c < NR; ++c) {
+          wv[c][0] = rows[0].column(c);
+          wv[c][1] = rows[1].column(c);
         }
-#pragma unroll
-        for (int q = 0; q < kSteps; ++q)
-#pragma unroll
-          for (int c = 0; c < NR; ++c) {
-            wv[q][c][0] = rows[q][0].column(c);
-            wv[q][c][1] = rows[q][1].column(c);
-          }
       } else {
+        Block16 wb[NR];
 #pragma unroll
-        for (int q = 0; q < kSteps; ++q) {
-          const int k = k0 + 64 * q + 8 * g;
+        for (int c = 0; c < NR; ++c)
 #pragma unroll
-          for (int c = 0; c < NR; ++c) {
-            uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-            if (r0 + c < R) {
-              const uint32_t o = ((uint32_t)(r0 + c) * D + k) * 2u;
-              if (k < k_end) lo = load_at<uint4>(w, o);
-              if (k + 32 < k_end) hi = load_at<uint4>(w, o + 64u);
-            }
-            wv[q][c][0] = as_bf16x8(lo);
-            wv[q][c][1] = as_bf16x8(hi);
+          for (int j = 0; j < 2; ++j) {
+            const int r = NR * (8 * j + row8) + c;
+            wb[c].load(j, w, ((uint32_t)r * D + kc) * 2u, r < R && kc < k_end);
           }
-        }
+#pragma unroll
+        for (int c = 0; c < NR; ++c) wb[c].turn(turn[wave][c & 1], lane, wv[c][0], wv[c][1]);
       }
 #pragma unroll
-      for (int q = 0; q < kSteps; ++q)
+      for (int f = 0; f < NF; ++f) {
+        if (f >= nf) continue;
+        bf16x8_t lo, hi;
+        xb[f].turn(turn[wave][f & 1], lane, lo, hi);
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          if (f >= nf) continue;
-#pragma unroll
-          for (int c = 0; c < NR; ++c) {
-            acc[f][c] = mfma16(wv[q][c][0], as_bf16x8(xv[q][f][0]), acc[f][c]);
-            acc[f][c] = mfma16(wv[q][c][1], as_bf16x8(xv[q][f][1]), acc[f][c]);
-          }
+        for (int c = 0; c < NR; ++c) {
+          acc[f][c] = mfma16(wv[c][0], lo, acc[f][c]);
+          acc[f][c] = mfma16(wv[c][1], hi, acc[f][c]);
         }
+      }
     }
     // the waves' sums, in wave order; value (c, lane, i) is r = 4 NR g + NR i + c
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
+    for (int f = 0; f < NF; ++f) {
       if (f >= nf) continue;
 #pragma unroll
       for (int c = 0; c < NR; ++c) red[wave][c][lane] = acc[f][c];
@@ -528,13 +533,14 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(
       floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
       if (m < len && r < R) {
         const uint32_t o = (uint32_t)((at + m) * R + r) * 4u;
-        floatx4 q[4];
+        for (int p = 0; p < parts; p += 4) {
+          floatx4 q[4];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) q[p] = load_at<floatx4>(part + (long)min(p, parts - 1) * T * R, o);
-        v = q[0];
+          for (int y = 0; y < 4; ++y) q[y] = load_at<floatx4>(part + (long)min(p + y, parts - 1) * T * R, o);
 #pragma unroll
-        for (int p = 1; p < 4; ++p)
-          if (p < parts) v += q[p];
+          for (int y = 0; y < 4; ++y)
+            if (p + y < parts) v += q[y];
+        }
         if (keep_sums) store_at<floatx4>(sums, (place[m] * (uint32_t)R + r) * 4u, scale_sums ? v * s : v);
       }
       uint2 hi, lo;
@@ -775,11 +781,11 @@ __global__ __launch_bounds__(256) void adapter_sum_kernel(const floatx4* __restr
 
 static int spans_of(int T) { return (T + kSpan - 1) / kSpan; }
 
-// Workgroups that share the units (of `size` tokens at most) of a span: as many as there can
-// be while the launch stays within some thousand workgroups.
-static int span_share(int T, int n, int size, int others) {
+// Workgroups that share the units of a span: as many as there can be while the launch stays
+// within some thousand workgroups.
+static int span_share(int T, int n, int others) {
   const int tokens = T < kSpan ? T : kSpan;
-  const int most = (tokens + size - 1) / size + (n < tokens ? n : tokens);
+  const int most = (tokens + kUnit - 1) / kUnit + (n < tokens ? n : tokens);
   const int room = 8192 / (spans_of(T) * others);
   return room < 1 ? 1 : (room < most ? room : most);
 }
@@ -821,7 +827,7 @@ static AdapterLayout adapter_layout(void* ws, int T, int n, int H, int N, int R,
 
 static hipError_t reduce(bool trans, const void* in, const AdapterParams& p, int D, const void* W,
                          const AdapterLayout& l, hipStream_t s) {
-  const int parts = adapter_parts(D), share = span_share(p.T, p.n, kUnit / 2, parts);
+  const int parts = adapter_parts(D), share = span_share(p.T, p.n, parts);
   const dim3 grid(parts, spans_of(p.T) * share);
   const int length = adapter_part_length(D);
   const uint16_t* x = static_cast<const uint16_t*>(in);
@@ -837,7 +843,7 @@ static hipError_t reduce(bool trans, const void* in, const AdapterParams& p, int
 
 static hipError_t expand(bool trans, int parts, const AdapterParams& p, int D, const void* W,
                          const AdapterLayout& l, float* sums, int scale_sums, hipStream_t s) {
-  const int chunks = p.out ? (D + 255) / 256 : 1, share = span_share(p.T, p.n, kUnit, chunks);
+  const int chunks = p.out ? (D + 255) / 256 : 1, share = span_share(p.T, p.n, chunks);
   const dim3 grid(chunks, spans_of(p.T) * share);
   const uint16_t* w = static_cast<const uint16_t*>(W);
   const uint16_t* b = static_cast<const uint16_t*>(p.base);
