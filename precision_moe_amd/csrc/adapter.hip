@@ -44,7 +44,7 @@ __device__ __forceinline__ floatx4 mfma16(bf16x8_t a, bf16x8_t b, floatx4 c) {
 
 // Loads and stores at a 32-bit byte offset from a pointer that is the same in all lanes: the
 // pointer stays in scalar registers. Offsets within a span of tokens or within one adapter's
-// matrix, and within a segment of 4096 tokens, are at most 2^27.
+// matrix, and within a window of 4096 tokens, are at most 2^27.
 template <typename V>
 __device__ __forceinline__ V load_at(const void* base, uint32_t offset) {
   return *reinterpret_cast<const V*>(static_cast<const char*>(base) + offset);
@@ -52,6 +52,26 @@ __device__ __forceinline__ V load_at(const void* base, uint32_t offset) {
 template <typename V>
 __device__ __forceinline__ void store_at(void* base, uint32_t offset, V v) {
   *reinterpret_cast<V*>(static_cast<char*>(base) + offset) = v;
+}
+// A buffer that starts at such a pointer, and loads from it that are 0 where `on` is false:
+// their offset lies behind the buffer's end, which the hardware's range check turns into zeros,
+// so that a masked load needs neither a branch nor registers set beforehand. `scalar` is an
+// offset that is the same in all lanes.
+using Buffer = __amdgpu_buffer_rsrc_t;
+__device__ __forceinline__ Buffer buffer_of(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+template <typename V>
+__device__ __forceinline__ V load_if(Buffer b, uint32_t offset, bool on, int scalar = 0) {
+  const uint32_t o = on ? offset : 0x80000000u;
+  if constexpr (sizeof(V) == 16)
+    return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b128(b, o, scalar, 0));
+  else if constexpr (sizeof(V) == 8)
+    return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b64(b, o, scalar, 0));
+  else if constexpr (sizeof(V) == 4)
+    return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b32(b, o, scalar, 0));
+  else
+    return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b16(b, o, scalar, 0));
 }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -240,19 +260,16 @@ template <int kCols>
 struct Rows8 {
   static constexpr int kWords = kCols < 2 ? 1 : kCols / 2;
   uint32_t w[8][kWords];
-  __device__ __forceinline__ void load(int j, const void* base, uint32_t offset, bool on) {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[j][i] = 0;
-    if (!on) return;
+  __device__ __forceinline__ void load(int j, Buffer from, uint32_t offset, bool on, int scalar = 0) {
     if constexpr (kCols == 1) {
-      w[j][0] = load_at<uint16_t>(base, offset);
+      w[j][0] = load_if<uint16_t>(from, offset, on, scalar);
     } else if constexpr (kCols == 2) {
-      w[j][0] = load_at<uint32_t>(base, offset);
+      w[j][0] = load_if<uint32_t>(from, offset, on, scalar);
     } else if constexpr (kCols == 4) {
-      const uint2 u = load_at<uint2>(base, offset);
+      const uint2 u = load_if<uint2>(from, offset, on, scalar);
       w[j][0] = u.x, w[j][1] = u.y;
     } else {
-      const uint4 u = load_at<uint4>(base, offset);
+      const uint4 u = load_if<uint4>(from, offset, on, scalar);
       w[j][0] = u.x, w[j][1] = u.y, w[j][2] = u.z, w[j][3] = u.w;
     }
   }
@@ -273,9 +290,8 @@ struct Rows8 {
 // bank conflicts.
 struct Block16 {
   uint4 v[2];  // rows 8 j + lane / 8
-  __device__ __forceinline__ void load(int j, const void* base, uint32_t offset, bool on) {
-    v[j] = make_uint4(0, 0, 0, 0);
-    if (on) v[j] = load_at<uint4>(base, offset);
+  __device__ __forceinline__ void load(int j, Buffer from, uint32_t offset, bool on) {
+    v[j] = load_if<uint4>(from, offset, on);
   }
   // lo: elements 8 g .. 8 g + 7 of row col, hi: 32 elements further
   __device__ __forceinline__ void turn(uint4* lds, int lane, bf16x8_t& lo, bf16x8_t& hi) const {
@@ -311,7 +327,7 @@ __global__ __launch_bounds__(kReduceThreads, NR <= 2 ? 4 : 2) void adapter_reduc
   if (mine == 0 && blockIdx.x == 0) keep_order(lds, units, count, n, orders + sp);
   const int k_begin = blockIdx.x * length + wave * 64, k_end = min(D, (int)(blockIdx.x + 1) * length);
   float* dst = part + ((long)blockIdx.x * T + t0) * R;
-  const uint16_t* rows_in = in + t0 * D;
+  const Buffer rows_in = buffer_of(in + t0 * D, (uint32_t)count * D * 2u);
   for (int item = mine; item < units * (4 / NF); item += share) {  // first halves before second
     const int u = item < units ? item : item - units;
     const int start = uniform(lds.start[u]), end = uniform(lds.start[u + 1]);
@@ -323,7 +339,7 @@ __global__ __launch_bounds__(kReduceThreads, NR <= 2 ? 4 : 2) void adapter_reduc
 #pragma unroll
     for (int j = 0; j < 2 * NF; ++j)
       x[j] = (lds.key[at + min(8 * j + row8, len - 1)] & (kSpan - 1)) * (uint32_t)D * 2u;
-    const uint16_t* w = W + (long)adapter * R * D;
+    const Buffer w = buffer_of(W + (long)adapter * R * D, (uint32_t)R * D * 2u);
     floatx4 acc[NF][NR];
 #pragma unroll
     for (int f = 0; f < NF; ++f)
@@ -343,7 +359,7 @@ __global__ __launch_bounds__(kReduceThreads, NR <= 2 ? 4 : 2) void adapter_reduc
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            rows[h].load(j, w + (32 * h + j) * R, ((uint32_t)k * R + r0) * 2u, k + 32 * h < k_end && r0 < R);
+            rows[h].load(j, w, ((uint32_t)k * R + r0) * 2u, k + 32 * h < k_end && r0 < R, (32 * h + j) * R * 2);
 #pragma unroll
         for (int c = 0; c < NR; ++c) {
           wv[c][0] = rows[0].column(c);
@@ -465,6 +481,7 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(
   const bool fill = out != nullptr && base != out;
   if (base) base += t0 * D;
   if (out) out += t0 * D;
+  const Buffer base_rows = buffer_of(base, base ? (uint32_t)min((long)kSpan, T - t0) * D * 2u : 0u);
   const bool keep_sums = sums != nullptr && blockIdx.x == 0;
   if (sums) sums += t0 * R;
   part += t0 * R;
@@ -487,7 +504,7 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(
     }
     const int nf = (len + 15) >> 4;
     const float s = scale[adapter];
-    const uint16_t* w = W + (long)adapter * R * D;
+    const Buffer w = buffer_of(W + (long)adapter * R * D, (uint32_t)R * D * 2u);
     bf16x8_t wop[Low::kSteps][4];
     if constexpr (kTrans) {
       Rows8<4> rows[Low::kSteps];
@@ -497,7 +514,7 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(
         const int rg = NR == 1 ? 8 * (g & 1) : 8 * g;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          rows[q].load(j, w + (long)(32 * q + j) * D, ((uint32_t)rg * D + cc) * 2u, cc < D && 32 * q + rg < R);
+          rows[q].load(j, w, ((uint32_t)rg * D + cc) * 2u, cc < D && 32 * q + rg < R, (32 * q + j) * D * 2);
       }
 #pragma unroll
       for (int q = 0; q < Low::kSteps; ++q)
@@ -510,9 +527,7 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(
 #pragma unroll
         for (int q = 0; q < Low::kSteps; ++q) {
           const int r = NR == 1 ? 8 * (g & 1) : 32 * q + 8 * g;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (cc < D && r < R) v = load_at<uint4>(w, ((uint32_t)cc * R + r) * 2u);
-          wop[q][b] = as_bf16x8(v);
+          wop[q][b] = as_bf16x8(load_if<uint4>(w, ((uint32_t)cc * R + r) * 2u, cc < D && r < R));
         }
       }
     }
@@ -520,12 +535,10 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(
     uint4 bv[4][2];
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
-      bv[f][0] = bv[f][1] = make_uint4(0, 0, 0, 0);
-      if (f < nf && base && 16 * f + col < len) {
-        const uint32_t b = (place[16 * f + col] * (uint32_t)D + c) * 2u;
-        if (c < D) bv[f][0] = load_at<uint4>(base, b);
-        if (c + 32 < D) bv[f][1] = load_at<uint4>(base, b + 64u);
-      }
+      const int m = 16 * f + col;
+      const uint32_t b = (place[m] * (uint32_t)D + c) * 2u;  // without base the buffer is empty
+      bv[f][0] = load_if<uint4>(base_rows, b, m < len && c < D);
+      bv[f][1] = load_if<uint4>(base_rows, b + 64u, m < len && c + 32 < D);
     }
 #pragma unroll 1
     for (int i = tid; i < nf * 16 * (4 * NR); i += 256) {
@@ -582,19 +595,26 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(
 }
 
 // ---------------------------------------------------------------- gradients of the matrices
-// Two values as h + m + l in BF16: all 24 bits of an FP32 value. An infinite value has
-// m = l = 0.
+// Two values as h + m + l in BF16, exactly: h is the upper half of x, which holds its first 8
+// significant bits, m that of the rest, and what then remains has 8 bits at most. An infinite
+// value gives NaN.
 __device__ __forceinline__ void split3(float x, float y, uint32_t& h, uint32_t& m, uint32_t& l) {
-  h = f32x2_to_bf16x2(x, y);
-  const float x1 = finite_rest(x, bf16_to_f32(h & 0xFFFFu)), y1 = finite_rest(y, bf16_to_f32(h >> 16));
-  m = f32x2_to_bf16x2(x1, y1);
-  l = f32x2_to_bf16x2(x1 - bf16_to_f32(m & 0xFFFFu), y1 - bf16_to_f32(m >> 16));
+  constexpr uint32_t kUpper = 0x07060302u;  // {upper half of the first, upper half of the second}
+  const auto upper = [](float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); };
+  h = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), kUpper);
+  const float x1 = x - upper(x), y1 = y - upper(y);
+  m = __builtin_amdgcn_perm(__float_as_uint(y1), __float_as_uint(x1), kUpper);
+  const float x2 = x1 - upper(x1), y2 = y1 - upper(y1);
+  l = __builtin_amdgcn_perm(__float_as_uint(y2), __float_as_uint(x2), kUpper);
 }
 
-constexpr int kSegMax = 4096;  // tokens of one segment at most; an adapter's are listed in LDS
-// Columns of one workgroup of adapter_grad_kernel, 16 NB: with R <= 32 NB = 8, above (where
-// there are four blocks of r) NB = 4, so that the accumulators leave room for two waves.
-static int grad_cols(int R) { return R <= 32 ? 128 : 64; }
+constexpr int kWindow = 4096;  // tokens of one window, of which an adapter's are listed in LDS
+constexpr int kShare = 512;    // listed tokens from which a window is shared by several workgroups
+constexpr int kMostShares = 8;
+__host__ __device__ inline int grad_windows(int T) { return T > kWindow ? (T + kWindow - 1) / kWindow : 1; }
+// Columns of one workgroup of the gradient kernels: 128 with R <= 32 (adapter_grad_kernel),
+// above 256 (adapter_grad_wide_kernel).
+static int grad_cols(int R) { return R <= 32 ? 128 : 256; }
 
 struct GradParams {
   const uint16_t* x;    // [T][H]
@@ -603,161 +623,369 @@ struct GradParams {
   const float* v;       // [T][R]
   const float* scale;   // [n]
   const void* ids;
-  int ids64, T, n, H, N, R, seg;
-  float* d_down;        // [n][R][H], or with several segments the partial sums [segments][n][R][H]
-  float* d_up;          // [n][N][R], likewise
+  int ids64, T, n, H, N, R;
+  int groups, most_shares;  // groups of windows, and shares of each
+  float* d_down;        // [n][R][H]
+  float* d_up;          // [n][N][R]
+  float* part_down;     // sums of the shares [groups * most_shares][n][R][H], with more than one in all
+  float* part_up;       // [groups * most_shares][n][N][R], likewise
+  int* shares;          // [groups][n]: shares that were used, likewise
 };
 
-// One workgroup: adapter blockIdx.y, segment blockIdx.z, 16 NB columns of x (dA)
-// or, behind those, of dy (dB), and 16 NR values of r (with R > 64 there are two
-// such halves). The
-// adapter's tokens of the segment are listed in LDS, the waves take every fourth
-// step of 32 of them, the rows of the next step on their way during one. k is the
-// token here, so both operands are wanted with eight tokens of one column: x (dy)
-// is turned in registers, du (s v) is read column by column.
-template <int NR, int NB>
-__global__ __launch_bounds__(256, 2) void adapter_grad_kernel(GradParams p) {
-  __shared__ __align__(16) int list[kSegMax + 32];
-  __shared__ int wave_count[4];
-  __shared__ floatx4 red[4][NB][64];
-  constexpr int kCols = 16 * NB;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int col = lane & 15, g = lane >> 4;
-  const int a = blockIdx.y, seg0 = blockIdx.z * p.seg;
-  const int seg1 = min(p.T, seg0 + p.seg);
+// What a workgroup of the gradient kernels works on: adapter blockIdx.y, kCols columns of x
+// (dA) or, behind those, of dy (dB), kRows values of r from r_begin on, and a share
+// (blockIdx.z % most_shares) of the adapter's tokens in each window of a group
+// (blockIdx.z / most_shares). A window of 4096 tokens has as many shares as have 512 of the
+// adapter's tokens each, but one at least and most_shares at most.
+template <bool kDown>
+struct GradBlock {
+  int c0, r_begin, D, share, group;
+  float scale;
+  int used;               // most shares of a window so far
+  // of the current window
+  Buffer in;              // rows of x or dy, tokens count from the window's first
+  Buffer low;             // rows of du or v
+  int first, last;        // the share's places in the list
+
+  __device__ __forceinline__ GradBlock(const GradParams& p, int kCols, int kRows) {
+    const int down_chunks = (p.H + kCols - 1) / kCols;
+    const int chunks = down_chunks + (p.N + kCols - 1) / kCols;
+    const int chunk = blockIdx.x % chunks;
+    r_begin = blockIdx.x / chunks * kRows;
+    c0 = (kDown ? chunk : chunk - down_chunks) * kCols;
+    D = kDown ? p.H : p.N;
+    scale = kDown ? 1.0f : p.scale[blockIdx.y];
+    group = blockIdx.z / p.most_shares;
+    share = blockIdx.z % p.most_shares;
+    used = group == 0 ? 1 : 0;  // the first leaves zeros where there are no tokens at all
+  }
+
+  // Windows of the group.
+  __device__ __forceinline__ int begin(const GradParams& p) const {
+    return (int)((long)grad_windows(p.T) * group / p.groups);
+  }
+  __device__ __forceinline__ int end(const GradParams& p) const {
+    return (int)((long)grad_windows(p.T) * (group + 1) / p.groups);
+  }
+
+  // kThreads threads list the adapter's tokens of the window in order, thread t those among
+  // the t-th kWindow / kThreads tokens; behind the share come 64 times -1. Begins and ends
+  // with a barrier.
+  template <int kThreads>
+  __device__ __forceinline__ void list_window(const GradParams& p, int window, int* list, int* wave_count) {
+    constexpr int kPer = kWindow / kThreads;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, a = blockIdx.y;
+    const long t0 = (long)window * kWindow;
+    const int count = (int)min((long)kWindow, p.T - t0);
+    uint32_t hit = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int t = tid * kPer + j;
+      if (t < count && adapter_of(p.ids, p.ids64, t0 + t, p.n) == a) hit |= 1u << j;
+    }
+    const int incl = wave_inclusive_sum(__popc(hit));
+    __syncthreads();  // the window before is done with
+    if (lane == 63) wave_count[wave] = incl;
+    __syncthreads();
+    int at = incl - __popc(hit), have = 0;
+    for (int w = 0; w < kThreads / 64; ++w) {
+      if (w < wave) at += wave_count[w];
+      have += wave_count[w];
+    }
+    have = uniform(have);
+    const int shares = min((have + kShare - 1) / kShare, p.most_shares);
+    const int each = shares > 0 ? ((have + shares - 1) / shares + 31) & ~31 : 0;
+    first = min(share * each, have);
+    last = share < shares ? min(first + each, have) : first;
+    used = max(used, shares);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (hit >> j & 1) {
+        if (at < last) list[at] = tid * kPer + j;
+        ++at;
+      }
+    if (tid < 64) list[last + tid] = -1;
+    in = buffer_of((kDown ? p.x : p.dy) + t0 * D, (uint32_t)count * D * 2u);
+    low = buffer_of((kDown ? p.du : p.v) + t0 * p.R, (uint32_t)count * p.R * 4u);
+    __syncthreads();
+  }
+
+  // Where the sums go: [R][H] or [N][R], null if the share was never used. The first
+  // workgroup leaves the number of shares for adapter_sum_kernel.
+  __device__ __forceinline__ float* output(const GradParams& p) const {
+    const int a = blockIdx.y;
+    if (p.groups * p.most_shares > 1 && share == 0 && blockIdx.x == 0 && threadIdx.x == 0)
+      p.shares[group * p.n + a] = used;
+    if (share >= used) return nullptr;
+    const bool whole = p.groups == 1 && used == 1;
+    float* to = kDown ? (whole ? p.d_down : p.part_down) : (whole ? p.d_up : p.part_up);
+    return to + (whole ? a : (long)blockIdx.z * p.n + a) * p.R * D;
+  }
+};
+
+// Whether a workgroup has columns of x.
+__device__ __forceinline__ bool grad_down(const GradParams& p, int kCols) {
   const int down_chunks = (p.H + kCols - 1) / kCols;
-  const int chunks = down_chunks + (p.N + kCols - 1) / kCols;
-  const int chunk = blockIdx.x % chunks, r_begin = blockIdx.x / chunks * (16 * NR);
-  const bool down = chunk < down_chunks;
-  const int c0 = (down ? chunk : chunk - down_chunks) * kCols;
-  const int D = down ? p.H : p.N, R = p.R;
-  const uint16_t* in = (down ? p.x : p.dy) + (long)seg0 * D;  // tokens count from the segment's first
-  const float* low = (down ? p.du : p.v) + (long)seg0 * R;
-  const float s = down ? 1.0f : p.scale[a];
-  // the adapter's tokens, in order: thread t looks at the t-th 16 of the segment
-  uint32_t hit = 0;
+  return (int)blockIdx.x % (down_chunks + (p.N + kCols - 1) / kCols) < down_chunks;
+}
+
+// Eight values of one column of du (s v), as the three operands of split3.
+__device__ __forceinline__ void split3_column(const float (&v)[8], float s, uint4& h, uint4& m, uint4& l) {
+  split3(v[0] * s, v[1] * s, h.x, m.x, l.x);
+  split3(v[2] * s, v[3] * s, h.y, m.y, l.y);
+  split3(v[4] * s, v[5] * s, h.z, m.z, l.z);
+  split3(v[6] * s, v[7] * s, h.w, m.w, l.w);
+}
+
+// acc[b] += (columns of x) (r)^T, or for dB (r) (columns of dy)^T.
+template <bool kDown, int NB>
+__device__ __forceinline__ void grad_mfma(const bf16x8_t (&op)[NB], uint4 low, floatx4 (&acc)[NB]) {
+  const bf16x8_t w = as_bf16x8(low);
 #pragma unroll
-  for (int j = 0; j < kSegMax / 256; ++j) {
-    const int t = seg0 + tid * (kSegMax / 256) + j;
-    if (t < seg1 && adapter_of(p.ids, p.ids64, t, p.n) == a) hit |= 1u << j;
-  }
-  const int incl = wave_inclusive_sum(__popc(hit));
-  if (lane == 63) wave_count[wave] = incl;
-  __syncthreads();
-  int at = incl - __popc(hit), have = 0;
-  for (int w = 0; w < 4; ++w) {
-    if (w < wave) at += wave_count[w];
-    have += wave_count[w];
-  }
+  for (int b = 0; b < NB; ++b) acc[b] = kDown ? mfma16(op[b], w, acc[b]) : mfma16(w, op[b], acc[b]);
+}
+
+// The listed tokens of step k0 for lane group g, and their rows' columns.
+template <bool kDown, int NB>
+__device__ __forceinline__ void grad_fetch(const GradBlock<kDown>& q, const int* list, int k0, int g, int cc,
+                                           int (&tok)[8], Rows8<NB>& rows) {
+  const int4 a = *reinterpret_cast<const int4*>(&list[k0 + 8 * g]);
+  const int4 b = *reinterpret_cast<const int4*>(&list[k0 + 8 * g + 4]);
+  const int t[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-  for (int j = 0; j < kSegMax / 256; ++j)
-    if (hit >> j & 1) list[at++] = tid * (kSegMax / 256) + j;
-  if (tid < 32) list[have + tid] = -1;
-  __syncthreads();
+  for (int j = 0; j < 8; ++j) {
+    tok[j] = t[j];
+    rows.load(j, q.in, ((uint32_t)t[j] * q.D + cc) * 2u, t[j] >= 0 && cc < q.D);
+  }
+}
+template <bool kDown>
+__device__ __forceinline__ void grad_low(const GradBlock<kDown>& q, int R, const int (&tok)[8], int r, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    v[j] = load_if<float>(q.low, ((uint32_t)tok[j] * R + r) * 4u, tok[j] >= 0 && r < R);
+}
+
+// The gradients for R <= 32, 128 columns and all r to a workgroup of four waves, which take
+// every fourth step of 32 tokens, the rows of the next step on their way during one. k is the
+// token here, so both operands are wanted with eight tokens of one column: x (dy) is turned in
+// registers, du (s v) is read column by column.
+struct GradLds {
+  int list[kWindow + 64];
+  int wave_count[4];
+  floatx4 red[4][8][64];
+};
+template <int NR, bool kDown>
+__device__ __forceinline__ void grad_body(const GradParams& p, GradLds& lds) {
+  constexpr int NB = 8, kCols = 16 * NB;
+  int* list = lds.list;
+  floatx4(*red)[NB][64] = lds.red;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int col = lane & 15, g = lane >> 4, R = p.R;
+  GradBlock<kDown> q(p, kCols, 16 * NR);
   floatx4 acc[NR][NB];
 #pragma unroll
   for (int c = 0; c < NR; ++c)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[c][b] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int cc = c0 + NB * col;
-  Rows8<NB> next;
-  int tok[8];
-  const auto fetch = [&](int k0) {
-    const int4 t0 = *reinterpret_cast<const int4*>(&list[k0 + 8 * g]);
-    const int4 t1 = *reinterpret_cast<const int4*>(&list[k0 + 8 * g + 4]);
-    const int t[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+  const int cc = q.c0 + NB * col;
+  const int end = q.end(p);
+  for (int window = q.begin(p); window < end; ++window) {
+    q.template list_window<256>(p, window, list, lds.wave_count);
+    const int begin = q.first + 32 * wave;
+    Rows8<NB> next;
+    int tok[8];
+    if (begin < q.last) grad_fetch(q, list, begin, g, cc, tok, next);
+    for (int k0 = begin; k0 < q.last; k0 += 128) {
+      bf16x8_t op[NB];
+      float lv[NR][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      tok[j] = t[j];
-      next.load(j, in, ((uint32_t)t[j] * D + cc) * 2u, t[j] >= 0 && cc < D);
-    }
-  };
-  if (32 * wave < have) fetch(32 * wave);
-  for (int k0 = 32 * wave; k0 < have; k0 += 128) {
-    bf16x8_t op[NB];
-    float lv[NR][8];
+      for (int c = 0; c < NR; ++c) grad_low(q, R, tok, 16 * c + col, lv[c]);
 #pragma unroll
-    for (int c = 0; c < NR; ++c)
+      for (int b = 0; b < NB; ++b) op[b] = next.column(b);
+      if (k0 + 128 < q.last) grad_fetch(q, list, k0 + 128, g, cc, tok, next);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int r = r_begin + 16 * c + col;
-        lv[c][j] = tok[j] >= 0 && r < R ? load_at<float>(low, ((uint32_t)tok[j] * R + r) * 4u) : 0.0f;
-      }
-#pragma unroll
-    for (int b = 0; b < NB; ++b) op[b] = next.column(b);
-    if (k0 + 128 < have) fetch(k0 + 128);
-#pragma unroll
-    for (int c = 0; c < NR; ++c) {
-      uint32_t h[4], m[4], l[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) split3(lv[c][2 * j] * s, lv[c][2 * j + 1] * s, h[j], m[j], l[j]);
-      const bf16x8_t ho = as_bf16x8(make_uint4(h[0], h[1], h[2], h[3]));
-      const bf16x8_t mo = as_bf16x8(make_uint4(m[0], m[1], m[2], m[3]));
-      const bf16x8_t lo = as_bf16x8(make_uint4(l[0], l[1], l[2], l[3]));
-      if (down) {  // rows: columns of x, columns: r
-#pragma unroll
-        for (int b = 0; b < NB; ++b) acc[c][b] = mfma16(op[b], lo, acc[c][b]);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) acc[c][b] = mfma16(op[b], mo, acc[c][b]);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) acc[c][b] = mfma16(op[b], ho, acc[c][b]);
-      } else {     // rows: r, columns: columns of dy
-#pragma unroll
-        for (int b = 0; b < NB; ++b) acc[c][b] = mfma16(lo, op[b], acc[c][b]);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) acc[c][b] = mfma16(mo, op[b], acc[c][b]);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) acc[c][b] = mfma16(ho, op[b], acc[c][b]);
+      for (int c = 0; c < NR; ++c) {
+        uint4 h, m, l;
+        split3_column(lv[c], q.scale, h, m, l);
+        grad_mfma<kDown>(op, l, acc[c]);
+        grad_mfma<kDown>(op, m, acc[c]);
+        grad_mfma<kDown>(op, h, acc[c]);
       }
     }
   }
-  // the waves' sums in wave order, 16 values of r at a time
-  const long slot = (long)blockIdx.z * p.n + a;
+  float* out = q.output(p);
+  if (out == nullptr) return;
+  // the waves' sums in wave order, 16 values of r at a time; the lanes' places in LDS are turned
+  // by 4 g, so that the reads meet all banks
 #pragma unroll
   for (int c = 0; c < NR; ++c) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b) red[wave][b][lane] = acc[c][b];
+    for (int b = 0; b < NB; ++b) red[wave][b][g * 16 + ((col + 4 * g) & 15)] = acc[c][b];
     __syncthreads();
-    if (down) {
-      // value (b, lane (col, g), i) is row r = r_begin + 16 c + col, column c0 + NB (4 g + i) + b
-      const int r16 = tid >> 4, gi = tid & 15;
-      const int r = r_begin + 16 * c + r16, h = c0 + NB * gi, ln = (gi >> 2) * 16 + r16;
+    if constexpr (kDown) {
+      // value (b, lane (col, g), i) is row r = 16 c + col, column c0 + NB (4 g + i) + b
+      const int r16 = tid >> 4, gi = tid & 15, gg = gi >> 2;
+      const int r = 16 * c + r16, h = q.c0 + NB * gi, ln = gg * 16 + ((r16 + 4 * gg) & 15);
 #pragma unroll
-      for (int q = 0; q < NB; q += 4) {
+      for (int o = 0; o < NB; o += 4) {
         floatx4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          v[e] = ((red[0][q + e][ln][gi & 3] + red[1][q + e][ln][gi & 3]) + red[2][q + e][ln][gi & 3]) +
-                 red[3][q + e][ln][gi & 3];
-        if (r < R && h < D) *reinterpret_cast<floatx4*>(p.d_down + (slot * R + r) * D + h + q) = v;
+          v[e] = ((red[0][o + e][ln][gi & 3] + red[1][o + e][ln][gi & 3]) + red[2][o + e][ln][gi & 3]) +
+                 red[3][o + e][ln][gi & 3];
+        if (r < R && h < q.D) *reinterpret_cast<floatx4*>(out + (long)r * q.D + h + o) = v;
       }
     } else {
-      // value (b, lane (col, g), i) is row c0 + NB col + b, column r = r_begin + 16 c + 4 g + i
+      // value (b, lane (col, g), i) is row c0 + NB col + b, column r = 16 c + 4 g + i
 #pragma unroll
       for (int item = tid; item < kCols * 4; item += 256) {
-        const int row = item >> 2, gg = item & 3, b = row % NB, ln = gg * 16 + row / NB;
+        const int gg = item & 3, cl = item >> 2 & 15, b = item >> 6, row = NB * cl + b;
+        const int ln = gg * 16 + ((cl + 4 * gg) & 15);
         const floatx4 v = ((red[0][b][ln] + red[1][b][ln]) + red[2][b][ln]) + red[3][b][ln];
-        const int r = r_begin + 16 * c + 4 * gg;
-        if (r < R && c0 + row < D) *reinterpret_cast<floatx4*>(p.d_up + (slot * D + c0 + row) * R + r) = v;
+        const int r = 16 * c + 4 * gg;
+        if (r < R && q.c0 + row < q.D)
+          *reinterpret_cast<floatx4*>(out + (long)(q.c0 + row) * R + r) = v;
       }
     }
     __syncthreads();
   }
 }
 
-// Sums over the segments, in order, for both gradients: quads [0, na4) of the one, then nb4
-// of the other.
-__global__ __launch_bounds__(256) void adapter_sum_kernel(const floatx4* __restrict__ pa, const floatx4* __restrict__ pb,
-                                                          int segments, long na4, long nb4,
-                                                          floatx4* __restrict__ oa, floatx4* __restrict__ ob) {
+template <int NR>
+__global__ __launch_bounds__(256, 2) void adapter_grad_kernel(GradParams p) {
+  __shared__ __align__(16) GradLds lds;
+  if (grad_down(p, 128))
+    grad_body<NR, true>(p, lds);
+  else
+    grad_body<NR, false>(p, lds);
+}
+
+// The gradients for R > 32: 256 columns and 64 values of r (with R > 64 there are two such
+// halves) to a workgroup of eight waves. Four waves take 64 columns each of the even steps of
+// 32 tokens, four of the odd ones. The three operands of du (s v), the same for all columns,
+// are made once for the four: each wave reads and splits 16 of the 64 r and leaves them in
+// LDS, in two buffers, so that one barrier a step is enough; it waits for LDS alone, the
+// loads of the next step stay in flight.
+struct GradWideLds {
+  int list[kWindow + 64];
+  int wave_count[8];
+  // [buffer][even, odd][c][l, m, h][lane]; behind the loop the waves' sums [wave][b][lane]
+  uint4 low[2][2][4][3][64];
+};
+template <bool kDown>
+__device__ __forceinline__ void grad_wide_body(const GradParams& p, GradWideLds& lds) {
+  constexpr int NR = 4, NB = 4, kCols = 64 * NB;
+  int* list = lds.list;
+  auto& low = lds.low;
+  floatx4(*red)[NB][64] = reinterpret_cast<floatx4(*)[NB][64]>(lds.low);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int col = lane & 15, g = lane >> 4, part = wave & 3, odd = wave >> 2, R = p.R;
+  GradBlock<kDown> q(p, kCols, 16 * NR);
+  floatx4 acc[NR][NB];
+#pragma unroll
+  for (int c = 0; c < NR; ++c)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[c][b] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int cc = q.c0 + 16 * NB * part + NB * col;
+  const int r_mine = q.r_begin + 16 * part + col;
+  const int end = q.end(p);
+  for (int window = q.begin(p); window < end; ++window) {
+    q.template list_window<512>(p, window, list, lds.wave_count);
+    Rows8<NB> next;
+    int tok[8];
+    float lv[8];
+    // both halves take the same number of steps; behind the share lie 64 times -1
+    if (q.first < q.last) {
+      grad_fetch(q, list, q.first + 32 * odd, g, cc, tok, next);
+      grad_low(q, R, tok, r_mine, lv);
+    }
+    int buffer = 0;
+    for (int k0 = q.first; k0 < q.last; k0 += 64) {
+      uint4 h, m, l;
+      split3_column(lv, q.scale, h, m, l);
+      low[buffer][odd][part][0][lane] = l;
+      low[buffer][odd][part][1][lane] = m;
+      low[buffer][odd][part][2][lane] = h;
+      bf16x8_t op[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) op[b] = next.column(b);
+      if (k0 + 64 < q.last) {
+        grad_fetch(q, list, k0 + 64 + 32 * odd, g, cc, tok, next);
+        grad_low(q, R, tok, r_mine, lv);
+      }
+      lds_barrier();
+#pragma unroll
+      for (int c = 0; c < NR; ++c)
+#pragma unroll
+        for (int y = 0; y < 3; ++y) {
+          grad_mfma<kDown>(op, low[buffer][odd][c][y][lane], acc[c]);
+          __builtin_amdgcn_sched_barrier(0);  // else all twelve operands are held at once: spills
+        }
+      buffer ^= 1;
+    }
+  }
+  float* out = q.output(p);
+  if (out == nullptr) return;
+#pragma unroll
+  for (int c = 0; c < NR; ++c) {
+    __syncthreads();  // the operands, or the sums before, are no longer read
+    // the lanes' places are turned by 4 (w % 4) + g, so that the reads meet all banks
+#pragma unroll
+    for (int b = 0; b < NB; ++b) red[wave][b][g * 16 + ((col + 4 * part + g) & 15)] = acc[c][b];
+    __syncthreads();
+    if constexpr (kDown) {
+      // value (b, lane (col, g), i) of wave w is row r = r_begin + 16 c + col, column
+      // c0 + 64 (w % 4) + 4 (4 g + i) + b
+#pragma unroll
+      for (int item = tid; item < 16 * kCols / 4; item += 512) {
+        const int r16 = item >> 6, w = item >> 4 & 3, gi = item & 15, gg = gi >> 2;
+        const int ln = gg * 16 + ((r16 + 4 * w + gg) & 15);
+        const int r = q.r_begin + 16 * c + r16, h = q.c0 + 64 * w + 4 * gi;
+        floatx4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = red[w][e][ln][gi & 3] + red[w + 4][e][ln][gi & 3];
+        if (r < R && h < q.D) *reinterpret_cast<floatx4*>(out + (long)r * q.D + h) = v;
+      }
+    } else {
+      // value (b, lane (col, g), i) of wave w is row c0 + 64 (w % 4) + 4 col + b, column
+      // r = r_begin + 16 c + 4 g + i
+#pragma unroll
+      for (int item = tid; item < kCols * 4; item += 512) {
+        const int gg = item & 3, cl = item >> 2 & 15, b = item >> 6 & 3, w = item >> 8, row = 64 * w + 4 * cl + b;
+        const int ln = gg * 16 + ((cl + 4 * w + gg) & 15);
+        const floatx4 v = red[w][b][ln] + red[w + 4][b][ln];
+        const int r = q.r_begin + 16 * c + 4 * gg;
+        if (r < R && q.c0 + row < q.D)
+          *reinterpret_cast<floatx4*>(out + (long)(q.c0 + row) * R + r) = v;
+      }
+    }
+  }
+}
+
+__global__ __launch_bounds__(512, 4) void adapter_grad_wide_kernel(GradParams p) {
+  __shared__ __align__(16) GradWideLds lds;
+  if (grad_down(p, 256))
+    grad_wide_body<true>(p, lds);
+  else
+    grad_wide_body<false>(p, lds);
+}
+
+// Adds the shares of the groups, in order, where there is more than one in all: quads
+// [0, na4) of the adapter's [R][H], then those of its [N][R]. Adapter blockIdx.y.
+__global__ __launch_bounds__(256) void adapter_sum_kernel(GradParams p) {
+  const int a = blockIdx.y;
+  if (p.groups == 1 && p.shares[a] == 1) return;  // written in place
+  const long na4 = (long)p.R * p.H / 4, nb4 = (long)p.R * p.N / 4;
   for (long i = blockIdx.x * 256L + threadIdx.x; i < na4 + nb4; i += (long)gridDim.x * 256) {
     const bool first = i < na4;
-    const long k = first ? i : i - na4, stride = first ? na4 : nb4;
-    const floatx4* part = (first ? pa : pb) + k;
-    floatx4 v = part[0];
-#pragma unroll 4
-    for (int s = 1; s < segments; ++s) v += part[s * stride];
-    (first ? oa : ob)[k] = v;
+    const long size = first ? na4 : nb4, k = a * size + (first ? i : i - na4);
+    const floatx4* part = reinterpret_cast<const floatx4*>(first ? p.part_down : p.part_up) + k;
+    floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int y = 0; y < p.groups; ++y) {
+      const int shares = p.shares[y * p.n + a];
+      for (int s = 0; s < shares; ++s) v += part[(long)(y * p.most_shares + s) * p.n * size];
+    }
+    reinterpret_cast<floatx4*>(first ? p.d_down : p.d_up)[k] = v;
   }
 }
 
@@ -794,15 +1022,32 @@ namespace {
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // The workspace: the orders of the spans, the parts of the reduction, and for the backward
-// call du and the segments' gradients.
+// call du and the sums of the shares.
 struct AdapterLayout {
   SpanOrder* orders;
-  float *part, *du, *d_down, *d_up;
+  float *part, *du, *part_down, *part_up;
+  int* shares;
   size_t bytes;
 };
 }  // namespace
 
-static int grad_segment(int T, int n, int H, int N, int R);
+// Groups of windows and shares of a window: as many as it takes to fill the GPU where few
+// adapters make few workgroups.
+struct GradSplit {
+  int groups, shares;
+};
+static GradSplit grad_split(int T, int n, int H, int N, int R) {
+  const int cols = grad_cols(R), windows = grad_windows(T);
+  const long each = (long)n * ((H + cols - 1) / cols + (N + cols - 1) / cols) * (R > 64 ? 2 : 1);
+  const int want = (int)(((R <= 32 ? 1024 : 768) + each - 1) / each);
+  GradSplit g;
+  g.groups = windows < want ? windows : want;
+  g.shares = (want + g.groups - 1) / g.groups;
+  const int most = T < kWindow ? (T + kShare - 1) / kShare : kMostShares;
+  if (g.shares > most) g.shares = most;
+  if (g.shares < 1) g.shares = 1;
+  return g;
+}
 
 static AdapterLayout adapter_layout(void* ws, int T, int n, int H, int N, int R, bool backward) {
   AdapterLayout l;
@@ -815,11 +1060,13 @@ static AdapterLayout adapter_layout(void* ws, int T, int n, int H, int N, int R,
   l.orders = reinterpret_cast<SpanOrder*>(take(sizeof(SpanOrder) * spans_of(T)));
   l.part = reinterpret_cast<float*>(take((size_t)adapter_parts(backward ? N : H) * T * R * 4));
   if (backward) {
-    const int seg = grad_segment(T, n, H, N, R), segments = (T + seg - 1) / seg;
-    const size_t each = segments > 1 ? (size_t)segments * n * R * 4 : 0;
+    const GradSplit g = grad_split(T, n, H, N, R);
+    const int slots = g.groups * g.shares;
+    const size_t each = slots > 1 ? (size_t)slots * n * R * 4 : 0;
     l.du = reinterpret_cast<float*>(take((size_t)T * R * 4));
-    l.d_down = reinterpret_cast<float*>(take(each * H));
-    l.d_up = reinterpret_cast<float*>(take(each * N));
+    l.part_down = reinterpret_cast<float*>(take(each * H));
+    l.part_up = reinterpret_cast<float*>(take(each * N));
+    l.shares = reinterpret_cast<int*>(take((size_t)g.groups * n * 4));
   }
   l.bytes = o;
   return l;
@@ -857,16 +1104,6 @@ static hipError_t expand(bool trans, int parts, const AdapterParams& p, int D, c
   return hipGetLastError();
 }
 
-// Segments of the tokens for the gradients of the matrices: several where few adapters make few
-// workgroups.
-static int grad_segment(int T, int n, int H, int N, int R) {
-  const int cols = grad_cols(R);
-  const long per_segment = (long)n * ((H + cols - 1) / cols + (N + cols - 1) / cols);
-  int seg = kSegMax;
-  while (seg > 512 && per_segment * ((T + seg - 1) / seg) < 384) seg /= 2;
-  return seg;
-}
-
 size_t adapter_forward_ws_bytes(int T, int n, int H, int N, int R) {
   return adapter_layout(nullptr, T, n, H, N, R, false).bytes;
 }
@@ -891,8 +1128,6 @@ hipError_t launch_adapter_backward(const AdapterParams& p, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (!p.d_down) return hipSuccess;
-  const int seg = grad_segment(p.T, p.n, p.H, p.N, p.R);
-  const int segments = p.T > 0 ? (p.T + seg - 1) / seg : 1;
   GradParams q;
   q.x = static_cast<const uint16_t*>(p.x);
   q.dy = static_cast<const uint16_t*>(p.dy);
@@ -901,19 +1136,23 @@ hipError_t launch_adapter_backward(const AdapterParams& p, hipStream_t s) {
   q.scale = p.scale;
   q.ids = p.ids;
   q.ids64 = p.ids64;
-  q.T = p.T, q.n = p.n, q.H = p.H, q.N = p.N, q.R = p.R, q.seg = seg;
-  q.d_down = segments > 1 ? l.d_down : p.d_down;
-  q.d_up = segments > 1 ? l.d_up : p.d_up;
+  q.T = p.T, q.n = p.n, q.H = p.H, q.N = p.N, q.R = p.R;
+  const GradSplit split = grad_split(p.T, p.n, p.H, p.N, p.R);
+  q.groups = split.groups, q.most_shares = split.shares;
+  q.d_down = p.d_down, q.d_up = p.d_up;
+  q.part_down = l.part_down, q.part_up = l.part_up, q.shares = l.shares;
   const int cols = grad_cols(p.R), chunks = (p.H + cols - 1) / cols + (p.N + cols - 1) / cols;
-  const dim3 grid(chunks * (p.R > 64 ? 2 : 1), p.n, segments);
-  PMOE_BY_RANK(p.R, (adapter_grad_kernel<(NR < 4 ? NR : 4), (NR < 4 ? 8 : 4)><<<grid, 256, 0, s>>>(q)));
+  const dim3 grid(chunks * (p.R > 64 ? 2 : 1), p.n, q.groups * q.most_shares);
+  if (p.R <= 16)
+    adapter_grad_kernel<1><<<grid, 256, 0, s>>>(q);
+  else if (p.R <= 32)
+    adapter_grad_kernel<2><<<grid, 256, 0, s>>>(q);
+  else
+    adapter_grad_wide_kernel<<<grid, 512, 0, s>>>(q);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || segments == 1) return e;
-  const long na4 = (long)p.n * p.R * p.H / 4, nb4 = (long)p.n * p.R * p.N / 4;
-  const long blocks = (na4 + nb4 + 255) / 256;
-  adapter_sum_kernel<<<(int)(blocks < 8192 ? blocks : 8192), 256, 0, s>>>(
-      reinterpret_cast<const floatx4*>(l.d_down), reinterpret_cast<const floatx4*>(l.d_up), segments, na4, nb4,
-      reinterpret_cast<floatx4*>(p.d_down), reinterpret_cast<floatx4*>(p.d_up));
+  if (e != hipSuccess || q.groups * q.most_shares == 1) return e;
+  const long quads = (long)p.R * (p.H + p.N) / 4, blocks = (quads + 255) / 256, room = 8192 / p.n + 1;
+  adapter_sum_kernel<<<dim3((int)(blocks < room ? blocks : room), p.n), 256, 0, s>>>(q);
   return hipGetLastError();
 }
 

@@ -1,7 +1,7 @@
 """GPU parity of the adapters with the float64 oracle.
 
 Tolerances, u = 2^-24. A sum over H (or N) of products of BF16 values (exact in FP32) is taken by
-waves over at most 512 elements each, then over 4 waves and at most 8 parts:
+waves over at most 256 elements each, then over 8 waves and at most 8 parts (below 528 in any cut):
   v, du    528 u of the sum of the sizes;
   out, dx  the FP32 result rounded to BF16 (half a step, 2^-8 of its size) plus the error of the low-rank
            term: that of v (du), two BF16 values for scale * v (rest below 2^-16 of it) and at most 256 + 2
@@ -121,20 +121,21 @@ def test_backward(pm, T, n, H, N, R, order):
     assert np.array_equal(bf16_bits(dx)[plain], c.dx_base[plain])
 
 
-def test_long_batches_of_few_adapters(pm):
-    """Tokens past one segment of the matrices' gradients, with one adapter and with a run that
-    crosses segments; sums over many tokens."""
+@pytest.mark.parametrize("n,R,order", [(1, 16, "one"), (2, 16, "runs"), (3, 16, "mixed"), (300, 16, "mixed"),
+                                       (700, 24, "runs"), (1, 40, "one"), (3, 72, "mixed"), (600, 64, "mixed")])
+def test_long_batches(pm, n, R, order):
+    """Tokens past one window of the matrices' gradients: with few adapters, whose windows are shared
+    by several workgroups, and with many, where one workgroup goes through several windows."""
     import torch
-    for n, order in ((1, "one"), (2, "runs"), (3, "mixed")):
-        c = Case(9001, n, 64, 48, 16, order)
-        v = ot.adapter_forward(c.f("x"), c.ids, c.f("down"), c.f("up"), c.f("scale"))[1].astype(F32)
-        _, d_down, d_up = pm.adapter_backward(c.d("dy"), c.d("x"), dev(v), c.d("ids"), *c.weights(), need_dx=False)
-        torch.cuda.synchronize()
-        args = [c.f(k) for k in ("dy", "x")] + [v, c.ids] + [c.f(k) for k in ("down", "up", "scale")]
-        want = ot.adapter_backward(*args)
-        size = ot.adapter_backward(*[a if a is c.ids else np.abs(a) for a in args])
-        for got, i in ((d_down, 1), (d_up, 2)):
-            assert np.all(np.abs(got.cpu().numpy() - want[i]) <= (9001 + 16 + 528) * U * size[i]), (n, i)
+    c = Case(9001, n, 64, 48, R, order)
+    v = ot.adapter_forward(c.f("x"), c.ids, c.f("down"), c.f("up"), c.f("scale"))[1].astype(F32)
+    _, d_down, d_up = pm.adapter_backward(c.d("dy"), c.d("x"), dev(v), c.d("ids"), *c.weights(), need_dx=False)
+    torch.cuda.synchronize()
+    args = [c.f(k) for k in ("dy", "x")] + [v, c.ids] + [c.f(k) for k in ("down", "up", "scale")]
+    want = ot.adapter_backward(*args)
+    size = ot.adapter_backward(*[a if a is c.ids else np.abs(a) for a in args])
+    for got, i in ((d_down, 1), (d_up, 2)):
+        assert np.all(np.abs(got.cpu().numpy() - want[i]) <= (9001 + 16 + 528) * U * size[i]), (n, i)
 
 
 def test_gradient_matches_differences(pm):
