@@ -111,7 +111,7 @@ def _check(rc):
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+    return t.data_ptr() if t is not None else None      # ctypes turns an int or None into void*
 
 
 def _stream(stream=None, *tensors):
@@ -121,7 +121,7 @@ def _stream(stream=None, *tensors):
     caching allocator does not hand its memory out again before that work is done."""
     import torch
     if stream is None:      # the raw handle alone: a quarter of the cost of a Stream object
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     cur = torch.cuda.current_stream()
     if stream == cur:
         return ctypes.c_void_p(cur.cuda_stream)
@@ -494,7 +494,7 @@ def moe_forward(x, topk_ids, topk_w, weights: PreparedWeights, recipe="per_token
             raise ValueError("adapters of a layer must be [n, R, H] and [n, H, R], adapter_ids [T]")
         _bf16(x, "x", (T, W.H))
         if out is not None:
-            _out(out, "out", torch.bfloat16, (T, W.H), x.device)
+            _out(out, "out", torch.bfloat16, (T, W.H), x)
     topk_ids, ids_type, topk_w = _routing_args(topk_ids, topk_w)
     workspace, out = _moe_buffers(T, K, W, act, x.device, workspace, out)
     evs = _event_array(step_events)
@@ -550,18 +550,17 @@ RouterBalance = namedtuple("RouterBalance", "counts tokens prob balance z")
 
 def _is(t, name, dtype, shape):
     """Checks the dtype and shape of a device tensor argument and returns it contiguous."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}".replace("torch.", ""))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     return t.contiguous()
 
 
-def _out(t, name, dtype, shape, device):
-    """An output: allocated if None, else checked (it is written in place)."""
-    import torch
+def _out(t, name, dtype, shape, like):
+    """An output: allocated on the device of `like` if None, else checked (it is written in place)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return _is(t, name, dtype, shape)
@@ -569,15 +568,17 @@ def _out(t, name, dtype, shape, device):
 
 def _ids(t, name):
     import torch
-    if t.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"{name} must be int32 or int64")
-    return t.contiguous(), IDS_INT32 if t.dtype == torch.int32 else IDS_INT64
+    if t.dtype is torch.int32:
+        return t.contiguous(), IDS_INT32
+    if t.dtype is torch.int64:
+        return t.contiguous(), IDS_INT64
+    raise TypeError(f"{name} must be int32 or int64")
 
 
-def _scratch(need, workspace, device):
+def _scratch(need, workspace, like):
     import torch
     if workspace is None:
-        return torch.empty(max(int(need), 256), dtype=torch.uint8, device=device)
+        return like.new_empty((max(need, 256),), dtype=torch.uint8)
     return workspace
 
 
@@ -618,12 +619,12 @@ def router_balance(logits, topk_ids, seq_offsets=None, out=None, workspace=None,
     import torch
     logits, ids, ids_type, T, K, E = _router_args(logits, topk_ids)
     off, S = _sequences(seq_offsets)
-    given = out if out is not None else RouterBalance(None, None, None, None, None)
-    kinds = ((torch.int32, (S, E)), (torch.int32, (S,)), (torch.float32, (S, E)), (torch.float32, (S,)),
-             (torch.float32, (S,)))
-    res = RouterBalance(*(_out(t, f"out.{name}", dt, shape, logits.device)
-                          for name, t, (dt, shape) in zip(RouterBalance._fields, given, kinds)))
-    ws = _scratch(lib().pmoe_router_balance_workspace_bytes(T, E, K, S), workspace, logits.device)
+    i32, f32 = torch.int32, torch.float32
+    counts, tokens, prob, balance, z = out if out is not None else (None,) * 5
+    res = RouterBalance(_out(counts, "counts", i32, (S, E), logits), _out(tokens, "tokens", i32, (S,), logits),
+                        _out(prob, "prob", f32, (S, E), logits), _out(balance, "balance", f32, (S,), logits),
+                        _out(z, "z", f32, (S,), logits))
+    ws = _scratch(lib().pmoe_router_balance_workspace_bytes(T, E, K, S), workspace, logits)
     _check(lib().pmoe_router_balance(
         _ptr(logits), _ptr(ids), ids_type, T, K, E, _ptr(off), S, *(_ptr(t) for t in res), _ptr(ws),
         ws.numel(), _stream(stream, logits, ids, off, ws, *res)))
@@ -639,7 +640,7 @@ def router_backward(logits, topk_ids, counts=None, tokens=None, d_balance=None, 
     logits, ids, ids_type, T, K, E = _router_args(logits, topk_ids)
     off, S = _sequences(seq_offsets)
     f32, i32 = torch.float32, torch.int32
-    out = _out(out, "out", f32, (T, E), logits.device)
+    out = _out(out, "out", f32, (T, E), logits)
     opt = [None if t is None else _is(t, name, dt, shape)
            for t, name, dt, shape in ((counts, "counts", i32, (S, E)), (tokens, "tokens", i32, (S,)),
                                       (d_balance, "d_balance", f32, (S,)), (d_z, "d_z", f32, (S,)),
@@ -664,8 +665,8 @@ def finalize_backward(dout, z, row_of_route, topk_w, need_d_topk_w=True, need_d_
     row = _is(row_of_route.reshape(-1), "row_of_route", torch.int32, (T * K,))
     topk_w = _is(topk_w, "topk_w", torch.float32, (T, K))
     given = out if out is not None else (None, None)
-    dw = _out(given[0], "d_topk_w", torch.float32, (T, K), z.device) if need_d_topk_w else None
-    dz = _out(given[1], "d_z", torch.bfloat16, (R, H), z.device) if need_d_z else None
+    dw = _out(given[0], "d_topk_w", torch.float32, (T, K), z) if need_d_topk_w else None
+    dz = _out(given[1], "d_z", torch.bfloat16, (R, H), z) if need_d_z else None
     _check(lib().pmoe_finalize_backward(
         _ptr(dout), _ptr(z), _ptr(row), _ptr(topk_w), T, K, H, R, _ptr(dw), _ptr(dz),
         _stream(stream, dout, z, row, topk_w, dw, dz)))
@@ -708,9 +709,9 @@ def adapter_forward(x, adapter_ids, down, up, scale, base=None, out=None, v=None
     x = _bf16(x, "x", (T, H))
     if base is not None:
         base = _bf16(base, "base", (T, N))
-    out = _out(out, "out", torch.bfloat16, (T, N), x.device)
-    v = _out(v, "v", torch.float32, (T, R), x.device) if need_v else None
-    ws = _scratch(lib().pmoe_adapter_workspace_bytes(T, n, H, N, R, 0), workspace, x.device)
+    out = _out(out, "out", torch.bfloat16, (T, N), x)
+    v = _out(v, "v", torch.float32, (T, R), x) if need_v else None
+    ws = _scratch(lib().pmoe_adapter_workspace_bytes(T, n, H, N, R, 0), workspace, x)
     _check(lib().pmoe_adapter_forward(
         _ptr(x), _ptr(ids), ids_type, T, n, H, N, R, _ptr(down), _ptr(up), _ptr(scale), _ptr(base),
         _ptr(out), _ptr(v), _ptr(ws), ws.numel(), _stream(stream, x, ids, down, up, scale, base, out, v, ws)))
@@ -732,10 +733,10 @@ def adapter_backward(dy, x, v, adapter_ids, down, up, scale, base=None, need_dx=
     if base is not None:
         base = _bf16(base, "base", (T, H))
     dx, d_down, d_up = out if out is not None else (None, None, None)
-    dx = _out(dx, "dx", torch.bfloat16, (T, H), dy.device) if need_dx else None
-    d_down = _out(d_down, "d_down", torch.float32, (n, R, H), dy.device) if need_weights else None
-    d_up = _out(d_up, "d_up", torch.float32, (n, N, R), dy.device) if need_weights else None
-    ws = _scratch(lib().pmoe_adapter_workspace_bytes(T, n, H, N, R, 1), workspace, dy.device)
+    dx = _out(dx, "dx", torch.bfloat16, (T, H), dy) if need_dx else None
+    d_down = _out(d_down, "d_down", torch.float32, (n, R, H), dy) if need_weights else None
+    d_up = _out(d_up, "d_up", torch.float32, (n, N, R), dy) if need_weights else None
+    ws = _scratch(lib().pmoe_adapter_workspace_bytes(T, n, H, N, R, 1), workspace, dy)
     _check(lib().pmoe_adapter_backward(
         _ptr(dy), _ptr(x), _ptr(v), _ptr(ids), ids_type, T, n, H, N, R, _ptr(down), _ptr(up), _ptr(scale),
         _ptr(base), _ptr(dx), _ptr(d_down), _ptr(d_up), _ptr(ws), ws.numel(),
