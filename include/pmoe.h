@@ -503,8 +503,8 @@ int pmoe_router_balance(const float* logits, const void* topk_ids, int ids_type,
  *                    every row is written. Tokens of no sequence have no part in the
  *                    losses, but may have one in d_topk_w.
  * counts is needed with d_balance, tokens with d_balance or d_z. With
- * renormalize = 1 a token whose chosen experts all have p = 0 gets no gradient
- * from d_topk_w. d_logits may be logits itself. Limits and alignment as above.
+ * renormalize = 1 a token whose chosen experts together have less than 1e-37 of
+ * the largest p gets no gradient from d_topk_w. d_logits may be logits itself. Limits and alignment as above.
  */
 int pmoe_router_backward(const float* logits, const void* topk_ids, int ids_type, int T, int K, int E,
                          int renormalize, const int32_t* seq_offsets, int S,

@@ -16,9 +16,17 @@
 // or, for the renormalized weights q_j = p_{id_j} / sum_k p_{id_k},
 //   d l_{id_j} += q_j (d w_j - sum_k d w_k q_k).
 //
-// One wavefront holds one row: lane i the logits of experts i, i + 64, ... .
+// L = 16 lanes hold one token up to E = 128 and L = 64 above: lane i the logits of
+// experts i, i + L, ..., or, where E fills them exactly, 4 i .. 4 i + 3, 4 L further,
+// ... (16 bytes a load). With 16 a wavefront works on four tokens, and what is done
+// once for a token costs a quarter of an instruction: the gradient of T = 65521
+// tokens, E = 64, takes 14.7 us a call (64 lanes: 19.8). With many experts the
+// registers of 16 lanes would leave too few wavefronts: T = 8192, E = 1024, 39 us
+// against 18.8.
 // The sums over tokens are taken in a fixed order without atomics on floats,
 // so results do not vary between runs.
+#include <algorithm>
+
 #include "device.h"
 #include "kernels.h"
 
@@ -27,33 +35,57 @@ namespace pmoe {
 typedef float floatx4_t __attribute__((ext_vector_type(4)));
 constexpr float kNegInf = -__builtin_inff();
 
-// Wave-wide sum and maximum by data-parallel-primitive moves (no LDS traffic): 1, 2, 4
-// and 8 lanes up within rows of 16, then row 0 into 1 and 2 into 3, then 1 into 3; lane
-// 63 ends with the result. A fixed order, so a fixed rounding.
+// Moves between lanes without LDS traffic (data-parallel primitives): rotations within
+// rows of 16 lanes, and, for sums over the wave, the last lanes of rows into the rows above.
 template <int kCtrl, int kRows>
 __device__ __forceinline__ float lane_move(float old, float v) {
   return __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(old), __float_as_uint(v), kCtrl, kRows, 0xf, false));
+}
+template <int kBy>
+__device__ __forceinline__ float turn16(float v) {
+  return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(v), 0x120 + kBy, 0xf, 0xf, true));
+}
+// Sum and maximum over 16 lanes, in all of them (the partial sums are the same in the lanes
+// that hold them, since an addition does not depend on its operands' order).
+__device__ __forceinline__ float sum16(float v) {
+  v += turn16<8>(v);
+  v += turn16<4>(v);
+  v += turn16<2>(v);
+  return v + turn16<1>(v);
+}
+__device__ __forceinline__ float max16(float v) {
+  v = __builtin_fmaxf(v, turn16<8>(v));
+  v = __builtin_fmaxf(v, turn16<4>(v));
+  v = __builtin_fmaxf(v, turn16<2>(v));
+  return __builtin_fmaxf(v, turn16<1>(v));
 }
 __device__ __forceinline__ float last_lane(float v) {
   return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
 }
 __device__ __forceinline__ float wave_sum_f(float v) {
-  v += lane_move<0x111, 0xf>(0.0f, v);
-  v += lane_move<0x112, 0xf>(0.0f, v);
-  v += lane_move<0x114, 0xf>(0.0f, v);
-  v += lane_move<0x118, 0xf>(0.0f, v);
+  v = sum16(v);
   v += lane_move<0x142, 0xa>(0.0f, v);
   v += lane_move<0x143, 0xc>(0.0f, v);
   return last_lane(v);
 }
 __device__ __forceinline__ float wave_max_f(float v) {
-  v = __builtin_fmaxf(v, lane_move<0x111, 0xf>(v, v));
-  v = __builtin_fmaxf(v, lane_move<0x112, 0xf>(v, v));
-  v = __builtin_fmaxf(v, lane_move<0x114, 0xf>(v, v));
-  v = __builtin_fmaxf(v, lane_move<0x118, 0xf>(v, v));
+  v = max16(v);
   v = __builtin_fmaxf(v, lane_move<0x142, 0xa>(v, v));
   v = __builtin_fmaxf(v, lane_move<0x143, 0xc>(v, v));
   return last_lane(v);
+}
+// Over the L lanes of a token, in all of them.
+template <int L>
+__device__ __forceinline__ float token_sum(float v) {
+  return L == 16 ? sum16(v) : wave_sum_f(v);
+}
+template <int L>
+__device__ __forceinline__ float token_max(float v) {
+  return L == 16 ? max16(v) : wave_max_f(v);
+}
+template <int L>
+__device__ __forceinline__ uint64_t token_ballot(bool on, int group) {
+  return L == 16 ? (__ballot(on) >> (16 * group)) & 0xFFFFull : __ballot(on);
 }
 
 // exp(x) for x <= 0 as 2^(x log2 e): the product is carried with its rounding
@@ -79,15 +111,16 @@ __device__ __forceinline__ int expert_id(const void* ids, int ids64, long i, int
   return id >= 0 && id < E ? (int)id : -1;
 }
 
-// The sequence of token t: the last s with offsets[s] <= t, -1 before the first
-// and S behind the last. Every round the 64 lanes probe 64 places of the range.
-__device__ __forceinline__ int sequence_of(const int* offsets, int S, int t, int lane) {
+// The sequence of token t (the same in L lanes): the last s with offsets[s] <= t, -1 before
+// the first and S behind the last. Every round the L lanes probe L places of the range.
+template <int L>
+__device__ __forceinline__ int sequence_of(const int* offsets, int S, int t, int group, int i) {
   if (offsets == nullptr) return 0;
   int lo = 0, n = S + 1;  // offsets[0 .. lo) <= t, offsets[lo + n ..) > t
   while (n > 0) {
-    const int step = (n + 63) >> 6;
-    const int at = lane * step;
-    const int passed = __popcll(__ballot(at < n && offsets[lo + min(at, n - 1)] <= t));
+    const int step = (n + L - 1) / L;
+    const int at = i * step;
+    const int passed = __popcll(token_ballot<L>(at < n && offsets[lo + min(at, n - 1)] <= t, group));
     if (passed == 0) return lo - 1;
     const int base = (passed - 1) * step;  // this place is <= t, the next probe is not
     const int next = min(passed * step, n);
@@ -97,7 +130,48 @@ __device__ __forceinline__ int sequence_of(const int* offsets, int S, int t, int
   return lo - 1;
 }
 
-// One row of logits in registers and what its softmax needs.
+// The expert of a lane's c-th logit. kFull: E is L NPL, and rows are aligned to 16 bytes.
+template <int L, bool kFull>
+__device__ __forceinline__ int expert_of(int i, int c) {
+  return kFull ? 4 * L * (c >> 2) + 4 * i + (c & 3) : i + L * c;
+}
+
+// What L lanes read of a token: its logits, and in lane j the ids of the slots j and j + L.
+// `first` is a token that is the same in all lanes, `by` the lane's distance to it.
+template <int L, int NPL, bool kFull>
+struct Token {
+  static constexpr int kSlots = 32 / L > 0 ? 32 / L : 1;  // K <= 32
+  float v[NPL];
+  int id[kSlots];
+  __device__ __forceinline__ void load(const float* logits, const void* ids, int ids64, long first, int by, int E,
+                                       int K, int i) {
+    const float* rows = logits + first * E;
+    const uint32_t at = (uint32_t)by * E;
+    if constexpr (kFull) {
+#pragma unroll
+      for (int c = 0; c < NPL; c += 4) {
+        const floatx4_t u = *reinterpret_cast<const floatx4_t*>(rows + (at + expert_of<L, kFull>(i, c)));
+        v[c] = u[0], v[c + 1] = u[1], v[c + 2] = u[2], v[c + 3] = u[3];
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < NPL; ++c) v[c] = i + L * c < E ? rows[at + i + L * c] : kNegInf;
+    }
+#pragma unroll
+    for (int y = 0; y < kSlots; ++y) {
+      const int j = i + L * y;
+      id[y] = j < K ? expert_id(ids, ids64, (first + by) * K + j, E) : -1;
+    }
+  }
+  __device__ __forceinline__ bool any_id(int group) const {
+    bool on = false;
+#pragma unroll
+    for (int y = 0; y < kSlots; ++y) on |= id[y] >= 0;
+    return token_ballot<L>(on, group) != 0;
+  }
+};
+
+// The softmax of a token.
 template <int NPL>
 struct Row {
   float ex[NPL];  // exp(l - m); 0 behind E
@@ -106,36 +180,34 @@ struct Row {
   __device__ __forceinline__ float lse() const { return m + logf(sum); }
 };
 
-template <int NPL>
-__device__ __forceinline__ void load_logits(const float* row, int E, int lane, float (&v)[NPL]) {
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = lane + 64 * i;
-    v[i] = e < E ? row[e] : kNegInf;
-  }
-}
-
-template <int NPL>
-__device__ __forceinline__ Row<NPL> softmax_row(const float (&v)[NPL], bool any_id) {
+template <int L, int NPL>
+__device__ __forceinline__ Row<NPL> softmax_row(const float (&v)[NPL], bool any_id, int group) {
   Row<NPL> r;
   float m = v[0];
-  bool some = !(v[0] == kNegInf);  // NaN counts: it has to come out as NaN
 #pragma unroll
-  for (int i = 1; i < NPL; ++i) {
-    some |= !(v[i] == kNegInf);
-    m = __builtin_fmaxf(m, v[i]);
+  for (int c = 1; c < NPL; ++c) m = __builtin_fmaxf(m, v[c]);
+  r.m = token_max<L>(m);
+  r.active = any_id && r.m > kNegInf;
+  if (__ballot(any_id && !r.active)) {  // rare: all -inf, or NaN among them, which has to come out as NaN
+    bool nan = false;
+#pragma unroll
+    for (int c = 0; c < NPL; ++c) nan |= v[c] != v[c];
+    r.active = any_id && (r.m > kNegInf || token_ballot<L>(nan, group) != 0);
   }
-  r.m = wave_max_f(m);
-  r.active = any_id && __ballot(some) != 0;
   if (!r.active) r.m = 0.0f;
   float part = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    r.ex[i] = exp_neg(v[i] - r.m);
-    part += r.ex[i];
+  for (int c = 0; c < NPL; ++c) {
+    r.ex[c] = exp_neg(v[c] - r.m);
+    part += r.ex[c];
   }
-  r.sum = wave_sum_f(part);
-  r.inv = r.active ? recip(r.sum) : 0.0f;
+  r.sum = token_sum<L>(part);
+  r.inv = recip(r.sum);
+  if (__ballot(!r.active)) {  // whatever stands in a padding token stays out of every sum
+#pragma unroll
+    for (int c = 0; c < NPL; ++c) r.ex[c] = r.active ? r.ex[c] : 0.0f;
+    r.inv = r.active ? r.inv : 0.0f;
+  }
   return r;
 }
 
@@ -169,29 +241,31 @@ __device__ __forceinline__ void write_sequence(const BalanceParams& p, int s, co
   }
 }
 
-// Workgroup c (16 waves, a row per wave at a time) takes the tokens [c * rows,
+// Workgroup c (8 waves, 8 or 32 tokens at a time) takes the tokens [c * rows,
 // (c + 1) * rows) and writes, for every sequence s that has tokens there, the
 // slot c + s. Along the tokens either c or s grows from one (c, s) to the
 // next, so the slot numbers differ; there are chunks + S of them at most. With
 // kDirect there is one workgroup and one sequence, and it writes the results.
-template <int NPL, bool kDirect>
-__global__ __launch_bounds__(1024) void balance_rows_kernel(BalanceParams p, int rows) {
-  __shared__ float prob[16][64 * NPL];
-  __shared__ int count[64 * NPL];
-  __shared__ float zsum[16];
-  __shared__ int nact[16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+constexpr int kRowWaves = 8;
+template <int L, int NPL, bool kFull, bool kDirect>
+__global__ __launch_bounds__(64 * kRowWaves) void balance_rows_kernel(BalanceParams p, int rows) {
+  constexpr int kThreads = 64 * kRowWaves, G = 64 / L;  // G tokens to a wave
+  __shared__ float prob[kRowWaves][L * NPL];
+  __shared__ int count[L * NPL];
+  __shared__ float zsum[16];  // also write_sequence's
+  __shared__ int nact[kRowWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, group = lane / L, i = lane % L;
   const int T = p.T, E = p.E, K = p.K;
   const int* offsets = p.offsets;
   const int begin = blockIdx.x * rows, end = min(T, begin + rows);
   int t0 = begin;
   if (kDirect && offsets) t0 = min(max(offsets[0], 0), end);
-  while (kDirect || t0 < end) {  // uniform: every wave sees the same offsets
+  while (kDirect || t0 < end) {  // uniform: every lane sees the same offsets
     int s = 0, t1 = end;
     if (kDirect) {
       if (offsets) t1 = min(max(offsets[1], t0), end);
     } else {
-      s = sequence_of(offsets, p.S, t0, lane);
+      s = sequence_of<L>(offsets, p.S, t0, group, i);
       if (s >= p.S) break;
       if (s < 0) {
         t0 = min(end, max(offsets[0], t0 + 1));
@@ -199,43 +273,56 @@ __global__ __launch_bounds__(1024) void balance_rows_kernel(BalanceParams p, int
       }
       if (offsets) t1 = min(end, max(offsets[s + 1], t0 + 1));
     }
-    for (int e = threadIdx.x; e < 64 * NPL; e += 1024) count[e] = 0;
+    for (int e = threadIdx.x; e < L * NPL; e += kThreads) count[e] = 0;
     __syncthreads();
     float sum[NPL];
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) sum[i] = 0.0f;
+    for (int c = 0; c < NPL; ++c) sum[c] = 0.0f;
     float z = 0.0f;
     int n = 0;
-    for (int t = t0 + wave; t < t1; t += 16) {
-      float v[NPL];
-      load_logits<NPL>(p.logits + (long)t * E, E, lane, v);
-      const int id = lane < K ? expert_id(p.ids, p.ids64, (long)t * K + lane, E) : -1;
-      const Row<NPL> r = softmax_row<NPL>(v, __ballot(id >= 0) != 0);
+    for (int t = t0 + G * wave; t < t1; t += G * kRowWaves) {
+      const bool on = t + group < t1;
+      Token<L, NPL, kFull> now;
+      now.load(p.logits, p.ids, p.ids64, t, on ? group : 0, E, K, i);
+      const Row<NPL> r = softmax_row<L, NPL>(now.v, now.any_id(group) && on, group);
       if (r.active) {
-        if (id >= 0) atomicAdd(&count[id], 1);
+#pragma unroll
+        for (int y = 0; y < now.kSlots; ++y)
+          if (now.id[y] >= 0) atomicAdd(&count[now.id[y]], 1);
         const float lse = r.lse();
         n += 1;
         z += lse * lse;
       }
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) sum[i] = __builtin_fmaf(r.ex[i], r.inv, sum[i]);
+      for (int c = 0; c < NPL; ++c) sum[c] = __builtin_fmaf(r.ex[c], r.inv, sum[c]);
     }
+    // the tokens of a wave, then the waves in order
+    const auto over_tokens = [](auto v) {
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) prob[wave][lane + 64 * i] = sum[i];
+      for (int d = L; d < 64; d *= 2) v += __shfl_xor(v, d, 64);
+      return v;
+    };
+#pragma unroll
+    for (int c = 0; c < NPL; ++c) {
+      const float v = over_tokens(sum[c]);
+      if (group == 0) prob[wave][expert_of<L, kFull>(i, c)] = v;
+    }
+    z = over_tokens(z);
+    n = over_tokens(n);
     if (lane == 0) {
       zsum[wave] = z;
       nact[wave] = n;
     }
     __syncthreads();
-    const int used = min(16, t1 - t0);  // waves that had a row, in wave order
-    for (int e = threadIdx.x; e < E; e += 1024) {
+    const int used = min(kRowWaves, (t1 - t0 + G - 1) / G);  // waves that had a token
+    for (int e = threadIdx.x; e < E; e += kThreads) {
       float q = prob[0][e];
       for (int w = 1; w < used; ++w) q += prob[w][e];
       prob[0][e] = q;
     }
     float zs = 0.0f;
     int ns = 0;
-    for (int w = 0; w < 16; ++w) {
+    for (int w = 0; w < kRowWaves; ++w) {
       zs += zsum[w];
       ns += nact[w];
     }
@@ -246,7 +333,7 @@ __global__ __launch_bounds__(1024) void balance_rows_kernel(BalanceParams p, int
     }
     const int E4 = balance_e4(E);
     float* slot = static_cast<float*>(p.ws) + (blockIdx.x + s) * balance_slot_words(E);
-    for (int e = threadIdx.x; e < E; e += 1024) {
+    for (int e = threadIdx.x; e < E; e += kThreads) {
       slot[e] = prob[0][e];
       reinterpret_cast<int*>(slot)[E4 + e] = count[e];
     }
@@ -341,35 +428,43 @@ size_t balance_ws_bytes(int T, int E, int S) {
   return ((size_t)(T + rows - 1) / rows + S) * balance_slot_words(E) * 4;
 }
 
-#define PMOE_BY_LOGITS(E, call)          \
-  do {                                   \
-    if ((E) <= 64) {                     \
-      constexpr int NPL = 1;             \
-      call;                              \
-    } else if ((E) <= 128) {             \
-      constexpr int NPL = 2;             \
-      call;                              \
-    } else if ((E) <= 256) {             \
-      constexpr int NPL = 4;             \
-      call;                              \
-    } else if ((E) <= 512) {             \
-      constexpr int NPL = 8;             \
-      call;                              \
-    } else {                             \
-      constexpr int NPL = 16;            \
-      call;                              \
-    }                                    \
+#define PMOE_BY_LOGITS2(E, l, npl, call)    \
+  do {                                      \
+    constexpr int L = l, NPL = npl;         \
+    if ((E) == L * NPL && aligned) {        \
+      constexpr bool kFull = true;          \
+      call;                                 \
+    } else {                                \
+      constexpr bool kFull = false;         \
+      call;                                 \
+    }                                       \
+  } while (0)
+#define PMOE_BY_LOGITS(E, call)             \
+  do {                                      \
+    if ((E) <= 64)                          \
+      PMOE_BY_LOGITS2(E, 16, 4, call);      \
+    else if ((E) <= 128)                    \
+      PMOE_BY_LOGITS2(E, 16, 8, call);      \
+    else if ((E) <= 256)                    \
+      PMOE_BY_LOGITS2(E, 64, 4, call);      \
+    else if ((E) <= 512)                    \
+      PMOE_BY_LOGITS2(E, 64, 8, call);      \
+    else                                    \
+      PMOE_BY_LOGITS2(E, 64, 16, call);     \
   } while (0)
 
+static bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
 hipError_t launch_router_balance(const BalanceParams& p, hipStream_t s) {
+  const bool aligned = aligned16(p.logits);
   if (p.S == 1 && p.T <= kDirectTokens) {
-    PMOE_BY_LOGITS(p.E, (balance_rows_kernel<NPL, true><<<1, 1024, 0, s>>>(p, p.T)));
+    PMOE_BY_LOGITS(p.E, (balance_rows_kernel<L, NPL, kFull, true><<<1, 64 * kRowWaves, 0, s>>>(p, p.T)));
     return hipGetLastError();
   }
   const int rows = balance_rows(p.T, p.S);
   if (p.T > 0) {
     const int chunks = (p.T + rows - 1) / rows;
-    PMOE_BY_LOGITS(p.E, (balance_rows_kernel<NPL, false><<<chunks, 1024, 0, s>>>(p, rows)));
+    PMOE_BY_LOGITS(p.E, (balance_rows_kernel<L, NPL, kFull, false><<<chunks, 64 * kRowWaves, 0, s>>>(p, rows)));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -381,107 +476,127 @@ hipError_t launch_router_balance(const BalanceParams& p, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------- backward
-// A wave takes `rows` consecutive tokens and keeps the expert shares f of their
-// sequence in registers while it stays the same; the next row's logits are on
-// their way while one is worked on. With
-//   u_e = d_balance E / n_s f_se + sum_{j: id_j = e} d w_j
-// the terms that are not renormalized are p_e (u_e - sum p u + 2 d_z / n_s lse).
-// The d w_j reach the lanes of their experts through a row of LDS that is zero
-// between tokens.
-template <int NPL>
+// A wave takes `rows` tokens for each of its G = 64 / L groups of lanes, G at a time, and the
+// groups keep the expert shares f of their sequence in registers while it stays the same; the next token is on its way while one is worked on.
+// With u_e = d_balance E / n_s f_se and a_j what the slots add at their experts,
+//   d l_e = p_e (u_e - mean + 2 d_z / n_s lse) + sum_{j: id_j = e} a_j,
+//   mean = sum_e u_e p_e + sum_j d w_j p_{id_j},  a_j = p_{id_j} d w_j,
+// or for renormalized weights mean = sum_e u_e p_e, a_j = q_j (d w_j - sum_k d w_k q_k).
+// The slots' logits are read once more, by the lanes of the slots; the a_j reach the lanes of
+// their experts through a row of LDS that is zero between tokens.
+template <int L, int NPL, bool kFull>
 __global__ __launch_bounds__(256) void router_grad_kernel(RouterGradParams p, int rows) {
-  __shared__ float direct_sh[4][64 * NPL];
-  __shared__ float times_sh[4][64 * NPL];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int t0 = (blockIdx.x * 4 + wave) * rows, t1 = min(p.T, t0 + rows);
+  constexpr int G = 64 / L, kSlots = Token<L, NPL, kFull>::kSlots;
+  __shared__ float add_sh[4 * G][L * NPL];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, group = lane / L, i = lane % L;
   const int E = p.E, K = p.K;
-  float* direct = direct_sh[wave];  // used by this wave alone: its LDS operations stay in order
-  float* times = times_sh[wave];
+  const long first = (long)(blockIdx.x * 4 + wave) * G * rows;  // the wave's tokens
+  const int n = (int)max(0l, min((long)G * rows, p.T - first));
+  float* add = add_sh[wave * G + group];  // these L lanes' alone: a wave's LDS operations stay in order
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) direct[lane + 64 * i] = times[lane + 64 * i] = 0.0f;
+  for (int c = 0; c < NPL; ++c) add[i + L * c] = 0.0f;
   float share[NPL];  // d_balance E / n_s f_se
   float cz = 0.0f;   // 2 d_z / n_s
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) share[i] = 0.0f;
-  float next[NPL];
-  if (t0 < t1) load_logits<NPL>(p.logits + (long)t0 * E, E, lane, next);
+  for (int c = 0; c < NPL; ++c) share[c] = 0.0f;
   const bool losses = p.tokens != nullptr;
-  int seq_end = t0;  // the sequence in `share` holds the tokens up to here
-  for (int t = t0; t < t1; ++t) {
-    float v[NPL];
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) v[i] = next[i];
-    const int id = lane < K ? expert_id(p.ids, p.ids64, (long)t * K + lane, E) : -1;
-    const float dw = p.d_topk_w && id >= 0 ? p.d_topk_w[(long)t * K + lane] : 0.0f;
-    if (t + 1 < t1) load_logits<NPL>(p.logits + (long)(t + 1) * E, E, lane, next);
-    if (losses && t >= seq_end) {
-      const int s = sequence_of(p.offsets, p.S, t, lane);
-      const bool in = s >= 0 && s < p.S;  // else the losses do not see the token
-      seq_end = in && p.offsets ? max(p.offsets[s + 1], t + 1) : (p.offsets ? t + 1 : p.T);
-      const float n = in ? (float)max(p.tokens[s], 1) : 1.0f;
-      cz = in && p.d_z ? 2.0f * p.d_z[s] / n : 0.0f;
-      const float cb = in && p.d_balance ? p.d_balance[s] * ((float)E / (n * n * (float)K)) : 0.0f;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const int e = lane + 64 * i;
-        share[i] = in && p.d_balance && e < E ? cb * (float)p.counts[(long)s * E + e] : 0.0f;
-      }
-    }
-    const Row<NPL> r = softmax_row<NPL>(v, __ballot(id >= 0) != 0);
-    float* out = p.d_logits + (long)t * E;
-    if (!r.active) {
-#pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (lane + 64 * i < E) out[lane + 64 * i] = 0.0f;
-      continue;
-    }
-    float u[NPL], top[NPL];  // top: the renormalized part of the gradient
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      u[i] = share[i];
-      top[i] = 0.0f;
-    }
+  long seq_end = 0;  // the sequence in `share` holds the tokens up to here
+  Token<L, NPL, kFull> next;
+  // lanes without a token look at group 0's
+  if (n > 0) next.load(p.logits, p.ids, p.ids64, first, group < n ? group : 0, E, K, i);
+  for (int y = 0; y < n; y += G) {
+    const bool on = y + group < n;
+    const int by = on ? y + group : y;
+    const long t = first + by;
+    const Token<L, NPL, kFull> now = next;
+    if (y + G < n) next.load(p.logits, p.ids, p.ids64, first, y + G + group < n ? y + G + group : y + G, E, K, i);
+    float dw[kSlots] = {}, slot[kSlots] = {};  // of the lane's slots: gradient, logit
     if (p.d_topk_w) {
-      if (id >= 0) atomicAdd(&direct[id], dw);
-      if (id >= 0 && p.renorm) atomicAdd(&times[id], 1.0f);  // slots of the expert
-      __builtin_amdgcn_wave_barrier();
-      if (p.renorm) {
-        float den = 0.0f, num = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-          den = __builtin_fmaf(times[lane + 64 * i], r.ex[i], den);
-          num = __builtin_fmaf(direct[lane + 64 * i], r.ex[i], num);
+      for (int h = 0; h < kSlots; ++h)
+        if (now.id[h] >= 0) {
+          dw[h] = p.d_topk_w[t * K + i + L * h];
+          slot[h] = p.logits[t * E + now.id[h]];
         }
-        den = wave_sum_f(den);
-        num = wave_sum_f(num);
-        const float inv = den > 0.0f ? recip(den) : 0.0f;
-        const float mean = num * inv;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i)
-          top[i] = r.ex[i] * inv * (direct[lane + 64 * i] - times[lane + 64 * i] * mean);
-      } else {
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) u[i] += direct[lane + 64 * i];
-      }
-      __builtin_amdgcn_wave_barrier();
-      if (id >= 0) direct[id] = times[id] = 0.0f;
     }
+    if (losses && on && t >= seq_end) {
+      const int s = sequence_of<L>(p.offsets, p.S, (int)t, group, i);
+      const bool in = s >= 0 && s < p.S;  // else the losses do not see the token
+      seq_end = p.offsets ? (in ? max((long)p.offsets[s + 1], t + 1) : t + 1) : p.T;
+      const float n_s = in ? (float)max(p.tokens[s], 1) : 1.0f;
+      cz = in && p.d_z ? 2.0f * p.d_z[s] / n_s : 0.0f;
+      const float cb = in && p.d_balance ? p.d_balance[s] * ((float)E / (n_s * n_s * (float)K)) : 0.0f;
+#pragma unroll
+      for (int c = 0; c < NPL; ++c) {
+        const int e = expert_of<L, kFull>(i, c);
+        share[c] = in && p.d_balance && (kFull || e < E) ? cb * (float)p.counts[(long)s * E + e] : 0.0f;
+      }
+    }
+    const Row<NPL> r = softmax_row<L, NPL>(now.v, now.any_id(group), group);
     float mean = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) mean = __builtin_fmaf(u[i], r.ex[i], mean);
-    mean = wave_sum_f(mean) * r.inv;
-    const float zt = losses && p.d_z ? cz * r.lse() : 0.0f;
+    for (int c = 0; c < NPL; ++c) mean = __builtin_fmaf(share[c], r.ex[c], mean);
+    mean = token_sum<L>(mean) * r.inv;
+    if (p.d_topk_w) {
+      float ps[kSlots], weight = 0.0f, dot = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      if (lane + 64 * i < E)
-        out[lane + 64 * i] = __builtin_fmaf(r.ex[i] * r.inv, (u[i] - mean) + zt, top[i]);
+      for (int h = 0; h < kSlots; ++h) {
+        ps[h] = now.id[h] >= 0 ? exp_neg(slot[h] - r.m) : 0.0f;
+        weight += ps[h];
+        dot = __builtin_fmaf(ps[h], dw[h], dot);
+      }
+      float inv = r.inv;
+      if (p.renorm) {
+        const float den = token_sum<L>(weight);
+        inv = den < 1e-37f ? 0.0f : recip(den);  // NaN stays
+      }
+      dot = token_sum<L>(dot) * inv;
+      if (!p.renorm) mean += dot;
+      const float minus = p.renorm ? dot : 0.0f;
+#pragma unroll
+      for (int h = 0; h < kSlots; ++h)
+        if (r.active && now.id[h] >= 0) atomicAdd(&add[now.id[h]], ps[h] * inv * (dw[h] - minus));
+      __builtin_amdgcn_wave_barrier();
+    }
+    const float shift = losses && p.d_z ? (r.active ? cz * r.lse() : 0.0f) - mean : -mean;
+    if (on) {
+      float* rows_out = p.d_logits + first * E;
+      const uint32_t at = (uint32_t)by * E;
+      float out[NPL];
+#pragma unroll
+      for (int c = 0; c < NPL; ++c) {
+        const float a = p.d_topk_w ? add[expert_of<L, kFull>(i, c)] : 0.0f;
+        const float v = __builtin_fmaf(r.ex[c] * r.inv, share[c] + shift, a);
+        out[c] = r.active ? v : 0.0f;
+      }
+      if constexpr (kFull) {
+#pragma unroll
+        for (int c = 0; c < NPL; c += 4)
+          *reinterpret_cast<floatx4_t*>(rows_out + (at + expert_of<L, kFull>(i, c))) =
+              floatx4_t{out[c], out[c + 1], out[c + 2], out[c + 3]};
+      } else {
+#pragma unroll
+        for (int c = 0; c < NPL; ++c)
+          if (i + L * c < E) rows_out[at + i + L * c] = out[c];
+      }
+    }
+    if (p.d_topk_w) {
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int h = 0; h < kSlots; ++h)
+        if (now.id[h] >= 0) add[now.id[h]] = 0.0f;
+    }
   }
 }
 
 hipError_t launch_router_backward(const RouterGradParams& p, hipStream_t s) {
-  const int rows = p.T >= 32768 ? 4 : 1;
-  const int grid = (p.T + 4 * rows - 1) / (4 * rows);
-  PMOE_BY_LOGITS(p.E, (router_grad_kernel<NPL><<<grid, 256, 0, s>>>(p, rows)));
+  // Up to four tokens to a group of lanes, which pays for its start, where that still leaves
+  // sixteen waves for each CU.
+  const int tokens = 4 * (p.E <= 128 ? 4 : 1);  // of a workgroup at a time
+  const int rows = std::max(1, std::min(4, p.T / (1024 * tokens)));
+  const int grid = (p.T + tokens * rows - 1) / (tokens * rows);
+  const bool aligned = aligned16(p.logits) && aligned16(p.d_logits);
+  PMOE_BY_LOGITS(p.E, (router_grad_kernel<L, NPL, kFull><<<grid, 256, 0, s>>>(p, rows)));
   return hipGetLastError();
 }
 

@@ -150,6 +150,26 @@ def test_lowest_values_and_nan(pm):
         assert torch.equal(g[rest], clean[rest])
 
 
+@pytest.mark.parametrize("E", [5, 64, 200, 1024])
+def test_padding_tokens_may_hold_anything(pm, E):
+    """Logits of tokens without a valid id do not reach any result, whatever they are."""
+    import torch
+    rng, logits, ids, off = _case(29, 150, E, 3, 4)
+    pad = rng.random(150) < 0.3
+    ids[pad] = -1
+    zero, wild = logits.copy(), logits.copy()
+    zero[pad] = 0.0
+    wild[pad] = rng.choice(np.array([np.nan, np.inf, -np.inf, 3e38, 700.0], F32), (int(pad.sum()), E))
+    dw = dev(rng.standard_normal(ids.shape).astype(F32))
+    a, b = pm.router_balance(*_args(zero, ids, off)), pm.router_balance(*_args(wild, ids, off))
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    one = torch.ones(4, device="cuda")
+    for renorm in (False, True):
+        g, h = (pm.router_backward(dev(l), dev(ids), counts=a.counts, tokens=a.tokens, d_balance=one, d_z=one,
+                                   d_topk_w=dw, renormalize=renorm, seq_offsets=dev(off)) for l in (zero, wild))
+        assert torch.equal(g, h) and not g[dev(pad)].any()
+
+
 def test_int64_ids_repeats_views_and_empty_batch(pm):
     import torch
     _, logits, ids, off = _case(13, 333, 100, 5, 6, pad=True)
