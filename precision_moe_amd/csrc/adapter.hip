@@ -852,7 +852,7 @@ __device__ __forceinline__ void grad_body(const GradParams& p, GradLds& lds) {
 }
 
 template <int NR>
-__global__ __launch_bounds__(256, 2) void adapter_grad_kernel(GradParams p) {
+__global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void adapter_grad_kernel(GradParams p) {
   __shared__ __align__(16) GradLds lds;
   if (grad_down(p, 128))
     grad_body<NR, true>(p, lds);
@@ -1032,14 +1032,16 @@ struct AdapterLayout {
 }  // namespace
 
 // Groups of windows and shares of a window: as many as it takes to fill the GPU where few
-// adapters make few workgroups.
+// adapters make few workgroups. More workgroups cost more than they bring, for each has to list
+// its tokens and leaves sums to be added: T = 4096, n = 4, H = N = 7168 took 88 us a call with 256
+// and 104 with 1024 wanted (R = 32), 125 with 512, 130 with 768 and 132 with 256 (R = 64).
 struct GradSplit {
   int groups, shares;
 };
 static GradSplit grad_split(int T, int n, int H, int N, int R) {
   const int cols = grad_cols(R), windows = grad_windows(T);
   const long each = (long)n * ((H + cols - 1) / cols + (N + cols - 1) / cols) * (R > 64 ? 2 : 1);
-  const int want = (int)(((R <= 32 ? 1024 : 768) + each - 1) / each);
+  const int want = (int)(((R <= 32 ? 256 : 512) + each - 1) / each);
   GradSplit g;
   g.groups = windows < want ? windows : want;
   g.shares = (want + g.groups - 1) / g.groups;
