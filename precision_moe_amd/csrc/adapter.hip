@@ -25,7 +25,10 @@
 // l % 16 and the eight k of group l / 16; the result lane holds column l % 16
 // and rows 4 (l / 16) + 0..3). FP32 factors (v, du) enter as sums of BF16
 // values: two (16 significant bits) where the result is rounded to BF16 (8
-// bits), three (24 bits, all of FP32) where it stays FP32.
+// bits), three where it stays FP32, which holds all 24 bits of an FP32 value.
+//
+// The time of a call is that of its passes over the rows: two forward, four backward (reduction,
+// expansion, gradients, and the sum of the gradients' shares). Small calls cost their launches.
 #include "device.h"
 #include "kernels.h"
 
@@ -36,7 +39,9 @@ typedef float floatx4 __attribute__((ext_vector_type(4)));
 constexpr int kUnit = 64;    // tokens of one unit at most
 constexpr int kSpan = 1024;  // tokens that are grouped together
 constexpr int kNone = -1;  // adapter of a unit of tokens without one
-constexpr int kMostRuns = 16;  // boundaries up to which a span is not sorted
+// Boundaries up to which a span is not sorted. Sorting costs 1 us; units of single tokens cost
+// more: n = 12 adapters over T = 128 tokens in mixed order take 15.8 us a call, unsorted 50.
+constexpr int kMostRuns = 16;
 
 __device__ __forceinline__ floatx4 mfma16(bf16x8_t a, bf16x8_t b, floatx4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -309,6 +314,11 @@ struct Block16 {
 // workgroups that take its units (with R > 64 its half units) in turn.
 // Operand row i of block b is r = NR i + b, so that a lane ends with 4 NR consecutive r of
 // one token, and with kTrans a lane reads NR neighbouring columns of eight rows.
+// Bound by the latency of the rows' loads: T = 8192, n = 6, H = 7168, R = 16 takes 33 us, 117 MB
+// at 3.6 TB/s. Parts of 1024 instead of 2048 elements group every span twice as often and were
+// slower. Many adapters in mixed order (T = 8192, n = 64, R = 64) read each matrix once a span,
+// 0.5 GB a call in all kernels; a grid that puts the spans of one part side by side makes that
+// call faster (255 -> 230 us) and the one above slower (83 -> 89).
 template <int NR, bool kTrans>
 __global__ __launch_bounds__(kReduceThreads, NR <= 2 ? 4 : 2) void adapter_reduce_kernel(
     const uint16_t* __restrict__ in, const void* __restrict__ ids, int ids64, int T, int n, int D, int R,
@@ -461,6 +471,8 @@ __device__ __forceinline__ void store16(uint16_t* out, uint32_t offset, bool fir
 // columns 8 g .. 8 g + 7 and 32 further of one token, so that four lanes read and write 64
 // bytes at a stretch. With kTrans W_a has its columns contiguous while an operand wants eight
 // r of one column: a lane reads four columns of eight rows and turns them in registers.
+// Bound by HBM: T = 8192, n = 6, N = 7168, R = 16 takes 50 us, 235 MB at 4.7 TB/s. Fetching the
+// next unit's rows ahead halved the waves that fit, and lost.
 template <int NR, bool kTrans>
 __global__ __launch_bounds__(256) void adapter_expand_kernel(
     const float* __restrict__ part, int parts, const SpanOrder* __restrict__ orders, int share, int T,
@@ -768,7 +780,8 @@ __device__ __forceinline__ void grad_low(const GradBlock<kDown>& q, int R, const
 // The gradients for R <= 32, 128 columns and all r to a workgroup of four waves, which take
 // every fourth step of 32 tokens, the rows of the next step on their way during one. k is the
 // token here, so both operands are wanted with eight tokens of one column: x (dy) is turned in
-// registers, du (s v) is read column by column.
+// registers, du (s v) is read column by column. Bound by the latency of that chain of list, rows
+// and du: T = 1100, n = 6, H = 2064, N = 2688, R = 8 takes 11 us, where 11 MB are to be read.
 struct GradLds {
   int list[kWindow + 64];
   int wave_count[4];
@@ -865,7 +878,11 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void adapter_grad_kernel(Grad
 // 32 tokens, four of the odd ones. The three operands of du (s v), the same for all columns,
 // are made once for the four: each wave reads and splits 16 of the 64 r and leaves them in
 // LDS, in two buffers, so that one barrier a step is enough; it waits for LDS alone, the
-// loads of the next step stay in flight.
+// loads of the next step stay in flight. T = 4096, n = 4, H = N = 7168, R = 64 takes 50 us:
+// 22.5 GFLOP, three products to a factor, at 450 TFLOP/s (a large product: 1200), and 117 MB at
+// 2.3 TB/s; each wave waits for its own loads in turn with its products.
+// R = 17 .. 32 leaves half of its rows empty: T = 4096, n = 4, H = N = 7168, R = 32 takes 101 us a
+// call with it and 88 with the kernel above.
 struct GradWideLds {
   int list[kWindow + 64];
   int wave_count[8];

@@ -246,6 +246,8 @@ __device__ __forceinline__ void write_sequence(const BalanceParams& p, int s, co
 // slot c + s. Along the tokens either c or s grows from one (c, s) to the
 // next, so the slot numbers differ; there are chunks + S of them at most. With
 // kDirect there is one workgroup and one sequence, and it writes the results.
+// Bound by latency more than by bytes: T = 32749, E = 96, K = 6, S = 61 reads 13.4 MB in 21 us a
+// call, most of it the two launches; T = 65536, E = 256, S = 200 reads 69 MB in 26.
 constexpr int kRowWaves = 8;
 template <int L, int NPL, bool kFull, bool kDirect>
 __global__ __launch_bounds__(64 * kRowWaves) void balance_rows_kernel(BalanceParams p, int rows) {
@@ -412,19 +414,25 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(BalanceParams p, int 
   write_sequence(p, s, prob, count, zs, ns, zsh);
 }
 
-// Up to this many tokens of one sequence go through one workgroup, in one launch.
-constexpr int kDirectTokens = 128;
+// Up to this many tokens of one sequence go through one workgroup, in one launch: 16 times as
+// many as it works on at a time. T = 512, E = 64 takes 16.2 us a call so and 18.3 in two launches,
+// T = 256, E = 256 21.7 and 18.3.
+static int direct_tokens(int E) { return E <= 128 ? 512 : 128; }
 
-// Tokens of one workgroup: the square root of a sequence's mean length, so
-// that the tokens of a workgroup and the slots of a sequence grow alike.
-int balance_rows(int T, int S) {
+// Tokens of one workgroup: the square root of a sequence's mean length, so that the tokens of a
+// workgroup and the slots of a sequence grow alike; with short sequences more, up to what the
+// workgroup's waves take at a time, as long as that stays within half the mean length (T = 65536,
+// E = 64, S = 2000: 41.9 us a call, without 65; with all of the mean length T = 4096, S = 200
+// takes 22.1 instead of 18.9, for then most workgroups walk through two sequences).
+int balance_rows(int T, int E, int S) {
+  const int wide = kRowWaves * (E <= 128 ? 4 : 1);
   int rows = 4;
-  while ((long)rows * rows * S < T) rows *= 2;
+  while ((long)rows * rows * S < T || (rows < wide && 2l * rows * S < T)) rows *= 2;
   return rows;
 }
 
 size_t balance_ws_bytes(int T, int E, int S) {
-  const int rows = balance_rows(T, S);
+  const int rows = balance_rows(T, E, S);
   return ((size_t)(T + rows - 1) / rows + S) * balance_slot_words(E) * 4;
 }
 
@@ -457,17 +465,19 @@ static bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 1
 
 hipError_t launch_router_balance(const BalanceParams& p, hipStream_t s) {
   const bool aligned = aligned16(p.logits);
-  if (p.S == 1 && p.T <= kDirectTokens) {
+  if (p.S == 1 && p.T <= direct_tokens(p.E)) {
     PMOE_BY_LOGITS(p.E, (balance_rows_kernel<L, NPL, kFull, true><<<1, 64 * kRowWaves, 0, s>>>(p, p.T)));
     return hipGetLastError();
   }
-  const int rows = balance_rows(p.T, p.S);
+  const int rows = balance_rows(p.T, p.E, p.S);
   if (p.T > 0) {
     const int chunks = (p.T + rows - 1) / rows;
     PMOE_BY_LOGITS(p.E, (balance_rows_kernel<L, NPL, kFull, false><<<chunks, 64 * kRowWaves, 0, s>>>(p, rows)));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
+  // With more sequences than CUs, small workgroups: T = 65536, E = 64, S = 2000 took 65 us a call
+  // so and 75 with 1024 threads, with S = 200, E = 256 25.9 with 1024 and 27.3 with 256.
   int quads = 16;
   while (quads < balance_e4(p.E) / 2) quads *= 2;
   const int threads = p.S <= 256 ? 1024 : (quads < 256 ? 256 : quads);
@@ -477,13 +487,17 @@ hipError_t launch_router_balance(const BalanceParams& p, hipStream_t s) {
 
 // ---------------------------------------------------------------- backward
 // A wave takes `rows` tokens for each of its G = 64 / L groups of lanes, G at a time, and the
-// groups keep the expert shares f of their sequence in registers while it stays the same; the next token is on its way while one is worked on.
+// groups keep the expert shares f of their sequence in registers while it stays the same; the
+// next token is on its way while one is worked on.
 // With u_e = d_balance E / n_s f_se and a_j what the slots add at their experts,
 //   d l_e = p_e (u_e - mean + 2 d_z / n_s lse) + sum_{j: id_j = e} a_j,
 //   mean = sum_e u_e p_e + sum_j d w_j p_{id_j},  a_j = p_{id_j} d w_j,
 // or for renormalized weights mean = sum_e u_e p_e, a_j = q_j (d w_j - sum_k d w_k q_k).
 // The slots' logits are read once more, by the lanes of the slots; the a_j reach the lanes of
 // their experts through a row of LDS that is zero between tokens.
+// The logits are read once and the gradient written once, which bounds it for long batches:
+// T = 65521, E = 256, K = 8 takes 37 us a call, 138 MB at 3.7 TB/s (a large copy: 5.1). Two
+// tokens in flight, or eight rows to a wave, took 42: fewer waves fit.
 template <int L, int NPL, bool kFull>
 __global__ __launch_bounds__(256) void router_grad_kernel(RouterGradParams p, int rows) {
   constexpr int G = 64 / L, kSlots = Token<L, NPL, kFull>::kSlots;
