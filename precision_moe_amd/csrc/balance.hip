@@ -424,10 +424,11 @@ static int direct_tokens(int E) { return E <= 128 ? 512 : 128; }
 // workgroup's waves take at a time, as long as that stays within half the mean length (T = 65536,
 // E = 64, S = 2000: 41.9 us a call, without 65; with all of the mean length T = 4096, S = 200
 // takes 22.1 instead of 18.9, for then most workgroups walk through two sequences).
+constexpr int kMostGroups = 1 << 22;  // a launch has less than 2^32 threads
 int balance_rows(int T, int E, int S) {
   const int wide = kRowWaves * (E <= 128 ? 4 : 1);
   int rows = 4;
-  while ((long)rows * rows * S < T || (rows < wide && 2l * rows * S < T)) rows *= 2;
+  while ((long)rows * rows * S < T || (rows < wide && 2l * rows * S < T) || T / rows >= kMostGroups) rows *= 2;
   return rows;
 }
 
@@ -607,7 +608,7 @@ hipError_t launch_router_backward(const RouterGradParams& p, hipStream_t s) {
   // Up to four tokens to a group of lanes, which pays for its start, where that still leaves
   // sixteen waves for each CU.
   const int tokens = 4 * (p.E <= 128 ? 4 : 1);  // of a workgroup at a time
-  const int rows = std::max(1, std::min(4, p.T / (1024 * tokens)));
+  const int rows = std::max({1, std::min(4, p.T / (1024 * tokens)), p.T / tokens / kMostGroups + 1});
   const int grid = (p.T + tokens * rows - 1) / (tokens * rows);
   const bool aligned = aligned16(p.logits) && aligned16(p.d_logits);
   PMOE_BY_LOGITS(p.E, (router_grad_kernel<L, NPL, kFull><<<grid, 256, 0, s>>>(p, rows)));

@@ -57,44 +57,46 @@ hipError_t launch_finalize(const uint16_t* z, const int* row_of_route, const flo
 // z, so the kernel is bound by reading z and writing d z. One workgroup per
 // token with one wave per slot (at most 16 waves, which then take several
 // slots): the waves read the same dout row, which stays in the CU's cache.
+// T = 4096, K = 8, H = 7168 takes 201 us: 999 MB at 5.0 TB/s, the rate of a large copy.
 __global__ __launch_bounds__(1024) void finalize_backward_kernel(
     const uint16_t* __restrict__ dout, const uint16_t* __restrict__ z,
-    const int* __restrict__ row_of_route, const float* __restrict__ w, int K, int H, int R,
+    const int* __restrict__ row_of_route, const float* __restrict__ w, int T, int K, int H, int R,
     float* __restrict__ d_w, uint16_t* __restrict__ d_z) {
-  const long t = blockIdx.x;
   const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-  const uint16_t* d = dout + t * H;
-  for (int j = threadIdx.x >> 6; j < K; j += waves) {
-    const int r = row_of_route[t * K + j];
-    const bool valid = r >= 0 && r < R;
-    float acc = 0.0f;
-    if (valid) {
-      const float wt = d_z ? w[t * K + j] : 0.0f;
-      for (int col = lane * 8; col < H; col += 512) {
-        const uint4 u = *reinterpret_cast<const uint4*>(d + col);
-        const uint32_t dv[4] = {u.x, u.y, u.z, u.w};
-        if (d_w) {
-          const uint4 q = *reinterpret_cast<const uint4*>(z + (long)r * H + col);
-          const uint32_t zv[4] = {q.x, q.y, q.z, q.w};
+  for (long t = blockIdx.x; t < T; t += gridDim.x) {
+    const uint16_t* d = dout + t * H;
+    for (int j = threadIdx.x >> 6; j < K; j += waves) {
+      const int r = row_of_route[t * K + j];
+      const bool valid = r >= 0 && r < R;
+      float acc = 0.0f;
+      if (valid) {
+        const float wt = d_z ? w[t * K + j] : 0.0f;
+        for (int col = lane * 8; col < H; col += 512) {
+          const uint4 u = *reinterpret_cast<const uint4*>(d + col);
+          const uint32_t dv[4] = {u.x, u.y, u.z, u.w};
+          if (d_w) {
+            const uint4 q = *reinterpret_cast<const uint4*>(z + (long)r * H + col);
+            const uint32_t zv[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            acc = __builtin_fmaf(bf16_to_f32(dv[i] & 0xFFFFu), bf16_to_f32(zv[i] & 0xFFFFu), acc);
-            acc = __builtin_fmaf(bf16_to_f32(dv[i] >> 16), bf16_to_f32(zv[i] >> 16), acc);
+            for (int i = 0; i < 4; ++i) {
+              acc = __builtin_fmaf(bf16_to_f32(dv[i] & 0xFFFFu), bf16_to_f32(zv[i] & 0xFFFFu), acc);
+              acc = __builtin_fmaf(bf16_to_f32(dv[i] >> 16), bf16_to_f32(zv[i] >> 16), acc);
+            }
+          }
+          if (d_z) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              o[i] = f32x2_to_bf16x2(wt * bf16_to_f32(dv[i] & 0xFFFFu), wt * bf16_to_f32(dv[i] >> 16));
+            *reinterpret_cast<uint4*>(d_z + (long)r * H + col) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
-        if (d_z) {
-          uint32_t o[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            o[i] = f32x2_to_bf16x2(wt * bf16_to_f32(dv[i] & 0xFFFFu), wt * bf16_to_f32(dv[i] >> 16));
-          *reinterpret_cast<uint4*>(d_z + (long)r * H + col) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
       }
-    }
-    if (d_w) {
+      if (d_w) {
 #pragma unroll
-      for (int off = 32; off > 0; off >>= 1) acc += __shfl_xor(acc, off, 64);
-      if (lane == 0) d_w[t * K + j] = acc;
+        for (int off = 32; off > 0; off >>= 1) acc += __shfl_xor(acc, off, 64);
+        if (lane == 0) d_w[t * K + j] = acc;
+      }
     }
   }
 }
@@ -103,7 +105,8 @@ hipError_t launch_finalize_backward(const uint16_t* dout, const uint16_t* z, con
                                     const float* w, int T, int K, int H, int R, float* d_w,
                                     uint16_t* d_z, hipStream_t s) {
   const int waves = K < 16 ? K : 16;
-  finalize_backward_kernel<<<T, waves * 64, 0, s>>>(dout, z, row_of_route, w, K, H, R, d_w, d_z);
+  const int grid = T < 1 << 20 ? T : 1 << 20;  // a launch has less than 2^32 threads
+  finalize_backward_kernel<<<grid, waves * 64, 0, s>>>(dout, z, row_of_route, w, T, K, H, R, d_w, d_z);
   return hipGetLastError();
 }
 

@@ -115,3 +115,24 @@ def test_refusals(pm):
     shifted = torch.empty(zz.numel() + 1, dtype=torch.bfloat16, device="cuda")[1:].view(zz.shape)
     with pytest.raises(pm.PmoeError, match="aligned"):
         pm.finalize_backward(d, shifted, r, ww)
+
+
+def test_more_tokens_than_one_launch_has_threads_for(pm):
+    import torch
+    T, K, H = (1 << 22) + 3, 16, 8                       # a wave for each slot would be 2^32 threads
+    rng = np.random.default_rng(5)
+    at = np.array([0, 1, 17, (1 << 20) - 1, 1 << 20, (1 << 22) - 1, 1 << 22, T - 1])
+    dout = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    some = f32_to_bf16_rne(rng.standard_normal((len(at), H)).astype(F32))
+    dout[torch.from_numpy(at).cuda()] = dev_bf16(some)
+    z = f32_to_bf16_rne(rng.standard_normal((len(at) * K, H)).astype(F32))
+    row = torch.full((T, K), -1, dtype=torch.int32, device="cuda")
+    names = rng.permutation(len(at) * K).astype(np.int32).reshape(len(at), K)
+    row[torch.from_numpy(at).cuda()] = dev(names)
+    w = torch.rand(T, K, device="cuda")
+    dw, dz = pm.finalize_backward(dout, dev_bf16(z), row.reshape(-1), w)
+    torch.cuda.synchronize()
+    pick = torch.from_numpy(at).cuda()
+    _check(dw[pick], dz, some, z, names.reshape(-1), w[pick].cpu().numpy())
+    dw[pick] = 0
+    assert not dw.any()

@@ -265,3 +265,19 @@ def test_graph_and_side_stream(pm):
         assert all(torch.equal(a, b) for a, b in zip(out, eager)) and torch.equal(dl, grad), i
     del g
     torch.cuda.synchronize()
+
+
+def test_most_tokens(pm):
+    import torch
+    # one expert: p = 1, lse = the logit 0.5, so every sum is exact in FP32
+    T, S, each = (1 << 30) - 1, 65536, 1 << 14
+    lg = torch.full((T, 1), 0.5, device="cuda")
+    ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    off = (torch.arange(S + 1, device="cuda", dtype=torch.int64) * each).clamp(max=T).to(torch.int32)
+    r = pm.router_balance(lg, ids, seq_offsets=off)
+    n = off[1:] - off[:-1]
+    assert torch.equal(r.tokens, n) and torch.equal(r.counts[:, 0], n) and torch.equal(r.prob[:, 0], n.float())
+    assert torch.equal(r.balance, torch.ones(S, device="cuda")) and torch.equal(r.z, torch.full_like(r.z, 0.25))
+    d = pm.router_backward(lg, ids, tokens=r.tokens, d_z=torch.ones(S, device="cuda"), seq_offsets=off, out=lg)
+    assert bool((d[:(S - 1) * each] == 1.0 / each).all())
+    assert bool(((d[(S - 1) * each:] * (each - 1) - 1).abs() <= 4 * 2.0 ** -24).all())
