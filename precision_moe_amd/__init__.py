@@ -489,12 +489,20 @@ def moe_forward(x, topk_ids, topk_w, weights: PreparedWeights, recipe="per_token
     if (adapters is None) != (adapter_ids is None):
         raise ValueError("adapters and adapter_ids are wanted both or neither")
     if adapters is not None:            # refused before the layer is enqueued
-        _, _, aT, _, aH, aN, *_ = _adapter_args(adapter_ids, *adapters)
+        _, _, aT, n, aH, aN, R, *on_device = _adapter_args(adapter_ids, *adapters)
         if (aT, aH, aN) != (T, W.H, W.H):
             raise ValueError("adapters of a layer must be [n, R, H] and [n, H, R], adapter_ids [T]")
         _bf16(x, "x", (T, W.H))
         if out is not None:
             _out(out, "out", torch.bfloat16, (T, W.H), x)
+            if abs(out.data_ptr() - x.data_ptr()) < 2 * T * W.H:
+                raise ValueError("out overlaps x, which the adapters read after the layer")
+        if any(t.device != x.device for t in (adapter_ids, *on_device)):
+            raise ValueError("adapters and adapter_ids must be on the device of x")
+        need = adapter_workspace_bytes(T, n, aH, aN, R)
+        adapter_workspace = _scratch(need, adapter_workspace, x)
+        if adapter_workspace.numel() < need:
+            raise ValueError("adapter_workspace too small")
     topk_ids, ids_type, topk_w = _routing_args(topk_ids, topk_w)
     workspace, out = _moe_buffers(T, K, W, act, x.device, workspace, out)
     evs = _event_array(step_events)

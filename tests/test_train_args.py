@@ -146,4 +146,17 @@ def test_layer_adapters_are_refused_before_the_layer_runs():
         pm.moe_forward(x, tk, w, P, adapters=(down, up, scale))
     with pytest.raises(ValueError, match="adapters of a layer"):
         pm.moe_forward(x, tk, w, P, adapters=(down, up, scale), adapter_ids=ids)
+    up = torch.zeros(2, H, 8, dtype=BF)
+    layer = dict(adapters=(down, up, scale), adapter_ids=ids)
+    with pytest.raises(ValueError, match="overlaps x"):
+        pm.moe_forward(x, tk, w, P, out=x, **layer)
+    with pytest.raises(ValueError, match="overlaps x"):
+        both = torch.zeros(T + 1, H, dtype=BF)
+        pm.moe_forward(both[1:], tk, w, P, out=both[:T], **layer)
+    with pytest.raises(ValueError, match="adapter_workspace too small"):
+        pm.moe_forward(x, tk, w, P, adapter_workspace=torch.empty(16, dtype=torch.uint8), **layer)
+    with pytest.raises(ValueError, match="on the device of x"):
+        pm.moe_forward(x, tk, w, P, adapters=(down, up.to("meta"), scale), adapter_ids=ids)
+    with pytest.raises(pm.PmoeError, match="multiple of 8"):
+        pm.moe_forward(x, tk, w, P, adapters=(down[:, :4], up[:, :, :4], scale), adapter_ids=ids)
     assert ctypes.sizeof(pm.MoeOptions) == 48          # the options of the C ABI keep their layout
