@@ -504,7 +504,8 @@ int pmoe_router_balance(const float* logits, const void* topk_ids, int ids_type,
  *                    losses, but may have one in d_topk_w.
  * counts is needed with d_balance, tokens with d_balance or d_z. With
  * renormalize = 1 a token whose chosen experts together have less than 1e-37 of
- * the largest p gets no gradient from d_topk_w. d_logits may be logits itself. Limits and alignment as above.
+ * the largest p gets no gradient from d_topk_w. d_logits may be logits itself, but
+ * overlaps no other input. Limits and alignment as above.
  */
 int pmoe_router_backward(const float* logits, const void* topk_ids, int ids_type, int T, int K, int E,
                          int renormalize, const int32_t* seq_offsets, int S,
@@ -520,7 +521,7 @@ int pmoe_router_backward(const float* logits, const void* topk_ids, int ids_type
  *   outside [0, R) is no route and no row is named twice (the routing names none
  *   twice; of a row named twice d_z holds one of the two);  topk_w, d_topk_w : float32 [T, K].
  * Either output may be NULL; z is needed for d_topk_w, topk_w for d_z. Rows of
- * d_z that no route names are left as they were. H must be a multiple of 8.
+ * d_z that no route names are left as they were. H must be a multiple of 8, at most 2^30.
  * Alignment: dout, z and d_z 16 bytes, others 4 bytes.
  */
 int pmoe_finalize_backward(const void* dout, const void* z, const int32_t* row_of_route,

@@ -918,6 +918,11 @@ PMOE_EXPORT int pmoe_router_backward(const float* logits, const void* topk_ids, 
   if (d_balance || d_z) PMOE_TRY(check_ptr_here(tokens, 4, "tokens"));
   if (d_topk_w) PMOE_TRY(check_ptr_here(d_topk_w, 4, "d_topk_w"));
   PMOE_TRY(check_ptr_here(d_logits, 4, "d_logits"));
+  const size_t bytes = (size_t)T * E * 4;
+  if ((d_logits != logits && overlap(d_logits, bytes, logits, bytes)) ||
+      overlap(d_logits, bytes, d_topk_w, (size_t)T * K * 4) ||
+      overlap(d_logits, bytes, topk_ids, (size_t)T * K * (ids_type == PMOE_IDS_INT64 ? 8 : 4)))
+    return fail(PMOE_ERR_ARG, "d_logits may be logits itself, but overlaps no other input");
   RouterGradParams p{logits, topk_ids, ids_type == PMOE_IDS_INT64, T, E, K, renormalize, seq_offsets, S,
                      counts, d_balance || d_z ? tokens : nullptr, d_balance, d_z, d_topk_w, d_logits};
   PMOE_HIP(launch_router_backward(p, static_cast<hipStream_t>(stream)));
@@ -930,7 +935,7 @@ PMOE_EXPORT int pmoe_finalize_backward(const void* dout, const void* z, const in
                                        void* d_z, void* stream) {
   if (T < 0 || K < 1 || K > 32) return fail(PMOE_ERR_SHAPE, "need T >= 0 and 1 <= K <= 32");
   if ((long long)T * K >= (1LL << 31) / 2) return fail(PMOE_ERR_SHAPE, "T*K too large");
-  if (H <= 0 || H % 8 != 0) return fail(PMOE_ERR_SHAPE, "H must be a positive multiple of 8");
+  if (H <= 0 || H % 8 != 0 || H > 1 << 30) return fail(PMOE_ERR_SHAPE, "H must be a positive multiple of 8, at most 2^30");
   if (R < 0) return fail(PMOE_ERR_SHAPE, "R must be >= 0");
   if (T == 0 || (R == 0 && !d_topk_w)) return ok();
   if (!d_topk_w && !d_z) return fail(PMOE_ERR_ARG, "one of d_topk_w and d_z is needed");
@@ -1000,7 +1005,10 @@ PMOE_EXPORT int pmoe_adapter_forward(const void* x, const void* adapter_ids, int
   const size_t need = adapter_forward_ws_bytes(T, n, H, N, R);
   if (ws_bytes < need)
     return fail(PMOE_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
-  const size_t out_bytes = (size_t)T * N * 2;
+  const size_t out_bytes = (size_t)T * N * 2, v_bytes = (size_t)T * R * 4;
+  if (overlap(v, v_bytes, out, out_bytes) || overlap(v, v_bytes, base, out_bytes) ||
+      overlap(v, v_bytes, x, (size_t)T * H * 2))
+    return fail(PMOE_ERR_ARG, "v overlaps another argument");
   if ((base != out && overlap(out, out_bytes, base, out_bytes)) ||
       overlap(out, out_bytes, x, (size_t)T * H * 2))
     return fail(PMOE_ERR_ARG, "out may be base itself, but overlaps no other input");
@@ -1053,6 +1061,13 @@ PMOE_EXPORT int pmoe_adapter_backward(const void* dy, const void* x, const float
   if ((base != dx && overlap(dx, dx_bytes, base, dx_bytes)) || overlap(dx, dx_bytes, dy, (size_t)T * N * 2) ||
       overlap(dx, dx_bytes, x, dx_bytes))
     return fail(PMOE_ERR_ARG, "dx may be base itself, but overlaps no other input");
+  const size_t down_bytes = (size_t)n * R * H * 4, up_bytes = (size_t)n * R * N * 4;
+  const auto meets = [&](const void* p, size_t bytes) {
+    return overlap(d_down, down_bytes, p, bytes) || overlap(d_up, up_bytes, p, bytes);
+  };
+  if (overlap(d_down, down_bytes, d_up, up_bytes) || meets(dx, dx_bytes) || meets(dy, (size_t)T * N * 2) ||
+      meets(x, dx_bytes) || meets(v, (size_t)T * R * 4))
+    return fail(PMOE_ERR_ARG, "d_down or d_up overlaps another argument");
   AdapterParams p{};
   p.x = x, p.ids = adapter_ids, p.ids64 = ids_type == PMOE_IDS_INT64;
   p.T = T, p.n = n, p.H = H, p.N = N, p.R = R;

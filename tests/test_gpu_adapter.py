@@ -340,5 +340,10 @@ def test_refusals(pm):
         pm.adapter_backward(dy, x, v, ids, *w, out=(dy, None, None))
     with pytest.raises(pm.PmoeError, match="workspace too small"):
         pm.adapter_backward(dy, x, v, ids, *w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(pm.PmoeError, match="v overlaps"):
+        pm.adapter_forward(x, ids, *w, out=out, v=out.view(torch.float32).view(-1)[:160].view(20, 8))
+    grads = torch.zeros(2 * 8 * 64 + 4, device="cuda")
+    with pytest.raises(pm.PmoeError, match="d_down or d_up overlaps"):
+        pm.adapter_backward(dy, x, v, ids, *w, out=(None, grads[:1024].view(2, 8, 64), grads[4:].view(2, 64, 8)))
     torch.cuda.synchronize()
     assert bool((out == 7).all())

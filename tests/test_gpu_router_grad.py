@@ -229,6 +229,10 @@ def test_refusals(pm):
         pm.router_balance(lg, tk.cpu(), out=out)
     with pytest.raises(pm.PmoeError, match="not a HIP device pointer|not device memory"):
         pm.router_backward(lg, tk, d_topk_w=torch.zeros(40, 2))
+    E = lg.shape[1]
+    rows = torch.zeros(41, E, device="cuda")
+    with pytest.raises(pm.PmoeError, match="overlaps"):
+        pm.router_backward(rows[:40], tk, d_topk_w=torch.zeros(40, tk.shape[1], device="cuda"), out=rows[1:])
     torch.cuda.synchronize()
     assert all(bool((t == 7).all()) for t in out)
 

@@ -55,7 +55,8 @@ def test_router_arguments():
 def test_finalize_backward_arguments():
     def call(T=4, K=2, H=64, R=8, dw=1, dz=None):
         return _rc("pmoe_finalize_backward", None, None, None, None, T, K, H, R, dw, dz, None)
-    for kw in (dict(T=-1), dict(K=0), dict(K=33), dict(H=0), dict(H=60), dict(R=-1), dict(T=1 << 29, K=2)):
+    for kw in (dict(T=-1), dict(K=0), dict(K=33), dict(H=0), dict(H=60), dict(H=(1 << 30) + 8), dict(R=-1),
+               dict(T=1 << 29, K=2)):
         assert call(**kw) == SHAPE, kw
     assert call(dw=None) == ARG
     assert call(T=0, dw=None) == 0 and call(R=0, dw=None) == 0         # nothing to do
