@@ -87,8 +87,13 @@ __device__ __forceinline__ int adapter_of(const void* ids, int ids64, long t, in
   return id >= 0 && id < n ? (int)id : -1;
 }
 
-constexpr int kReduceWaves = 8;
-constexpr int kReduceThreads = 64 * kReduceWaves;
+// Waves of a reducing workgroup, and the longest part of a row that it takes. Above rank 32 a wave
+// holds so many sums that a CU has room for twelve: three workgroups of four, of which one groups
+// or adds up while the others load (with eight waves and parts of 2048: T = 1024, n = 4, H = 4096,
+// R = 64 24.8 us a call, not 22.7). Up to rank 32 two of eight fit, and longer parts group each
+// span less often (with four waves and parts of 1024: T = 8192, n = 6, H = 7168, R = 16 84.5 us, not 83.3).
+__host__ __device__ constexpr int reduce_waves(int R) { return R <= 32 ? 8 : 4; }
+__host__ __device__ constexpr int reduce_part(int R) { return 256 * reduce_waves(R); }
 
 // Order and units of a span: unit u holds the places [start[u], start[u + 1]) of
 // the order; key = adapter << 10 | token of the span, adapter n for none.
@@ -97,7 +102,7 @@ struct SpanLds {
   uint32_t key[kSpan];
   uint16_t start[kSpan + 8];
   int table[16][kChunks];  // sort: keys of a digit in a chunk of 64, then the places before them
-  int wave[2][kReduceWaves];
+  int wave[2][8];
 };
 // The same in the workspace, one for each span: the order, and the units as
 // {first place | tokens << 16, adapter}.
@@ -133,15 +138,16 @@ __device__ __forceinline__ int wave_inclusive_max(int v) {
   return v;
 }
 
-// Groups the tokens [t0, t0 + count) with a workgroup of kReduceThreads; returns
+// Groups the tokens [t0, t0 + count) with a workgroup of kWaves; returns
 // the number of units. Ends with a barrier.
+template <int kWaves>
 __device__ __forceinline__ int group_span(const void* ids, int ids64, long t0, int count, int n, SpanLds& l) {
-  constexpr int kPer = kSpan / kReduceThreads;
+  constexpr int kThreads = 64 * kWaves, kPer = kSpan / kThreads;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   uint32_t key[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    const int i = tid + kReduceThreads * j;
+    const int i = tid + kThreads * j;
     key[j] = 0xFFFFFFFFu;
     if (i < count) {
       const int a = adapter_of(ids, ids64, t0 + i, n);
@@ -153,25 +159,25 @@ __device__ __forceinline__ int group_span(const void* ids, int ids64, long t0, i
   int edges = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    const int i = tid + kReduceThreads * j;
+    const int i = tid + kThreads * j;
     edges += __popcll(__ballot(i > 0 && i < count && key[j] >> 10 != l.key[max(i, 1) - 1] >> 10));
   }
   if (lane == 0) l.wave[0][wave] = edges;
   __syncthreads();
   edges = 0;
-  for (int w = 0; w < kReduceWaves; ++w) edges += l.wave[0][w];
+  for (int w = 0; w < kWaves; ++w) edges += l.wave[0][w];
   if (edges > kMostRuns) {
     // Stable sort by adapter, four bits at a time from the lowest: a key's place is the number of
     // keys with a smaller digit, plus those with its digit in the chunks before its own, plus
     // those among the lanes below (found by ballots on the digit's bits).
     const uint64_t below = lane == 0 ? 0ull : (~0ull >> (64 - lane));
     for (int shift = 10; n >> (shift - 10) != 0; shift += 4) {
-      for (int i = tid; i < 16 * kChunks; i += kReduceThreads) (&l.table[0][0])[i] = 0;
+      for (int i = tid; i < 16 * kChunks; i += kThreads) (&l.table[0][0])[i] = 0;
       __syncthreads();
       int digit[kPer], rank[kPer];
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const bool on = tid + kReduceThreads * j < count;
+        const bool on = tid + kThreads * j < count;
         digit[j] = key[j] >> shift & 15;
         uint64_t match = __ballot(on);
 #pragma unroll
@@ -180,7 +186,7 @@ __device__ __forceinline__ int group_span(const void* ids, int ids64, long t0, i
           match &= digit[j] >> b & 1 ? set : ~set;
         }
         rank[j] = __popcll(match & below);
-        if (on && rank[j] == 0) l.table[digit[j]][wave + kReduceWaves * j] = __popcll(match);
+        if (on && rank[j] == 0) l.table[digit[j]][wave + kWaves * j] = __popcll(match);
       }
       __syncthreads();
       const int mine = tid < 16 * kChunks ? (&l.table[0][0])[tid] : 0;
@@ -193,11 +199,11 @@ __device__ __forceinline__ int group_span(const void* ids, int ids64, long t0, i
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
-        if (tid + kReduceThreads * j < count)
-          l.key[l.table[digit[j]][wave + kReduceWaves * j] + rank[j]] = key[j];
+        if (tid + kThreads * j < count)
+          l.key[l.table[digit[j]][wave + kWaves * j] + rank[j]] = key[j];
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) key[j] = l.key[tid + kReduceThreads * j];
+      for (int j = 0; j < kPer; ++j) key[j] = l.key[tid + kThreads * j];
     }
   }
   // Units. Thread t looks at the places kPer t .. kPer t + kPer - 1.
@@ -230,7 +236,7 @@ __device__ __forceinline__ int group_span(const void* ids, int ids64, long t0, i
   place -= starts;
   __syncthreads();
   int units = 0;
-  for (int w = 0; w < kReduceWaves; ++w) {
+  for (int w = 0; w < kWaves; ++w) {
     if (w < wave) place += l.wave[1][w];
     units += l.wave[1][w];
   }
@@ -242,9 +248,10 @@ __device__ __forceinline__ int group_span(const void* ids, int ids64, long t0, i
   return units;
 }
 
+template <int kThreads>
 __device__ __forceinline__ void keep_order(const SpanLds& l, int units, int count, int n, SpanOrder* o) {
-  for (int i = threadIdx.x; i < count; i += kReduceThreads) o->key[i] = l.key[i];
-  for (int i = threadIdx.x; i < units; i += kReduceThreads) {
+  for (int i = threadIdx.x; i < count; i += kThreads) o->key[i] = l.key[i];
+  for (int i = threadIdx.x; i < units; i += kThreads) {
     const uint32_t at = l.start[i], len = l.start[i + 1] - at;
     const int a = l.key[at] >> 10;
     o->unit[i] = make_uint2(at | len << 16, a == n ? kNone : a);
@@ -253,11 +260,14 @@ __device__ __forceinline__ void keep_order(const SpanLds& l, int units, int coun
 }
 
 // ---------------------------------------------------------------- reduction over H (or N)
-// A sum over a row of D elements is cut into parts of adapter_part_length(D) elements (a
-// multiple of 64, at most 2048), one workgroup of eight waves each, whose waves take pieces of
+// A sum over a row of D elements is cut into parts of adapter_part_length(D, R) elements (a
+// multiple of 64, at most reduce_part(R)), one workgroup each, whose waves take pieces of
 // 64 elements in turn: together they read a row in long stretches.
-int adapter_parts(int D) { return (D + 2047) / 2048; }
-static int adapter_part_length(int D) { return ((D + adapter_parts(D) - 1) / adapter_parts(D) + 63) / 64 * 64; }
+static int adapter_parts(int D, int R) { return (D + reduce_part(R) - 1) / reduce_part(R); }
+static int adapter_part_length(int D, int R) {
+  const int parts = adapter_parts(D, R);
+  return ((D + parts - 1) / parts + 63) / 64 * 64;
+}
 
 // Eight rows of kCols columns each, turned: op[b] gets the eight values of
 // column b, ready as an MFMA operand. kCols is 1, 2, 4 or 8.
@@ -314,27 +324,28 @@ struct Block16 {
 // workgroups that take its units (with R > 64 its half units) in turn.
 // Operand row i of block b is r = NR i + b, so that a lane ends with 4 NR consecutive r of
 // one token, and with kTrans a lane reads NR neighbouring columns of eight rows.
-// Bound by the latency of the rows' loads: T = 8192, n = 6, H = 7168, R = 16 takes 33 us, 117 MB
-// at 3.6 TB/s. Parts of 1024 instead of 2048 elements group every span twice as often and were
-// slower. Many adapters in mixed order (T = 8192, n = 64, R = 64) read each matrix once a span,
-// 0.5 GB a call in all kernels; a grid that puts the spans of one part side by side makes that
-// call faster (255 -> 230 us) and the one above slower (83 -> 89).
+// Bound by the latency of grouping, loads and adding up, one after the other: T = 8192, n = 6,
+// H = 7168, R = 16 takes 32 us, 117 MB at 3.7 TB/s. Loading the next 64 elements ahead gained 1%
+// there and lost 6% with R = 32, for want of registers. Many adapters in mixed order read each
+// matrix once a span: T = 8192, n = 64, R = 64 takes 230 us a call. A grid with the spans of one
+// part side by side, not its parts, lost on the former (83 us a call -> 87).
 template <int NR, bool kTrans>
-__global__ __launch_bounds__(kReduceThreads, NR <= 2 ? 4 : 2) void adapter_reduce_kernel(
+__global__ __launch_bounds__(64 * reduce_waves(16 * NR), NR <= 2 ? 4 : NR <= 4 ? 3 : 2) void adapter_reduce_kernel(
     const uint16_t* __restrict__ in, const void* __restrict__ ids, int ids64, int T, int n, int D, int R,
     const uint16_t* __restrict__ W, int length, int share, SpanOrder* __restrict__ orders,
     float* __restrict__ part) {
+  constexpr int kWaves = reduce_waves(16 * NR);
   constexpr int NF = NR <= 4 ? 4 : 2;      // row blocks of an item: a unit, or half a unit
   __shared__ __align__(16) SpanLds lds;
-  __shared__ uint4 turn[kReduceWaves][2][128];
-  __shared__ floatx4 red[kReduceWaves][NR][64];
+  __shared__ uint4 turn[kWaves][2][128];
+  __shared__ floatx4 red[kWaves][NR][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = lane & 15, g = lane >> 4, row8 = lane >> 3, chunk = lane & 7;
   const int sp = blockIdx.y / share, mine = blockIdx.y % share;
   const long t0 = (long)sp * kSpan;
   const int count = (int)min((long)kSpan, T - t0);
-  const int units = group_span(ids, ids64, t0, count, n, lds);
-  if (mine == 0 && blockIdx.x == 0) keep_order(lds, units, count, n, orders + sp);
+  const int units = group_span<kWaves>(ids, ids64, t0, count, n, lds);
+  if (mine == 0 && blockIdx.x == 0) keep_order<64 * kWaves>(lds, units, count, n, orders + sp);
   const int k_begin = blockIdx.x * length + wave * 64, k_end = min(D, (int)(blockIdx.x + 1) * length);
   float* dst = part + ((long)blockIdx.x * T + t0) * R;
   const Buffer rows_in = buffer_of(in + t0 * D, (uint32_t)count * D * 2u);
@@ -355,7 +366,7 @@ __global__ __launch_bounds__(kReduceThreads, NR <= 2 ? 4 : 2) void adapter_reduc
     for (int f = 0; f < NF; ++f)
 #pragma unroll
       for (int c = 0; c < NR; ++c) acc[f][c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k0 = k_begin; k0 < k_end; k0 += 64 * kReduceWaves) {
+    for (int k0 = k_begin; k0 < k_end; k0 += 64 * kWaves) {
       Block16 xb[NF];
       const int kc = k0 + 8 * chunk;
 #pragma unroll
@@ -407,14 +418,14 @@ __global__ __launch_bounds__(kReduceThreads, NR <= 2 ? 4 : 2) void adapter_reduc
       for (int c = 0; c < NR; ++c) red[wave][c][lane] = acc[f][c];
       __syncthreads();
       const int m = 16 * f + col;
-      for (int q = wave; q < NR; q += kReduceWaves) {
+      for (int q = wave; q < NR; q += kWaves) {
         floatx4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = (4 * q + e) / NR, c = (4 * q + e) % NR;
           float sum = red[0][c][lane][i];
 #pragma unroll
-          for (int y = 1; y < kReduceWaves; ++y) sum += red[y][c][lane][i];
+          for (int y = 1; y < kWaves; ++y) sum += red[y][c][lane][i];
           v[e] = sum;
         }
         const int r = 4 * NR * g + 4 * q;
@@ -1077,7 +1088,7 @@ static AdapterLayout adapter_layout(void* ws, int T, int n, int H, int N, int R,
     return at;
   };
   l.orders = reinterpret_cast<SpanOrder*>(take(sizeof(SpanOrder) * spans_of(T)));
-  l.part = reinterpret_cast<float*>(take((size_t)adapter_parts(backward ? N : H) * T * R * 4));
+  l.part = reinterpret_cast<float*>(take((size_t)adapter_parts(backward ? N : H, R) * T * R * 4));
   if (backward) {
     const GradSplit g = grad_split(T, n, H, N, R);
     const int slots = g.groups * g.shares;
@@ -1093,16 +1104,16 @@ static AdapterLayout adapter_layout(void* ws, int T, int n, int H, int N, int R,
 
 static hipError_t reduce(bool trans, const void* in, const AdapterParams& p, int D, const void* W,
                          const AdapterLayout& l, hipStream_t s) {
-  const int parts = adapter_parts(D), share = span_share(p.T, p.n, parts);
+  const int parts = adapter_parts(D, p.R), share = span_share(p.T, p.n, parts);
   const dim3 grid(parts, spans_of(p.T) * share);
-  const int length = adapter_part_length(D);
+  const int length = adapter_part_length(D, p.R);
   const uint16_t* x = static_cast<const uint16_t*>(in);
   const uint16_t* w = static_cast<const uint16_t*>(W);
   if (trans)
-    PMOE_BY_RANK(p.R, (adapter_reduce_kernel<NR, true><<<grid, kReduceThreads, 0, s>>>(
+    PMOE_BY_RANK(p.R, (adapter_reduce_kernel<NR, true><<<grid, 64 * reduce_waves(p.R), 0, s>>>(
                           x, p.ids, p.ids64, p.T, p.n, D, p.R, w, length, share, l.orders, l.part)));
   else
-    PMOE_BY_RANK(p.R, (adapter_reduce_kernel<NR, false><<<grid, kReduceThreads, 0, s>>>(
+    PMOE_BY_RANK(p.R, (adapter_reduce_kernel<NR, false><<<grid, 64 * reduce_waves(p.R), 0, s>>>(
                           x, p.ids, p.ids64, p.T, p.n, D, p.R, w, length, share, l.orders, l.part)));
   return hipGetLastError();
 }
@@ -1135,7 +1146,7 @@ hipError_t launch_adapter_forward(const AdapterParams& p, hipStream_t s) {
   const AdapterLayout l = adapter_layout(p.ws, p.T, p.n, p.H, p.N, p.R, false);
   const hipError_t e = reduce(false, p.x, p, p.H, p.down, l, s);
   if (e != hipSuccess) return e;
-  return expand(false, adapter_parts(p.H), p, p.N, p.up, l, p.v_out, 0, s);
+  return expand(false, adapter_parts(p.H, p.R), p, p.N, p.up, l, p.v_out, 0, s);
 }
 
 hipError_t launch_adapter_backward(const AdapterParams& p, hipStream_t s) {
@@ -1143,7 +1154,7 @@ hipError_t launch_adapter_backward(const AdapterParams& p, hipStream_t s) {
   if (p.T > 0) {
     hipError_t e = reduce(true, p.dy, p, p.N, p.up, l, s);
     if (e != hipSuccess) return e;
-    e = expand(true, adapter_parts(p.N), p, p.H, p.down, l, l.du, 1, s);
+    e = expand(true, adapter_parts(p.N, p.R), p, p.H, p.down, l, l.du, 1, s);
     if (e != hipSuccess) return e;
   }
   if (!p.d_down) return hipSuccess;

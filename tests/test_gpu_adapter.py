@@ -1,7 +1,7 @@
 """GPU parity of the adapters with the float64 oracle.
 
 Tolerances, u = 2^-24. A sum over H (or N) of products of BF16 values (exact in FP32) is taken by
-waves over at most 256 elements each, then over 8 waves and at most 8 parts (below 528 in any cut):
+waves over at most 256 elements each, then over 8 waves and at most 8 parts, or 4 and 16 (below 528):
   v, du    528 u of the sum of the sizes;
   out, dx  the FP32 result rounded to BF16 (half a step, 2^-8 of its size) plus the error of the low-rank
            term: that of v (du), two BF16 values for scale * v (rest below 2^-16 of it) and at most 256 + 2

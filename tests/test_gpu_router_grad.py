@@ -4,8 +4,9 @@ Counts and token numbers are exact. Tolerances, with u = 2^-24 (half a step of F
   softmax  exp's argument l - m is rounded (at most |l - m| u; where |l - m| > 16 the value
            is below 2^-23 of the row's largest, so 16 u covers what is seen), exp and log within
            2 u, the sum over at most 1024 logits in 16 + 6 additions: 64 u in all;
-  prob     one sum of positive terms: a wave adds rows / 4 of them, then 4 waves, then the slots,
-           rows / 4 + 4 + T / rows additions, below 64 + T / 16;
+  prob     one sum of positive terms: of the rows of a workgroup a wave adds an eighth at most, then
+           4 lanes and 8 waves are added, then the slots of the sequence: rows / 8 + 10 + slots
+           additions, below 64 + T / 16 at every size here (rows and slots are about sqrt(T));
   balance  the same and 20 more for the sum over experts and the scaling;
   z        lse enters squared (twice its error), lse itself with 64 u of max(|m|, 1) + log E;
   gradient every term within 64 u of its size, the sizes added up by the oracle.
