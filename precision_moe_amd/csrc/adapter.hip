@@ -471,8 +471,14 @@ __device__ __forceinline__ void store16(uint16_t* out, uint32_t offset, bool fir
   if (second) store_at<uint4>(out, offset + 64u, make_uint4(o[4], o[5], o[6], o[7]));
 }
 
+// Columns, and threads, of an expanding workgroup. Each one adds the parts of its tokens again, so
+// wide ones pay as soon as there are enough of them: T = 4096, n = 4, H = N = 7168, R = 128 takes 97
+// us a call with 512 and 107 with 256, T = 8192, n = 6, R = 16 81.7 and 83.3; T = 2048, n = 8,
+// H = N = 4096, R = 32 25.8 and 23.9.
+static int expand_cols(int T, int D) { return (long)T * D >= 1l << 24 ? 512 : 256; }
+
 // out[t][c] = bf16(base[t][c] + sum_r low[t][r] W_a[c][r]) (kTrans: W_a[r][c]),
-// low = scale * (sum of the parts). blockIdx.x is a block of 256 columns, 64 for each wave,
+// low = scale * (sum of the parts). blockIdx.x is a block of kCols columns, 64 for each wave,
 // so that neighbouring workgroups write neighbouring pieces of the same tokens; blockIdx.y
 // is a span and one of `share` workgroups that take its units in turn. Workgroups with
 // blockIdx.x == 0 also write the sum of the parts to `sums` (times the scale if scale_sums),
@@ -484,8 +490,8 @@ __device__ __forceinline__ void store16(uint16_t* out, uint32_t offset, bool fir
 // r of one column: a lane reads four columns of eight rows and turns them in registers.
 // Bound by HBM: T = 8192, n = 6, N = 7168, R = 16 takes 50 us, 235 MB at 4.7 TB/s. Fetching the
 // next unit's rows ahead halved the waves that fit, and lost.
-template <int NR, bool kTrans>
-__global__ __launch_bounds__(256) void adapter_expand_kernel(
+template <int NR, bool kTrans, int kCols>
+__global__ __launch_bounds__(kCols) void adapter_expand_kernel(
     const float* __restrict__ part, int parts, const SpanOrder* __restrict__ orders, int share, int T,
     int D, int R, const uint16_t* __restrict__ W, const float* __restrict__ scale,
     const uint16_t* base, uint16_t* out, float* __restrict__ sums, int scale_sums) {
@@ -498,7 +504,7 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(
   const SpanOrder* order = orders + sp;
   const int units = order->units;
   const long t0 = (long)sp * kSpan;
-  const int c0 = blockIdx.x * 256 + 64 * wave;
+  const int c0 = blockIdx.x * kCols + 64 * wave;
   const int c = c0 + 8 * g;  // the lane's columns of the result: c .. c + 7 and c + 32 .. c + 39
   // tokens without an adapter: base, or zeros
   const bool fill = out != nullptr && base != out;
@@ -516,13 +522,13 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(
     if (adapter == kNone) {
       __syncthreads();
       if (fill)
-        for (int m = tid >> 5; m < len; m += 8) {
-          const int cn = blockIdx.x * 256 + (tid & 31) * 8;
+        for (int m = tid / (kCols / 8); m < len; m += 8) {
+          const int cn = blockIdx.x * kCols + tid % (kCols / 8) * 8;
           const uint32_t o = (place[m] * (uint32_t)D + cn) * 2u;
           if (cn < D) store_at<uint4>(out, o, base ? load_at<uint4>(base, o) : make_uint4(0, 0, 0, 0));
         }
       if (keep_sums)
-        for (int i = tid; i < len * R; i += 256) sums[place[i / R] * R + i % R] = 0.0f;
+        for (int i = tid; i < len * R; i += kCols) sums[place[i / R] * R + i % R] = 0.0f;
       continue;
     }
     const int nf = (len + 15) >> 4;
@@ -564,7 +570,7 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(
       bv[f][1] = load_if<uint4>(base_rows, b + 64u, m < len && c + 32 < D);
     }
 #pragma unroll 1
-    for (int i = tid; i < nf * 16 * (4 * NR); i += 256) {
+    for (int i = tid; i < nf * 16 * (4 * NR); i += kCols) {
       const int m = i / (4 * NR), r = i % (4 * NR) * 4;
       floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
       if (m < len && r < R) {
@@ -1118,20 +1124,24 @@ static hipError_t reduce(bool trans, const void* in, const AdapterParams& p, int
   return hipGetLastError();
 }
 
-static hipError_t expand(bool trans, int parts, const AdapterParams& p, int D, const void* W,
-                         const AdapterLayout& l, float* sums, int scale_sums, hipStream_t s) {
-  const int chunks = p.out ? (D + 255) / 256 : 1, share = span_share(p.T, p.n, chunks);
+template <bool kTrans, int kCols>
+static hipError_t expand_by(int parts, const AdapterParams& p, int D, const void* W, const AdapterLayout& l,
+                            float* sums, int scale_sums, hipStream_t s) {
+  const int chunks = p.out ? (D + kCols - 1) / kCols : 1, share = span_share(p.T, p.n, chunks);
   const dim3 grid(chunks, spans_of(p.T) * share);
   const uint16_t* w = static_cast<const uint16_t*>(W);
   const uint16_t* b = static_cast<const uint16_t*>(p.base);
   uint16_t* o = static_cast<uint16_t*>(p.out);
-  if (trans)
-    PMOE_BY_RANK(p.R, (adapter_expand_kernel<NR, true><<<grid, 256, 0, s>>>(
-                          l.part, parts, l.orders, share, p.T, D, p.R, w, p.scale, b, o, sums, scale_sums)));
-  else
-    PMOE_BY_RANK(p.R, (adapter_expand_kernel<NR, false><<<grid, 256, 0, s>>>(
-                          l.part, parts, l.orders, share, p.T, D, p.R, w, p.scale, b, o, sums, scale_sums)));
+  PMOE_BY_RANK(p.R, (adapter_expand_kernel<NR, kTrans, kCols><<<grid, kCols, 0, s>>>(
+                        l.part, parts, l.orders, share, p.T, D, p.R, w, p.scale, b, o, sums, scale_sums)));
   return hipGetLastError();
+}
+
+template <bool kTrans>
+static hipError_t expand(int parts, const AdapterParams& p, int D, const void* W, const AdapterLayout& l,
+                         float* sums, int scale_sums, hipStream_t s) {
+  return expand_cols(p.T, D) == 512 ? expand_by<kTrans, 512>(parts, p, D, W, l, sums, scale_sums, s)
+                                    : expand_by<kTrans, 256>(parts, p, D, W, l, sums, scale_sums, s);
 }
 
 size_t adapter_forward_ws_bytes(int T, int n, int H, int N, int R) {
@@ -1146,7 +1156,7 @@ hipError_t launch_adapter_forward(const AdapterParams& p, hipStream_t s) {
   const AdapterLayout l = adapter_layout(p.ws, p.T, p.n, p.H, p.N, p.R, false);
   const hipError_t e = reduce(false, p.x, p, p.H, p.down, l, s);
   if (e != hipSuccess) return e;
-  return expand(false, adapter_parts(p.H, p.R), p, p.N, p.up, l, p.v_out, 0, s);
+  return expand<false>(adapter_parts(p.H, p.R), p, p.N, p.up, l, p.v_out, 0, s);
 }
 
 hipError_t launch_adapter_backward(const AdapterParams& p, hipStream_t s) {
@@ -1154,7 +1164,7 @@ hipError_t launch_adapter_backward(const AdapterParams& p, hipStream_t s) {
   if (p.T > 0) {
     hipError_t e = reduce(true, p.dy, p, p.N, p.up, l, s);
     if (e != hipSuccess) return e;
-    e = expand(true, adapter_parts(p.N, p.R), p, p.H, p.down, l, l.du, 1, s);
+    e = expand<true>(adapter_parts(p.N, p.R), p, p.H, p.down, l, l.du, 1, s);
     if (e != hipSuccess) return e;
   }
   if (!p.d_down) return hipSuccess;

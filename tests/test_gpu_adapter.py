@@ -347,3 +347,30 @@ def test_refusals(pm):
         pm.adapter_backward(dy, x, v, ids, *w, out=(None, grads[:1024].view(2, 8, 64), grads[4:].view(2, 64, 8)))
     torch.cuda.synchronize()
     assert bool((out == 7).all())
+
+
+@pytest.mark.parametrize("R,order", [(8, "runs"), (24, "mixed"), (40, "mixed"), (128, "runs")])
+def test_long_batches_of_wide_rows(pm, R, order):
+    """From T * N (T * H) = 2^24 on a workgroup writes 512 columns: right at a width that is no
+    multiple of them, for tokens with and without an adapter, and with the bits of a short call."""
+    import torch
+    c = Case(1100, 5, 64, 15888, R, order)
+    w, x, ids, base = c.weights(), c.d("x"), c.d("ids"), c.d("base")
+    out, v = pm.adapter_forward(x, ids, *w, base=base)
+    some, _ = pm.adapter_forward(x[7:90], ids[7:90], *w, base=base[7:90])
+    none, _ = pm.adapter_forward(x, torch.full_like(ids, -1), *w)
+    torch.cuda.synchronize()
+    _check_forward(c, out, v)
+    assert torch.equal(some.view(torch.int16), out[7:90].view(torch.int16))
+    assert not none.any()
+    c = Case(1100, 5, 15888, 64, R, order)
+    w, ids, dy, dx_base = c.weights(), c.d("ids"), c.d("dy"), c.d("dx_base")
+    dx, _, _ = pm.adapter_backward(dy, None, None, ids, *w, base=dx_base, need_weights=False)
+    some, _, _ = pm.adapter_backward(dy[7:90], None, None, ids[7:90], *w, base=dx_base[7:90], need_weights=False)
+    torch.cuda.synchronize()
+    v0 = np.zeros((1100, R), F32)
+    args = [c.f(k) for k in ("dy", "x")] + [v0, c.ids] + [c.f(k) for k in ("down", "up", "scale")]
+    want = ot.adapter_backward(*args, c.f("dx_base"))[0]
+    size = ot.adapter_backward(*[a if a is c.ids else np.abs(a) for a in args])[0]
+    _close_bf16(dx, want, size, "dx")
+    assert torch.equal(some.view(torch.int16), dx[7:90].view(torch.int16))
