@@ -571,7 +571,8 @@ int pmoe_adapter_forward(const void* x, const void* adapter_ids, int ids_type, i
  * dx may be NULL (x has no gradient), or d_down and d_up both (the adapters are
  * not trained; x and v are then not read). d_down and d_up are written whole,
  * zeros for adapters without tokens, and their sums over tokens are taken in a
- * fixed order. The gradient of base is dy itself.
+ * fixed order; an infinite v or du makes the entries that it enters NaN. The
+ * gradient of base is dy itself.
  */
 int pmoe_adapter_backward(const void* dy, const void* x, const float* v, const void* adapter_ids,
                           int ids_type, int T, int n, int H, int N, int R, const void* down,

@@ -27,6 +27,8 @@ Modules:
              pipeline with the layer options (SwiGLU clamp, fused finalize).
   layer   -- the router front (top-k, softmax weights), the SwiGLU clamp and
              the fused (order-free) finalize.
+  train   -- the router's balance loss and gradients, the gradients of the
+             finalize, and low-rank adapters with theirs.
 
 Parity pins: every function here is pinned by a CPU test against something
 other than itself (hand enumerations, a library cast, brute force, closed

@@ -488,7 +488,7 @@ static int expand_cols(int T, int D) { return (long)T * D >= 1l << 24 ? 512 : 25
 // columns 8 g .. 8 g + 7 and 32 further of one token, so that four lanes read and write 64
 // bytes at a stretch. With kTrans W_a has its columns contiguous while an operand wants eight
 // r of one column: a lane reads four columns of eight rows and turns them in registers.
-// Bound by HBM: T = 8192, n = 6, N = 7168, R = 16 takes 50 us, 235 MB at 4.7 TB/s. Fetching the
+// Bound by HBM: T = 8192, n = 6, N = 7168, R = 16 takes 49 us, 235 MB at 4.8 TB/s. Fetching the
 // next unit's rows ahead halved the waves that fit, and lost.
 template <int NR, bool kTrans, int kCols>
 __global__ __launch_bounds__(kCols) void adapter_expand_kernel(
