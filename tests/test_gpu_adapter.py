@@ -374,3 +374,18 @@ def test_long_batches_of_wide_rows(pm, R, order):
     size = ot.adapter_backward(*[a if a is c.ids else np.abs(a) for a in args])[0]
     _close_bf16(dx, want, size, "dx")
     assert torch.equal(some.view(torch.int16), dx[7:90].view(torch.int16))
+
+
+@pytest.mark.parametrize("T,n,H,N,R", [(2000, 300, 1040, 784, 72), (1500, 400, 272, 528, 16), (4200, 3, 528, 784, 40)])
+def test_runs_repeat(pm, T, n, H, N, R):
+    """The same inputs give the same bits, with many workgroups to a CU and with shared windows."""
+    import torch
+    c = Case(T, n, H, N, R)
+    w, x, ids, dy = c.weights(), c.d("x"), c.d("ids"), c.d("dy")
+
+    def call():
+        out, v = pm.adapter_forward(x, ids, *w)
+        return (out, v, *pm.adapter_backward(dy, x, v, ids, *w))
+    first = call()
+    for _ in range(5):
+        assert all(torch.equal(p, q) for p, q in zip(call(), first))
