@@ -1038,8 +1038,8 @@ PMOE_EXPORT int pmoe_adapter_backward(const void* dy, const void* x, const float
     PMOE_TRY(check_ptr_here(dy, 16, "dy"));
     PMOE_TRY(check_ids(adapter_ids, ids_type, "adapter_ids"));
     PMOE_TRY(check_ptr_here(up, 16, "up"));
+    PMOE_TRY(check_ptr_here(down, 16, "down"));  // the pass that sums du's parts reads it, with dx or without
     if (dx) {
-      PMOE_TRY(check_ptr_here(down, 16, "down"));
       if (base) PMOE_TRY(check_ptr_here(base, 16, "base"));
       PMOE_TRY(check_ptr_here(dx, 16, "dx"));
     }

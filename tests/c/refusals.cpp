@@ -1,0 +1,81 @@
+// Refusals of calls that need a device to get past their first checks. The program defines the
+// HIP runtime calls of the library's host layer itself (its symbols come before the runtime's):
+// one gfx950 device, two whose memory can be told apart, and launches that are only counted. No
+// address is ever read. Each call has to be refused before the first launch, or, as it stands
+// without the fault, has to reach one.
+#include <hip/hip_runtime_api.h>
+
+#include <cstdint>
+#include <cstdio>
+#include <cstring>
+#include <string>
+
+#include "pmoe.h"
+
+static int launches = 0, failures = 0;
+
+// 16 MiB blocks: number i is device 0's, 64 + i device 1's, 128 + i the host's.
+static char* block(int i, size_t at = 0) { return reinterpret_cast<char*>(((uintptr_t)i + 4096) << 24) + at; }
+
+extern "C" {
+hipError_t hipGetDevice(int* d) { return *d = 0, hipSuccess; }
+hipError_t hipGetDeviceProperties(hipDeviceProp_t* p, int) {  // the header maps the name to its version
+  std::memset(p, 0, sizeof *p);
+  std::strcpy(p->gcnArchName, "gfx950:sramecc+:xnack-");
+  return hipSuccess;
+}
+hipError_t hipPointerGetAttributes(hipPointerAttribute_t* a, const void* p) {
+  const uintptr_t i = (reinterpret_cast<uintptr_t>(p) >> 24) - 4096;
+  std::memset(a, 0, sizeof *a);
+  if (i >= 128) return hipErrorInvalidValue;
+  a->type = hipMemoryTypeDevice;
+  a->device = i >= 64;
+  return hipSuccess;
+}
+// what stands between <<<...>>> and the launch
+hipError_t __hipPushCallConfiguration(dim3, dim3, size_t, hipStream_t) { return hipSuccess; }
+hipError_t __hipPopCallConfiguration(dim3* grid, dim3* block, size_t* lds, hipStream_t* s) {
+  return *grid = *block = dim3(1), *lds = 0, *s = nullptr, hipSuccess;
+}
+hipError_t hipLaunchKernel(const void*, dim3, dim3, void**, size_t, hipStream_t) { return ++launches, hipSuccess; }
+hipError_t hipGetLastError(void) { return hipSuccess; }
+}
+
+static void expect(const char* what, int rc, int want, const char* message = "") {
+  const bool launched = launches > 0, refused = want != PMOE_OK;
+  if (rc != want || launched == refused || std::string(pmoe_last_error()).find(message) == std::string::npos) {
+    std::printf("FAIL %s: %d instead of %d, %d launches, last error: %s\n", what, rc, want, launches, pmoe_last_error());
+    ++failures;
+  }
+  launches = 0;
+}
+
+// ---------------------------------------------------------------- adapters
+struct Adapters {
+  int T = 4, n = 2, H = 64, N = 48, R = 8;
+  void *dy = block(0), *x = block(1), *v = block(2), *ids = block(3), *down = block(4), *up = block(5),
+       *scale = block(6), *base = block(7), *out = block(8), *d_down = block(9), *d_up = block(10), *ws = block(11);
+  int backward() const {
+    return pmoe_adapter_backward(dy, x, (float*)v, ids, PMOE_IDS_INT32, T, n, H, N, R, down, up, (float*)scale, base,
+                                 out, (float*)d_down, (float*)d_up, ws, 1 << 24, nullptr);
+  }
+};
+
+static void adapters() {
+  Adapters a;
+  expect("backward", a.backward(), PMOE_OK);
+  a.out = a.base = nullptr;  // the matrices' gradients alone; both matrices are read
+  expect("backward without dx", a.backward(), PMOE_OK);
+  a.down = nullptr;
+  expect("no down", a.backward(), PMOE_ERR_POINTER, "down is null");
+  a.down = block(128);
+  expect("down on the host", a.backward(), PMOE_ERR_POINTER, "down is not");
+  a.down = block(64);
+  expect("down on another device", a.backward(), PMOE_ERR_POINTER, "down is on device 1");
+}
+
+int main() {
+  adapters();
+  std::printf(failures ? "refusals: %d failures\n" : "refusals: ok\n", failures);
+  return failures != 0;
+}
