@@ -81,10 +81,10 @@ int check_ptr_here(const void* p, size_t align, const char* name) {
   return check_ptr(p, align, name, dev);
 }
 
-// Whether [a, a + a_bytes) and [b, b + b_bytes) share a byte; null shares none.
+// Whether [a, a + a_bytes) and [b, b + b_bytes) share a byte; null and empty ranges share none.
 bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + b_bytes && y < x + a_bytes;
+  return a && b && a_bytes && b_bytes && x < y + b_bytes && y < x + a_bytes;
 }
 
 #define PMOE_TRY(expr)          \

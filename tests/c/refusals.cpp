@@ -74,8 +74,19 @@ static void adapters() {
   expect("down on another device", a.backward(), PMOE_ERR_POINTER, "down is on device 1");
 }
 
+// What has no bytes overlaps nothing, wherever its pointer lies.
+static void empty_ranges() {
+  Adapters a;
+  a.T = 0;
+  a.dy = block(9, 64), a.x = block(10, 64), a.v = block(9, 128), a.ids = block(3), a.out = a.base = block(9, 256);
+  expect("backward of no tokens, cut from the gradients' own memory", a.backward(), PMOE_OK);
+  expect("gradients of no rows", pmoe_finalize_backward(block(0), block(0, 64), (int*)block(1), (float*)block(2), 4, 2, 64, 0,
+                                                        (float*)block(3), block(0, 64), nullptr), PMOE_OK);
+}
+
 int main() {
   adapters();
+  empty_ranges();
   std::printf(failures ? "refusals: %d failures\n" : "refusals: ok\n", failures);
   return failures != 0;
 }
