@@ -486,6 +486,7 @@ size_t pmoe_router_balance_workspace_bytes(int T, int E, int K, int S);
  * T = 0 writes zeros. Sums over tokens are taken in a fixed order: the same
  * inputs give the same bits. 1 <= E <= 1024, 1 <= K <= min(32, E), T*K < 2^30,
  * 1 <= S <= PMOE_MAX_SEQUENCES. Alignment: ws 16 bytes, int64 ids 8, others 4.
+ * The outputs and ws share no memory with each other or with an input.
  */
 int pmoe_router_balance(const float* logits, const void* topk_ids, int ids_type, int T, int K, int E,
                         const int32_t* seq_offsets, int S,
@@ -505,7 +506,7 @@ int pmoe_router_balance(const float* logits, const void* topk_ids, int ids_type,
  * counts is needed with d_balance, tokens with d_balance or d_z. With
  * renormalize = 1 a token whose chosen experts together have less than 1e-37 of
  * the largest p gets no gradient from d_topk_w. d_logits may be logits itself, but
- * overlaps no other input. Limits and alignment as above.
+ * shares no memory with another argument that the call reads. Limits and alignment as above.
  */
 int pmoe_router_backward(const float* logits, const void* topk_ids, int ids_type, int T, int K, int E,
                          int renormalize, const int32_t* seq_offsets, int S,

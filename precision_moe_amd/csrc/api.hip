@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
@@ -85,6 +86,24 @@ int check_ptr_here(const void* p, size_t align, const char* name) {
 bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a && b && a_bytes && b_bytes && x < y + b_bytes && y < x + a_bytes;
+}
+
+// What a call writes (its workspace is one) shares no byte with what else it writes, nor with
+// what it reads: workgroups read and write in no order between them. Arguments that the call
+// does not touch stay out of both lists.
+struct Range {
+  const char* name;
+  const void* at;
+  size_t bytes;
+};
+int check_apart(std::initializer_list<Range> written, std::initializer_list<Range> read) {
+  for (const Range* a = written.begin(); a != written.end(); ++a) {
+    const auto meets = [a](const Range& b) { return overlap(a->at, a->bytes, b.at, b.bytes); };
+    const Range* b = std::find_if(a + 1, written.end(), meets);
+    if (b == written.end()) b = std::find_if(read.begin(), read.end(), meets);
+    if (b != read.end()) return fail(PMOE_ERR_ARG, std::string(a->name) + " overlaps " + b->name);
+  }
+  return PMOE_OK;
 }
 
 #define PMOE_TRY(expr)          \
@@ -850,10 +869,12 @@ int check_router_shape(int T, int E, int K, int S, const void* seq_offsets) {
   return PMOE_OK;
 }
 
+size_t ids_bytes(int ids_type) { return ids_type == PMOE_IDS_INT64 ? 8 : 4; }
+
 int check_ids(const void* ids, int ids_type, const char* name) {
   if (ids_type != PMOE_IDS_INT32 && ids_type != PMOE_IDS_INT64)
     return fail(PMOE_ERR_ARG, "ids_type must be PMOE_IDS_INT32 or PMOE_IDS_INT64");
-  return check_ptr_here(ids, ids_type == PMOE_IDS_INT64 ? 8 : 4, name);
+  return check_ptr_here(ids, ids_bytes(ids_type), name);
 }
 
 }  // namespace
@@ -886,6 +907,11 @@ PMOE_EXPORT int pmoe_router_balance(const float* logits, const void* topk_ids, i
   const size_t need = balance_ws_bytes(T, E, S);
   if (ws_bytes < need)
     return fail(PMOE_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
+  const size_t per_seq = (size_t)S * 4;
+  PMOE_TRY(check_apart({{"counts", counts, per_seq * E}, {"tokens", tokens, per_seq}, {"prob", prob, per_seq * E},
+                        {"balance", balance, per_seq}, {"z", z, per_seq}, {"ws", ws, need}},
+                       {{"logits", logits, (size_t)T * E * 4}, {"topk_ids", topk_ids, (size_t)T * K * ids_bytes(ids_type)},
+                        {"seq_offsets", seq_offsets, per_seq + 4}}));
   BalanceParams p{logits, topk_ids, ids_type == PMOE_IDS_INT64, T, E, K, seq_offsets, S,
                   counts, tokens, prob, balance, z, ws};
   PMOE_HIP(launch_router_balance(p, static_cast<hipStream_t>(stream)));
@@ -919,10 +945,16 @@ PMOE_EXPORT int pmoe_router_backward(const float* logits, const void* topk_ids, 
   if (d_topk_w) PMOE_TRY(check_ptr_here(d_topk_w, 4, "d_topk_w"));
   PMOE_TRY(check_ptr_here(d_logits, 4, "d_logits"));
   const size_t bytes = (size_t)T * E * 4;
-  if ((d_logits != logits && overlap(d_logits, bytes, logits, bytes)) ||
-      overlap(d_logits, bytes, d_topk_w, (size_t)T * K * 4) ||
-      overlap(d_logits, bytes, topk_ids, (size_t)T * K * (ids_type == PMOE_IDS_INT64 ? 8 : 4)))
-    return fail(PMOE_ERR_ARG, "d_logits may be logits itself, but overlaps no other input");
+  const size_t slots = (size_t)T * K, per_seq = (size_t)S * 4;
+  PMOE_TRY(check_apart({{"d_logits", d_logits, bytes}},
+                       {{"logits", d_logits == logits ? nullptr : logits, bytes},
+                        {"topk_ids", topk_ids, slots * ids_bytes(ids_type)},
+                        {"seq_offsets", seq_offsets, per_seq + 4},
+                        {"counts", d_balance ? counts : nullptr, per_seq * E},
+                        {"tokens", d_balance || d_z ? tokens : nullptr, per_seq},
+                        {"d_balance", d_balance, per_seq},
+                        {"d_z", d_z, per_seq},
+                        {"d_topk_w", d_topk_w, slots * 4}}));
   RouterGradParams p{logits, topk_ids, ids_type == PMOE_IDS_INT64, T, E, K, renormalize, seq_offsets, S,
                      counts, d_balance || d_z ? tokens : nullptr, d_balance, d_z, d_topk_w, d_logits};
   PMOE_HIP(launch_router_backward(p, static_cast<hipStream_t>(stream)));

@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <functional>
 #include <string>
 
 #include "pmoe.h"
@@ -74,6 +75,48 @@ static void adapters() {
   expect("down on another device", a.backward(), PMOE_ERR_POINTER, "down is on device 1");
 }
 
+// ---------------------------------------------------------------- router
+// An argument, and what it may not share memory with.
+static void each_shared(const char* what, std::initializer_list<void**> outputs, std::initializer_list<void**> others,
+                        const std::function<int()>& call) {
+  int i = 0;
+  for (void** o : outputs)
+    for (void** other : others) {
+      if (o == other) continue;
+      for (size_t at : {size_t(0), size_t(16)}) {
+        void* keep = *o;
+        *o = static_cast<char*>(*other) + at;
+        expect((what + (" " + std::to_string(i))).c_str(), call(), PMOE_ERR_ARG, "overlaps");
+        *o = keep;
+      }
+      ++i;
+    }
+  expect(what, call(), PMOE_OK);
+}
+
+static void router() {
+  const int T = 40, K = 2, E = 16, S = 12;  // every argument has more than 16 bytes
+  void *logits = block(0), *ids = block(1), *off = block(2), *counts = block(3), *tokens = block(4), *prob = block(5),
+       *balance = block(6), *z = block(7), *ws = block(8), *d_balance = block(9), *d_z = block(10), *d_w = block(11),
+       *d_logits = block(12);
+  each_shared("balance", {&counts, &tokens, &prob, &balance, &z, &ws},
+              {&logits, &ids, &off, &counts, &tokens, &prob, &balance, &z, &ws}, [&] {
+                return pmoe_router_balance((float*)logits, ids, PMOE_IDS_INT32, T, K, E, (int*)off, S, (int*)counts,
+                                           (int*)tokens, (float*)prob, (float*)balance, (float*)z, ws, 1 << 20, nullptr);
+              });
+  const auto backward = [&] {
+    return pmoe_router_backward((float*)logits, ids, PMOE_IDS_INT32, T, K, E, 0, (int*)off, S, (int*)counts, (int*)tokens,
+                                (float*)d_balance, (float*)d_z, (float*)d_w, (float*)d_logits, nullptr);
+  };
+  each_shared("router_backward", {&d_logits}, {&ids, &off, &counts, &tokens, &d_balance, &d_z, &d_w}, backward);
+  d_logits = static_cast<char*>(logits) + 64;
+  expect("router_backward over some logits", backward(), PMOE_ERR_ARG, "overlaps");
+  d_logits = logits;
+  expect("router_backward in place", backward(), PMOE_OK);
+  d_logits = d_w, d_balance = nullptr, counts = d_w, d_w = nullptr;  // counts are not read without d_balance
+  expect("router_backward over what it does not read", backward(), PMOE_OK);
+}
+
 // What has no bytes overlaps nothing, wherever its pointer lies.
 static void empty_ranges() {
   Adapters a;
@@ -86,6 +129,7 @@ static void empty_ranges() {
 
 int main() {
   adapters();
+  router();
   empty_ranges();
   std::printf(failures ? "refusals: %d failures\n" : "refusals: ok\n", failures);
   return failures != 0;
