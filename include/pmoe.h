@@ -522,7 +522,8 @@ int pmoe_router_backward(const float* logits, const void* topk_ids, int ids_type
  *   outside [0, R) is no route and no row is named twice (the routing names none
  *   twice; of a row named twice d_z holds one of the two);  topk_w, d_topk_w : float32 [T, K].
  * Either output may be NULL; z is needed for d_topk_w, topk_w for d_z. Rows of
- * d_z that no route names are left as they were. H must be a multiple of 8, at most 2^30.
+ * d_z that no route names are left as they were. The outputs share no memory with each
+ * other or with an input that the call reads. H must be a multiple of 8, at most 2^30.
  * Alignment: dout, z and d_z 16 bytes, others 4 bytes.
  */
 int pmoe_finalize_backward(const void* dout, const void* z, const int32_t* row_of_route,

@@ -981,10 +981,13 @@ PMOE_EXPORT int pmoe_finalize_backward(const void* dout, const void* z, const in
   if (d_z) {
     PMOE_TRY(check_ptr_here(topk_w, 4, "topk_w"));
     if (R > 0) PMOE_TRY(check_ptr_here(d_z, 16, "d_z"));
-    const size_t rows = (size_t)R * H * 2;
-    if (overlap(d_z, rows, z, rows) || overlap(d_z, rows, dout, (size_t)T * H * 2))
-      return fail(PMOE_ERR_ARG, "d_z overlaps an input");
   }
+  const size_t slots = (size_t)T * K * 4, rows = (size_t)R * H * 2;
+  PMOE_TRY(check_apart({{"d_topk_w", d_topk_w, slots}, {"d_z", d_z, rows}},
+                       {{"dout", dout, (size_t)T * H * 2},
+                        {"z", z, rows},
+                        {"row_of_route", row_of_route, slots},
+                        {"topk_w", d_z ? topk_w : nullptr, slots}}));
   PMOE_HIP(launch_finalize_backward(static_cast<const uint16_t*>(dout), static_cast<const uint16_t*>(z),
                                     row_of_route, topk_w, T, K, H, R, d_topk_w,
                                     static_cast<uint16_t*>(d_z), static_cast<hipStream_t>(stream)));

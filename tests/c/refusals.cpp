@@ -117,6 +117,17 @@ static void router() {
   expect("router_backward over what it does not read", backward(), PMOE_OK);
 }
 
+// ---------------------------------------------------------------- finalize
+static void finalize() {
+  void *dout = block(0), *z = block(1), *row = block(2), *w = block(3), *d_w = block(4), *d_z = block(5);
+  const auto call = [&] {
+    return pmoe_finalize_backward(dout, z, (int*)row, (float*)w, 40, 2, 64, 70, (float*)d_w, d_z, nullptr);
+  };
+  each_shared("finalize_backward", {&d_w, &d_z}, {&dout, &z, &row, &w, &d_w, &d_z}, call);
+  d_z = nullptr, d_w = w;  // the weights are not read without d_z
+  expect("finalize_backward over what it does not read", call(), PMOE_OK);
+}
+
 // What has no bytes overlaps nothing, wherever its pointer lies.
 static void empty_ranges() {
   Adapters a;
@@ -130,6 +141,7 @@ static void empty_ranges() {
 int main() {
   adapters();
   router();
+  finalize();
   empty_ranges();
   std::printf(failures ? "refusals: %d failures\n" : "refusals: ok\n", failures);
   return failures != 0;
