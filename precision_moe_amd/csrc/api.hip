@@ -1040,13 +1040,14 @@ PMOE_EXPORT int pmoe_adapter_forward(const void* x, const void* adapter_ids, int
   const size_t need = adapter_forward_ws_bytes(T, n, H, N, R);
   if (ws_bytes < need)
     return fail(PMOE_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
-  const size_t out_bytes = (size_t)T * N * 2, v_bytes = (size_t)T * R * 4;
-  if (overlap(v, v_bytes, out, out_bytes) || overlap(v, v_bytes, base, out_bytes) ||
-      overlap(v, v_bytes, x, (size_t)T * H * 2))
-    return fail(PMOE_ERR_ARG, "v overlaps another argument");
-  if ((base != out && overlap(out, out_bytes, base, out_bytes)) ||
-      overlap(out, out_bytes, x, (size_t)T * H * 2))
-    return fail(PMOE_ERR_ARG, "out may be base itself, but overlaps no other input");
+  const size_t out_bytes = (size_t)T * N * 2, matrix = (size_t)n * R * 2;
+  PMOE_TRY(check_apart({{"v", v, (size_t)T * R * 4}, {"out", out, out_bytes}, {"ws", ws, need}},
+                       {{"x", x, (size_t)T * H * 2},
+                        {"adapter_ids", adapter_ids, (size_t)T * ids_bytes(ids_type)},
+                        {"down", down, matrix * H},
+                        {"up", up, matrix * N},
+                        {"scale", scale, (size_t)n * 4},
+                        {"base", base == out ? nullptr : base, out_bytes}}));
   AdapterParams p{};
   p.x = x, p.ids = adapter_ids, p.ids64 = ids_type == PMOE_IDS_INT64;
   p.T = T, p.n = n, p.H = H, p.N = N, p.R = R;
@@ -1092,17 +1093,19 @@ PMOE_EXPORT int pmoe_adapter_backward(const void* dy, const void* x, const float
   const size_t need = adapter_backward_ws_bytes(T, n, H, N, R);
   if (ws_bytes < need)
     return fail(PMOE_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
-  const size_t dx_bytes = (size_t)T * H * 2;
-  if ((base != dx && overlap(dx, dx_bytes, base, dx_bytes)) || overlap(dx, dx_bytes, dy, (size_t)T * N * 2) ||
-      overlap(dx, dx_bytes, x, dx_bytes))
-    return fail(PMOE_ERR_ARG, "dx may be base itself, but overlaps no other input");
-  const size_t down_bytes = (size_t)n * R * H * 4, up_bytes = (size_t)n * R * N * 4;
-  const auto meets = [&](const void* p, size_t bytes) {
-    return overlap(d_down, down_bytes, p, bytes) || overlap(d_up, up_bytes, p, bytes);
-  };
-  if (overlap(d_down, down_bytes, d_up, up_bytes) || meets(dx, dx_bytes) || meets(dy, (size_t)T * N * 2) ||
-      meets(x, dx_bytes) || meets(v, (size_t)T * R * 4))
-    return fail(PMOE_ERR_ARG, "d_down or d_up overlaps another argument");
+  const size_t dx_bytes = (size_t)T * H * 2, matrix = (size_t)n * R * 2;
+  PMOE_TRY(check_apart({{"dx", dx, dx_bytes},
+                        {"d_down or d_up", d_down, 2 * matrix * H},
+                        {"d_down or d_up", d_up, 2 * matrix * N},
+                        {"ws", ws, need}},
+                       {{"dy", dy, (size_t)T * N * 2},
+                        {"x", d_down ? x : nullptr, dx_bytes},
+                        {"v", d_down ? v : nullptr, (size_t)T * R * 4},
+                        {"adapter_ids", adapter_ids, (size_t)T * ids_bytes(ids_type)},
+                        {"down", T > 0 ? down : nullptr, matrix * H},
+                        {"up", T > 0 ? up : nullptr, matrix * N},
+                        {"scale", scale, (size_t)n * 4},
+                        {"base", base == dx ? nullptr : base, dx_bytes}}));
   AdapterParams p{};
   p.x = x, p.ids = adapter_ids, p.ids64 = ids_type == PMOE_IDS_INT64;
   p.T = T, p.n = n, p.H = H, p.N = N, p.R = R;

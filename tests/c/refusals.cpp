@@ -51,11 +51,33 @@ static void expect(const char* what, int rc, int want, const char* message = "")
   launches = 0;
 }
 
+// An argument, and what it may not share memory with.
+static void each_shared(const char* what, std::initializer_list<void**> outputs, std::initializer_list<void**> others,
+                        const std::function<int()>& call) {
+  int i = 0;
+  for (void** o : outputs)
+    for (void** other : others) {
+      if (o == other) continue;
+      for (size_t at : {size_t(0), size_t(16)}) {
+        void* keep = *o;
+        *o = static_cast<char*>(*other) + at;
+        expect((what + (" " + std::to_string(i))).c_str(), call(), PMOE_ERR_ARG, "overlaps");
+        *o = keep;
+      }
+      ++i;
+    }
+  expect(what, call(), PMOE_OK);
+}
+
 // ---------------------------------------------------------------- adapters
 struct Adapters {
-  int T = 4, n = 2, H = 64, N = 48, R = 8;
+  int T = 40, n = 12, H = 64, N = 48, R = 8;
   void *dy = block(0), *x = block(1), *v = block(2), *ids = block(3), *down = block(4), *up = block(5),
        *scale = block(6), *base = block(7), *out = block(8), *d_down = block(9), *d_up = block(10), *ws = block(11);
+  int forward() const {
+    return pmoe_adapter_forward(x, ids, PMOE_IDS_INT32, T, n, H, N, R, down, up, (float*)scale, base, out, (float*)v, ws,
+                                1 << 24, nullptr);
+  }
   int backward() const {
     return pmoe_adapter_backward(dy, x, (float*)v, ids, PMOE_IDS_INT32, T, n, H, N, R, down, up, (float*)scale, base,
                                  out, (float*)d_down, (float*)d_up, ws, 1 << 24, nullptr);
@@ -75,25 +97,41 @@ static void adapters() {
   expect("down on another device", a.backward(), PMOE_ERR_POINTER, "down is on device 1");
 }
 
-// ---------------------------------------------------------------- router
-// An argument, and what it may not share memory with.
-static void each_shared(const char* what, std::initializer_list<void**> outputs, std::initializer_list<void**> others,
-                        const std::function<int()>& call) {
-  int i = 0;
-  for (void** o : outputs)
-    for (void** other : others) {
-      if (o == other) continue;
-      for (size_t at : {size_t(0), size_t(16)}) {
-        void* keep = *o;
-        *o = static_cast<char*>(*other) + at;
-        expect((what + (" " + std::to_string(i))).c_str(), call(), PMOE_ERR_ARG, "overlaps");
-        *o = keep;
-      }
-      ++i;
-    }
-  expect(what, call(), PMOE_OK);
+static void adapters_apart() {
+  Adapters f;
+  const auto forward = [&] { return f.forward(); };
+  each_shared("adapter_forward", {&f.v, &f.out}, {&f.x, &f.ids, &f.down, &f.up, &f.scale, &f.v, &f.out}, forward);
+  f.ws = block(11);
+  for (void** p : {&f.x, &f.ids, &f.down, &f.up, &f.scale, &f.base, &f.v, &f.out}) {
+    f.ws = *p;
+    expect("adapter_forward, ws", f.forward(), PMOE_ERR_ARG, "overlaps");
+  }
+  f.ws = block(11);
+  f.v = f.base;
+  expect("adapter_forward, v over base", f.forward(), PMOE_ERR_ARG, "overlaps");
+  f.v = block(2), f.out = static_cast<char*>(f.base) + 64;
+  expect("adapter_forward, some of base", f.forward(), PMOE_ERR_ARG, "overlaps");
+  f.out = f.base;
+  expect("adapter_forward in place", f.forward(), PMOE_OK);
+
+  Adapters b;
+  const auto backward = [&] { return b.backward(); };
+  each_shared("adapter_backward", {&b.d_down, &b.d_up},
+              {&b.dy, &b.x, &b.v, &b.ids, &b.down, &b.up, &b.scale, &b.base, &b.out, &b.d_down, &b.d_up}, backward);
+  each_shared("adapter_backward, dx", {&b.out}, {&b.dy, &b.x, &b.v, &b.ids, &b.down, &b.up, &b.scale}, backward);
+  for (void** p : {&b.dy, &b.x, &b.v, &b.ids, &b.down, &b.up, &b.scale, &b.base, &b.out, &b.d_down, &b.d_up}) {
+    b.ws = *p;
+    expect("adapter_backward, ws", b.backward(), PMOE_ERR_ARG, "overlaps");
+  }
+  b.ws = block(11), b.out = static_cast<char*>(b.base) + 64;
+  expect("adapter_backward, some of base", b.backward(), PMOE_ERR_ARG, "overlaps");
+  b.out = b.base;
+  expect("adapter_backward in place", b.backward(), PMOE_OK);
+  b.d_down = b.d_up = nullptr, b.out = b.x, b.base = nullptr;  // x and v are not read without the matrices' gradients
+  expect("adapter_backward over what it does not read", b.backward(), PMOE_OK);
 }
 
+// ---------------------------------------------------------------- router
 static void router() {
   const int T = 40, K = 2, E = 16, S = 12;  // every argument has more than 16 bytes
   void *logits = block(0), *ids = block(1), *off = block(2), *counts = block(3), *tokens = block(4), *prob = block(5),
@@ -140,6 +178,7 @@ static void empty_ranges() {
 
 int main() {
   adapters();
+  adapters_apart();
   router();
   finalize();
   empty_ranges();
