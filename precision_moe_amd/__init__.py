@@ -472,6 +472,28 @@ def routed_moe_ex(x, x_sf, x_scale, topk_ids, topk_w, weights: PreparedWeights, 
     return out
 
 
+def _adapters_beside(x, out, adapters, workspace, need):
+    """Refuses what adapter_forward on x and the layer's `out` would refuse after the layer."""
+    import torch
+    given = {**adapters, "adapter_workspace": workspace} | ({} if out is None else {"out": out})
+    for name, t in given.items():
+        if t.device != x.device:
+            raise ValueError(f"adapters and adapter_ids, out and adapter_workspace must be on the device of x: {name}")
+    if x.is_cuda and x.device.index != torch.cuda.current_device():
+        raise ValueError("x must be on the current device")
+    if workspace.numel() < need:
+        raise ValueError("adapter_workspace too small")
+    written = [(k, given[k].data_ptr(), n) for k, n in (("out", 2 * x.numel()), ("adapter_workspace", need)) if k in given]
+    read = [(k, t.data_ptr(), t.numel() * t.element_size()) for k, t in (("x", x), *adapters.items())]
+    for i, (name, at, size) in enumerate(written):
+        for other, start, length in written[i + 1:] + read:
+            if size and length and at < start + length and start < at + size:
+                raise ValueError(f"{name} overlaps {other}, which the adapters use after the layer")
+    for name, align in (("down", 16), ("up", 16), ("adapter_workspace", 256)):
+        if given[name].data_ptr() % align:
+            raise ValueError(f"{name} is not {align}-byte aligned")
+
+
 def moe_forward(x, topk_ids, topk_w, weights: PreparedWeights, recipe="per_token",
                 finalize="ordered", swiglu_limit=0.0, a1=None, a2=None, act=None, expert_offset=0,
                 workspace=None, out=None, stream=None, streams=0, step_events=None, adapters=None,
@@ -489,20 +511,16 @@ def moe_forward(x, topk_ids, topk_w, weights: PreparedWeights, recipe="per_token
     if (adapters is None) != (adapter_ids is None):
         raise ValueError("adapters and adapter_ids are wanted both or neither")
     if adapters is not None:            # refused before the layer is enqueued
-        _, _, aT, n, aH, aN, R, *on_device = _adapter_args(adapter_ids, *adapters)
+        adapter_ids, _, aT, n, aH, aN, R, *adapters = _adapter_args(adapter_ids, *adapters)
         if (aT, aH, aN) != (T, W.H, W.H):
             raise ValueError("adapters of a layer must be [n, R, H] and [n, H, R], adapter_ids [T]")
         _bf16(x, "x", (T, W.H))
         if out is not None:
             _out(out, "out", torch.bfloat16, (T, W.H), x)
-            if abs(out.data_ptr() - x.data_ptr()) < 2 * T * W.H:
-                raise ValueError("out overlaps x, which the adapters read after the layer")
-        if any(t.device != x.device for t in (adapter_ids, *on_device)):
-            raise ValueError("adapters and adapter_ids must be on the device of x")
         need = adapter_workspace_bytes(T, n, aH, aN, R)
         adapter_workspace = _scratch(need, adapter_workspace, x)
-        if adapter_workspace.numel() < need:
-            raise ValueError("adapter_workspace too small")
+        _adapters_beside(x, out, dict(zip(("adapter_ids", "down", "up", "scale"), (adapter_ids, *adapters))),
+                         adapter_workspace, need)
     topk_ids, ids_type, topk_w = _routing_args(topk_ids, topk_w)
     workspace, out = _moe_buffers(T, K, W, act, x.device, workspace, out)
     evs = _event_array(step_events)

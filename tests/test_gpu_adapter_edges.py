@@ -1,6 +1,7 @@
 """The adapter calls at the edges of what they accept: arguments that only some outputs need."""
 import pytest
 
+from helpers import dev, dev_bf16
 from test_gpu_adapter import Case, pm  # noqa: F401  (the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -15,3 +16,36 @@ def test_down_has_to_be_on_the_device_without_dx_too(pm):  # noqa: F811
         pm.adapter_backward(dy, x, v, ids, down.cpu(), up, scale, need_dx=False)
     _, d_down, d_up = pm.adapter_backward(dy, x, v, ids, down, up, scale, need_dx=False)
     assert d_down.shape == down.shape and d_up.shape == up.shape
+
+
+def test_layer_adapters_that_are_refused_leave_out_alone(pm):  # noqa: F811
+    """`out` is not written by the layer either; views and int64 ids that are accepted give the layer
+    followed by the adapter call."""
+    import torch
+    import synth
+    w = synth.WORKLOADS["tiny"]
+    P = pm.prepare_weights(*synth.all_weights(w, device="cuda"))
+    x, (tk, wt) = dev_bf16(synth.activations(w)), (dev(a) for a in synth.router(w))
+    c = Case(w.T, 3, w.H, w.H, 8)
+    down, up, scale = c.weights()
+    ids = c.d("ids").long()
+    out = torch.full((w.T, w.H), 7.0, dtype=torch.bfloat16, device="cuda")
+    shifted = torch.empty(down.numel() + 1, dtype=torch.bfloat16, device="cuda")[1:].view(down.shape)
+    for adapters in ((shifted, up, scale), (down.cpu(), up, scale)):
+        with pytest.raises(ValueError, match="aligned|on the device of x"):
+            pm.moe_forward(x, tk, wt, P, out=out, adapters=adapters, adapter_ids=ids)
+    ws = torch.empty(pm.adapter_workspace_bytes(w.T, 3, w.H, w.H, 8) + 8, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="aligned"):
+        pm.moe_forward(x, tk, wt, P, out=out, adapters=(down, up, scale), adapter_ids=ids, adapter_workspace=ws[8:])
+    torch.cuda.synchronize()
+    assert bool((out == 7).all())
+    want, _ = pm.adapter_forward(x, ids, down, up, scale, base=pm.moe_forward(x, tk, wt, P))
+    wide = torch.zeros(3, 8, 2 * w.H, dtype=torch.bfloat16, device="cuda")
+    wide[:, :, ::2] = down
+    far = torch.stack((ids, ids), 1)[:, 0]
+    side = torch.cuda.Stream()
+    for stream in (None, side):
+        got = pm.moe_forward(x, tk, wt, P, out=out, adapters=(wide[:, :, ::2], up, scale), adapter_ids=far, stream=stream)
+        torch.cuda.current_stream().wait_stream(side)
+        assert got is out and torch.equal(got.view(torch.int16), want.view(torch.int16))
+        out.fill_(7)
