@@ -353,10 +353,12 @@ __global__ __launch_bounds__(64 * kRowWaves) void balance_rows_kernel(BalancePar
 // threads, group g every groups-th slot; then the groups in order.
 __global__ __launch_bounds__(1024) void balance_sum_kernel(BalanceParams p, int rows, int quads) {
   __shared__ uint4 part[1024];
-  __shared__ float prob[kMaxExperts];
-  __shared__ int count[kMaxExperts];
+  __shared__ __align__(16) float prob[kMaxExperts];
+  __shared__ __align__(16) int count[kMaxExperts];
   __shared__ float zsh[16];
   __shared__ int nsh[16];
+  static_assert(__alignof__(part) % 16 == 0 && __alignof__(prob) % 16 == 0 && __alignof__(count) % 16 == 0,
+                "written 16 bytes at a time");
   const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int E4 = balance_e4(p.E);
   const int a = p.offsets ? min(max(p.offsets[s], 0), p.T) : 0;
