@@ -437,13 +437,16 @@ __global__ __launch_bounds__(64 * reduce_waves(16 * NR), NR <= 2 ? 4 : NR <= 4 ?
 }
 
 // ---------------------------------------------------------------- expansion to N (or H)
-// Two values as hi + lo in BF16, 16 significant bits each. An infinite value has lo = 0.
-__device__ __forceinline__ float finite_rest(float x, float hi) {
-  return __builtin_fabsf(x) == __builtin_inff() ? 0.0f : x - hi;
+// Two values as hi + lo in BF16, 16 significant bits each. What lies beyond BF16's largest value is
+// left to lo (2^120 at most, or infinity), so that hi never rounds up to an infinity that lo would
+// have to take back.
+__device__ __forceinline__ float within_bf16(float x) {
+  constexpr float kMost = 0x1.fep+127f;
+  return __builtin_amdgcn_fmed3f(x, -kMost, kMost);
 }
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = f32x2_to_bf16x2(x, y);
-  lo = f32x2_to_bf16x2(finite_rest(x, bf16_to_f32(hi & 0xFFFFu)), finite_rest(y, bf16_to_f32(hi >> 16)));
+  hi = f32x2_to_bf16x2(within_bf16(x), within_bf16(y));
+  lo = f32x2_to_bf16x2(x - bf16_to_f32(hi & 0xFFFFu), y - bf16_to_f32(hi >> 16));
 }
 
 // Rows of the low-rank vectors of a unit in LDS: the sum of the parts (in

@@ -49,3 +49,28 @@ def test_layer_adapters_that_are_refused_leave_out_alone(pm):  # noqa: F811
         torch.cuda.current_stream().wait_stream(side)
         assert got is out and torch.equal(got.view(torch.int16), want.view(torch.int16))
         out.fill_(7)
+
+
+@pytest.mark.parametrize("R", [8, 24, 64, 128])
+def test_low_rank_values_at_the_end_of_the_range(pm, R):  # noqa: F811
+    """scale * v and scale * du between BF16's largest value and FP32's (2^128 (1 - 2^-10), whose
+    nearest BF16 value would be infinite) enter the second product as finite values; infinite
+    ones give infinite results. Few bits are set in any value, so the results are exact."""
+    import torch
+
+    def zeros(*shape):
+        return torch.zeros(*shape, dtype=torch.bfloat16, device="cuda")
+    H, N = 32, 48
+    ids, r = torch.zeros(3, dtype=torch.int32, device="cuda"), R - 1
+    scale = torch.full((1,), 2.0 ** 28 * (1 - 2.0 ** -10), device="cuda")
+    x, down, up = zeros(3, H), zeros(1, R, H), zeros(1, N, R)
+    x[:, 5], down[0, r, 5], up[0, :, r] = 2.0 ** 100, 1.0, 2.0 ** -120
+    out, v = pm.adapter_forward(x, ids, down, up, scale)
+    assert bool((v[:, r] == 2.0 ** 100).all()) and bool((out == 256).all())      # 255.75 in BF16
+    x[1, 5], down[0, :, 5], up[0, :, :] = float("inf"), 1.0, 2.0 ** -120         # without inf * 0
+    out, _ = pm.adapter_forward(x, ids, down, up, scale)
+    assert bool((out[[0, 2]] == 256 * R).all()) and bool((out[1] == float("inf")).all())
+    dy, down, up = zeros(3, N), zeros(1, R, H), zeros(1, N, R)
+    dy[:, 7], up[0, 7, r], down[0, r, :] = -2.0 ** 100, 1.0, 2.0 ** -120
+    dx, _, _ = pm.adapter_backward(dy, None, None, ids, down, up, scale, need_weights=False)
+    assert bool((dx == -256).all())
