@@ -465,9 +465,10 @@ int pmoe_finalize(const void* z, const int32_t* row_of_route, const float* topk_
  * before the first or behind the last belong to none. With p = softmax(logits)
  * over all E experts, lse = log sum exp(logits), n_s the active tokens and c_se
  * the routes of sequence s to expert e:
- *   balance_s = E * sum_e c_se / (n_s K) * sum_t p_te / n_s   (1 at an even load)
+ *   balance_s = E * sum_e c_se / (n_s K) * sum_t p_te / n_s
  *   z_s       = sum_t lse_t^2 / n_s
- * and both are 0 when n_s = 0.
+ * and both are 0 when n_s = 0. balance_s is 1 at an even load of all n_s K slots;
+ * slots without an expert are in K but not in c_se.
  */
 
 #define PMOE_MAX_SEQUENCES 65536
@@ -499,7 +500,11 @@ int pmoe_router_balance(const float* logits, const void* topk_ids, int ids_type,
  *                    this rank's tokens meets the load of all)
  *   d_balance, d_z : float32 [S], gradients of the two losses, or NULL
  *   d_topk_w       : float32 [T, K], gradient of the weights of pmoe_router_topk
- *                    called with the same `renormalize`, or NULL
+ *                    called with the same `renormalize`, or NULL. With
+ *                    renormalize = 1 the weights are p over the sum of the slots that have
+ *                    an expert in topk_ids. pmoe_router_topk divides by the sum over all K: where
+ *                    a slot is dropped after it, keep the slot's id here and give it a
+ *                    zero d_topk_w
  *   d_logits       : float32 [T, E] out: the sum of the gradients that are given;
  *                    every row is written. Tokens of no sequence have no part in the
  *                    losses, but may have one in d_topk_w.

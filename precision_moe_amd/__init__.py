@@ -661,7 +661,9 @@ def router_backward(logits, topk_ids, counts=None, tokens=None, d_balance=None, 
                     renormalize=False, seq_offsets=None, out=None, stream=None):
     """Gradient of the logits (pmoe_router_backward), float32 [T, E]: from the losses of
     router_balance (d_balance, d_z float32 [S], with its counts and tokens) and from the
-    weights of router_topk (d_topk_w float32 [T, K]); at least one of the three."""
+    weights of router_topk (d_topk_w float32 [T, K]); at least one of the three. With renormalize
+    the weights are those over the slots whose id is an expert's: a slot that was dropped after
+    router_topk keeps its id here and gets a zero d_topk_w."""
     import torch
     logits, ids, ids_type, T, K, E = _router_args(logits, topk_ids)
     off, S = _sequences(seq_offsets)
