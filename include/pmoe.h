@@ -546,8 +546,10 @@ int pmoe_finalize_backward(const void* dout, const void* z, const int32_t* row_o
  * adapter of a smaller rank has zeros in the rest), 1 <= n <= 65535, T <= 2^24;
  * T*H and T*N may pass 2^31. Alignment: ws 256 bytes, ids and scale their own
  * size, everything else 16 bytes. Outputs and ws share no memory with each other
- * or with an argument that the call reads, but out (dx) may be base itself. Runs on
- * the caller's stream alone.
+ * or with an argument that the call reads, but out (dx) may be base itself. An
+ * infinite entry of x, dy, down or up makes every result that it enters infinite
+ * or NaN (FP32 factors enter products as sums of BF16 values, whose products with it
+ * may cancel). Runs on the caller's stream alone.
  */
 
 #define PMOE_ADAPTER_MAX 65535

@@ -74,3 +74,33 @@ def test_low_rank_values_at_the_end_of_the_range(pm, R):  # noqa: F811
     dy[:, 7], up[0, 7, r], down[0, r, :] = -2.0 ** 100, 1.0, 2.0 ** -120
     dx, _, _ = pm.adapter_backward(dy, None, None, ids, down, up, scale, need_weights=False)
     assert bool((dx == -256).all())
+
+
+@pytest.mark.parametrize("R", [16, 40])
+def test_infinite_entries_stay_where_they_enter(pm, R):  # noqa: F811
+    """An infinite entry of a matrix, x or dy makes every result that it enters infinite or NaN, and
+    changes no bit of the others."""
+    import torch
+    c = Case(50, 3, 64, 96, R)
+    down, up, scale = c.weights()
+    x, dy, ids = c.d("x"), c.d("dy"), c.d("ids")
+    out, v = pm.adapter_forward(x, ids, down, up, scale)
+    dx, d_down, d_up = pm.adapter_backward(dy, x, v, ids, down, up, scale)
+
+    def check(got, want, *hit):
+        touched = torch.zeros(want.shape, dtype=torch.bool, device="cuda")
+        touched[hit] = True
+        assert touched.any() and not torch.isfinite(got[touched]).any()
+        assert torch.equal(got[~touched], want[~touched])
+    mine, t = (ids == 1).nonzero()[:, 0], int((ids == 1).nonzero()[2])
+    inf = float("inf")
+    bad_up, bad_down, bad_x, bad_dy = up.clone(), down.clone(), x.clone(), dy.clone()
+    bad_up[1, 5, 3], bad_down[1, 2, 7], bad_x[t, 9], bad_dy[t, 11] = inf, -inf, inf, -inf
+    check(pm.adapter_forward(x, ids, down, bad_up, scale)[0], out, mine, 5)
+    got = pm.adapter_backward(dy, x, v, ids, bad_down, up, scale)
+    check(got[0], dx, mine, 7)
+    assert torch.equal(got[1], d_down) and torch.equal(got[2], d_up)
+    got = pm.adapter_backward(dy, bad_x, v, ids, down, up, scale)
+    check(got[1], d_down, 1, slice(None), 9)
+    assert torch.equal(got[0], dx) and torch.equal(got[2], d_up)
+    check(pm.adapter_backward(bad_dy, x, v, ids, down, up, scale)[2], d_up, 1, 11)
