@@ -299,7 +299,9 @@ def moe_workspace_layout(T, K, E, H, I, act):
 
 
 def workspace_views(ws, T, K, E, H, I, act):
-    """Typed views of the routed_moe workspace fields (for inspection in tests)."""
+    """Typed views of the routed_moe workspace fields. After moe_forward (ordered finalize) z (BF16
+    bits) and row_of_route are what finalize_backward takes, until the workspace is used again; the
+    other fields are for inspection in tests."""
     import torch
     off = moe_workspace_layout(T, K, E, H, I, act)
     TK = T * K
