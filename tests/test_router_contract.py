@@ -75,3 +75,23 @@ def test_the_two_ways_to_drop_a_slot_on_the_gpu():
         assert np.abs(got.cpu().numpy() - want).max() < 64 * 16 * 2.0 ** -24 + 1e-7
     even = pm.router_balance(torch.zeros(2, 2, device="cuda"), dev(np.array([[0, -1], [1, -1]], np.int32)))
     assert even.balance.item() == 0.5
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E", [40, 64, 256, 700])
+def test_one_expert_in_many_slots_repeats(E):
+    """32 slots of a token on two experts: the gradient is the oracle's to 64 u of the sizes and 31
+    additions, and has the same bits every time."""
+    import torch
+    import precision_moe_amd as pm
+    from helpers import dev
+    rng = np.random.default_rng(E)
+    logits, dw = rng.standard_normal((300, E)).astype(F32), rng.standard_normal((300, 32)).astype(F32)
+    ids = rng.choice(np.array([3, E - 1], np.int32), (300, 32))
+    for renorm in (False, True):
+        want, size = ot.router_backward(logits, ids, d_w=dw, renormalize=renorm)
+        args = dev(logits), dev(ids)
+        first = pm.router_backward(*args, d_topk_w=dev(dw), renormalize=renorm)
+        assert np.all(np.abs(first.cpu().numpy() - want) <= (64 + 31) * 2.0 ** -24 * size + 1e-36)
+        for _ in range(5):
+            assert torch.equal(pm.router_backward(*args, d_topk_w=dev(dw), renormalize=renorm), first)
