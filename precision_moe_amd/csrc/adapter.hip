@@ -325,7 +325,7 @@ struct Block16 {
 // Operand row i of block b is r = NR i + b, so that a lane ends with 4 NR consecutive r of
 // one token, and with kTrans a lane reads NR neighbouring columns of eight rows.
 // Bound by the latency of grouping, loads and adding up, one after the other: T = 8192, n = 6,
-// H = 7168, R = 16 takes 32 us, 117 MB at 3.7 TB/s. Loading the next 64 elements ahead gained 1%
+// H = 7168, R = 16 takes 41 us where every token has an adapter, 117 MB at 2.9 TB/s. Loading the next 64 elements ahead gained 1%
 // there and lost 6% with R = 32, for want of registers. Many adapters in mixed order read each
 // matrix once a span: T = 8192, n = 64, R = 64 takes 230 us a call. A grid with the spans of one
 // part side by side, not its parts, lost on the former (83 us a call -> 87).
@@ -491,7 +491,7 @@ static int expand_cols(int T, int D) { return (long)T * D >= 1l << 24 ? 512 : 25
 // columns 8 g .. 8 g + 7 and 32 further of one token, so that four lanes read and write 64
 // bytes at a stretch. With kTrans W_a has its columns contiguous while an operand wants eight
 // r of one column: a lane reads four columns of eight rows and turns them in registers.
-// Bound by HBM: T = 8192, n = 6, N = 7168, R = 16 takes 49 us, 235 MB at 4.8 TB/s. Fetching the
+// Bound by HBM: T = 8192, n = 6, N = 7168, R = 16 takes 50 us, 235 MB at 4.7 TB/s. Fetching the
 // next unit's rows ahead halved the waves that fit, and lost.
 template <int NR, bool kTrans, int kCols>
 __global__ __launch_bounds__(kCols) void adapter_expand_kernel(
@@ -801,7 +801,9 @@ __device__ __forceinline__ void grad_low(const GradBlock<kDown>& q, int R, const
 // every fourth step of 32 tokens, the rows of the next step on their way during one. k is the
 // token here, so both operands are wanted with eight tokens of one column: x (dy) is turned in
 // registers, du (s v) is read column by column. Bound by the latency of that chain of list, rows
-// and du: T = 1100, n = 6, H = 2064, N = 2688, R = 8 takes 11 us, where 11 MB are to be read.
+// and du, in which the list weighs most, for a thread waits for each of its 16 ids before it asks for
+// the next: T = 1100, n = 6, H = 2064, N = 2688, R = 8 takes 12 us, where 9 MB are to be read (one
+// token in seven has no adapter).
 struct GradLds {
   int list[kWindow + 64];
   int wave_count[4];
@@ -898,9 +900,10 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void adapter_grad_kernel(Grad
 // 32 tokens, four of the odd ones. The three operands of du (s v), the same for all columns,
 // are made once for the four: each wave reads and splits 16 of the 64 r and leaves them in
 // LDS, in two buffers, so that one barrier a step is enough; it waits for LDS alone, the
-// loads of the next step stay in flight. T = 4096, n = 4, H = N = 7168, R = 64 takes 50 us:
-// 22.5 GFLOP, three products to a factor, at 450 TFLOP/s (a large product: 1200), and 117 MB at
-// 2.3 TB/s; each wave waits for its own loads in turn with its products.
+// loads of the next step stay in flight. T = 4096, n = 4 runs of 1024, H = N = 7168, R = 64 takes
+// 42 us: 22.5 GFLOP, three products to a factor, at 540 TFLOP/s (a large product: 1200), and 117 MB
+// at 2.8 TB/s. Runs of random length, a fifth of the tokens without an adapter, take 51: the longest
+// share decides. Each operand is waited for before its four products, and 14 registers are spilled.
 // R = 17 .. 32 leaves half of its rows empty: T = 4096, n = 4, H = N = 7168, R = 32 takes 101 us a
 // call with it and 88 with the kernel above.
 struct GradWideLds {

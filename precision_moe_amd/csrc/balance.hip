@@ -490,8 +490,9 @@ hipError_t launch_router_balance(const BalanceParams& p, hipStream_t s) {
 
 // ---------------------------------------------------------------- backward
 // A wave takes `rows` tokens for each of its G = 64 / L groups of lanes, G at a time, and the
-// groups keep the expert shares f of their sequence in registers while it stays the same; the
-// next token is on its way while one is worked on.
+// groups keep the expert shares f of their sequence in registers while it stays the same. The
+// next token is asked for before one is worked on, but Token::load checks the range of its ids, which
+// waits for them and for the logits asked for before: only other waves' work hides that time.
 // With u_e = d_balance E / n_s f_se and a_j what the slots add at their experts,
 //   d l_e = p_e (u_e - mean + 2 d_z / n_s lse) + sum_{j: id_j = e} a_j,
 //   mean = sum_e u_e p_e + sum_j d w_j p_{id_j},  a_j = p_{id_j} d w_j,
@@ -500,7 +501,7 @@ hipError_t launch_router_balance(const BalanceParams& p, hipStream_t s) {
 // their experts through a row of LDS that is zero between tokens.
 // The logits are read once and the gradient written once, which bounds it for long batches:
 // T = 65521, E = 256, K = 8 takes 37 us a call, 138 MB at 3.7 TB/s (a large copy: 5.1). Two
-// tokens in flight, or eight rows to a wave, took 42: fewer waves fit.
+// tokens asked for ahead, or eight rows to a wave, took 42, with the same wait in them.
 template <int L, int NPL, bool kFull>
 __global__ __launch_bounds__(256) void router_grad_kernel(RouterGradParams p, int rows) {
   constexpr int G = 64 / L, kSlots = Token<L, NPL, kFull>::kSlots;
