@@ -474,8 +474,9 @@ def routed_moe_ex(x, x_sf, x_scale, topk_ids, topk_w, weights: PreparedWeights, 
     return out
 
 
-def _adapters_beside(x, out, adapters, workspace, need):
-    """Refuses what adapter_forward on x and the layer's `out` would refuse after the layer."""
+def _adapters_beside(x, out, adapters, workspace, need, layer_workspace):
+    """Refuses what adapter_forward on x and the layer's `out` would refuse after the layer, and
+    adapters that the layer would overwrite: layer_workspace is None or (tensor, bytes it uses)."""
     import torch
     given = {**adapters, "adapter_workspace": workspace} | ({} if out is None else {"out": out})
     for name, t in given.items():
@@ -491,6 +492,11 @@ def _adapters_beside(x, out, adapters, workspace, need):
         for other, start, length in written[i + 1:] + read:
             if size and length and at < start + length and start < at + size:
                 raise ValueError(f"{name} overlaps {other}, which the adapters use after the layer")
+    if layer_workspace is not None:     # it may be the adapters' workspace too, one after the other
+        at, size = layer_workspace[0].data_ptr(), layer_workspace[1]
+        for other, start, length in read[1:]:
+            if length and at < start + length and start < at + size:
+                raise ValueError(f"workspace overlaps {other}, which the adapters use after the layer")
     for name, align in (("down", 16), ("up", 16), ("adapter_workspace", 256)):
         if given[name].data_ptr() % align:
             raise ValueError(f"{name} is not {align}-byte aligned")
@@ -522,7 +528,8 @@ def moe_forward(x, topk_ids, topk_w, weights: PreparedWeights, recipe="per_token
         need = adapter_workspace_bytes(T, n, aH, aN, R)
         adapter_workspace = _scratch(need, adapter_workspace, x)
         _adapters_beside(x, out, dict(zip(("adapter_ids", "down", "up", "scale"), (adapter_ids, *adapters))),
-                         adapter_workspace, need)
+                         adapter_workspace, need,
+                         None if workspace is None else (workspace, moe_workspace_bytes(T, K, W.E, W.H, W.I, act)))
     topk_ids, ids_type, topk_w = _routing_args(topk_ids, topk_w)
     workspace, out = _moe_buffers(T, K, W, act, x.device, workspace, out)
     evs = _event_array(step_events)

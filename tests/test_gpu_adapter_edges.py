@@ -104,3 +104,41 @@ def test_infinite_entries_stay_where_they_enter(pm, R):  # noqa: F811
     check(got[1], d_down, 1, slice(None), 9)
     assert torch.equal(got[0], dx) and torch.equal(got[2], d_up)
     check(pm.adapter_backward(bad_dy, x, v, ids, down, up, scale)[2], d_up, 1, 11)
+
+
+def test_one_workspace_for_the_layer_and_its_adapters(pm):  # noqa: F811
+    """The adapters run after the layer, so both may use one workspace; no tokens are a call too; and
+    captured, the whole call replays to the eager bits."""
+    import torch
+    import synth
+    w = synth.WORKLOADS["tiny"]
+    P = pm.prepare_weights(*synth.all_weights(w, device="cuda"))
+    x, (tk, wt) = dev_bf16(synth.activations(w)), (dev(a) for a in synth.router(w))
+    c = Case(w.T, 3, w.H, w.H, 8)
+    adapters, ids = c.weights(), c.d("ids")
+    want = pm.moe_forward(x, tk, wt, P, adapters=adapters, adapter_ids=ids)
+    need = max(pm.moe_workspace_bytes(w.T, w.K, w.E, w.H, w.I, P.act), pm.adapter_workspace_bytes(w.T, 3, w.H, w.H, 8))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(want)
+
+    def call():
+        out.fill_(7)
+        pm.moe_forward(x, tk, wt, P, adapters=adapters, adapter_ids=ids, workspace=ws, adapter_workspace=ws, out=out)
+    call()
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    none = pm.moe_forward(x[:0], tk[:0], wt[:0], P, adapters=adapters, adapter_ids=ids[:0])
+    assert none.shape == (0, w.H)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for i in range(3):
+        out.fill_(i)
+        ws.fill_(i)
+        assert torch.equal(pm.adapter_forward(x, ids, *adapters)[0], pm.adapter_forward(x, ids, *adapters)[0])
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16)), i
+    del g
+    torch.cuda.synchronize()

@@ -28,12 +28,12 @@ def args():
                 ws=_aligned(pm.adapter_workspace_bytes(T, n, H, H, R)))
 
 
-def _refused(args, match):
+def _refused(args, match, workspace=None):
     P = pm.PreparedWeights(E, H, H, H, *([None] * 6))
     with pytest.raises(ValueError, match=match):
         pm.moe_forward(args["x"], torch.zeros(T, K, dtype=I32), torch.zeros(T, K), P, out=args["out"],
                        adapters=(args["down"], args["up"], args["scale"]), adapter_ids=args["ids"],
-                       adapter_workspace=args["ws"])
+                       adapter_workspace=args["ws"], workspace=workspace)
 
 
 @pytest.mark.parametrize("name", ["x", "down", "up", "scale", "ids"])
@@ -50,6 +50,14 @@ def test_workspace_over_an_argument(args, name):
     t = args[name]
     args[name] = _as(args["ws"], t.dtype, *t.shape)
     _refused(args, "overlaps")
+
+
+@pytest.mark.parametrize("name", ["down", "up", "scale", "ids"])
+def test_layer_workspace_over_what_the_adapters_read(args, name):
+    ws = _aligned(pm.moe_workspace_bytes(T, K, E, H, H, pm.ACT_RELU2))
+    t = args[name]
+    args[name] = _as(ws[256:], t.dtype, *t.shape)
+    _refused(args, "workspace overlaps", workspace=ws)
 
 
 @pytest.mark.parametrize("name", ["down", "up", "ws"])
