@@ -580,10 +580,10 @@ int pmoe_adapter_forward(const void* x, const void* adapter_ids, int ids_type, i
  *   dy : BF16 [T, N];  x, v as in the forward call;  base : BF16 [T, H], the gradient
  *   that dx adds to, or NULL (zeros);  dx : BF16 [T, H], may be base itself.
  * dx may be NULL (x has no gradient), or d_down and d_up both (the adapters are
- * not trained; x and v are then not read). down and up are read either way. d_down and d_up are written whole,
- * zeros for adapters without tokens, and their sums over tokens are taken in a
- * fixed order; an infinite v or du makes the entries that it enters NaN. The
- * gradient of base is dy itself.
+ * not trained; x and v are then not read). down and up are read either way. d_down
+ * and d_up are written whole, zeros for adapters without tokens, and their sums over
+ * tokens are taken in a fixed order; an infinite v or du makes the entries that it
+ * enters NaN. The gradient of base is dy itself.
  */
 int pmoe_adapter_backward(const void* dy, const void* x, const float* v, const void* adapter_ids,
                           int ids_type, int T, int n, int H, int N, int R, const void* down,

@@ -325,10 +325,11 @@ struct Block16 {
 // Operand row i of block b is r = NR i + b, so that a lane ends with 4 NR consecutive r of
 // one token, and with kTrans a lane reads NR neighbouring columns of eight rows.
 // Bound by the latency of grouping, loads and adding up, one after the other: T = 8192, n = 6,
-// H = 7168, R = 16 takes 41 us where every token has an adapter, 117 MB at 2.9 TB/s. Loading the next 64 elements ahead gained 1%
-// there and lost 6% with R = 32, for want of registers. Many adapters in mixed order read each
-// matrix once a span: T = 8192, n = 64, R = 64 takes 230 us a call. A grid with the spans of one
-// part side by side, not its parts, lost on the former (83 us a call -> 87).
+// H = 7168, R = 16 takes 41 us where every token has an adapter, 117 MB at 2.9 TB/s. Loading the
+// next 64 elements ahead gained 1% there and lost 6% with R = 32, for want of registers. Many
+// adapters in mixed order read each matrix once a span: T = 8192, n = 64, R = 64 takes 230 us a
+// call. A grid with the spans of one part side by side, not its parts, lost on the former (83 us a
+// call -> 87).
 template <int NR, bool kTrans>
 __global__ __launch_bounds__(64 * reduce_waves(16 * NR), NR <= 2 ? 4 : NR <= 4 ? 3 : 2) void adapter_reduce_kernel(
     const uint16_t* __restrict__ in, const void* __restrict__ ids, int ids64, int T, int n, int D, int R,
