@@ -590,6 +590,137 @@ int pmoe_adapter_backward(const void* dy, const void* x, const float* v, const v
                           const void* up, const float* scale, const void* base, void* dx,
                           float* d_down, float* d_up, void* ws, size_t ws_bytes, void* stream);
 
+/* ============================================================ tokens sorted by expert
+ *
+ * The order that pmoe_routed_moe gives its routes inside its workspace, for
+ * callers that run the experts' products themselves: the rows of an expert follow
+ * ascending route index f = t*K + j. The way back with the weights applied is
+ * pmoe_finalize, its gradient pmoe_finalize_backward.
+ */
+
+/* Device workspace of pmoe_permute_tokens (bytes). 0 on bad shapes. */
+size_t pmoe_permute_workspace_bytes(int T, int K, int E);
+
+/*
+ *   topk_ids       : [T, K] int32 or int64 (ids_type); a route is valid iff
+ *                    expert_offset <= id < expert_offset + E, others have no row
+ *   x              : [T] rows of row_bytes bytes, of any type, or NULL: only the
+ *                    order is wanted (rows is NULL too, row_bytes unused)
+ *   rows           : [T*K] rows of row_bytes bytes out; row row_of_route[t*K+j] is token
+ *                    t's. Rows behind the last valid one are left as they were
+ *   row_of_route   : int32 [T*K] out, -1 where the route has no row
+ *   route_of_row   : int32 [T*K] out, the valid rows; behind them left as it was
+ *   expert_offsets : int32 [E+1] out, first row of each expert; [E] = valid rows
+ * T = 0 writes zeros to expert_offsets. 1 <= E <= 1024, 1 <= K <= min(32, E),
+ * T*K < 2^30, row_bytes a positive multiple of 16, at most 2^20. Outputs and ws share no
+ * memory with each other or with an input. Alignment: x and rows 16 bytes, ws
+ * 256, int64 ids 8, others 4.
+ */
+int pmoe_permute_tokens(const void* topk_ids, int ids_type, int T, int K, int E, int expert_offset,
+                        const void* x, int row_bytes, void* rows, int32_t* row_of_route,
+                        int32_t* route_of_row, int32_t* expert_offsets, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* Element types of the entry points below. */
+#define PMOE_BF16 0
+#define PMOE_F32 1
+
+/*
+ * Gradient of the copy: dx[t] = sum over j of d_rows[row_of_route[t*K+j]], in FP32,
+ * slot order, rounded once; +0 for a token without a row. A value of row_of_route
+ * outside [0, R) is no row.
+ *   d_rows : BF16 or FP32 (type) [R, H];  row_of_route : int32 [T*K];  dx : as d_rows,
+ *   [T, H].  1 <= K <= 32, T*K < 2^30, H a multiple of 8 (FP32: 4), at most 2^18.
+ * dx shares no memory with the inputs. Alignment: d_rows and dx 16 bytes.
+ */
+int pmoe_permute_tokens_backward(const void* d_rows, int type, const int32_t* row_of_route, int T, int K,
+                                 int R, int H, void* dx, void* stream);
+
+/* ============================================================ microscaled formats
+ *
+ * Blocks of 32 consecutive elements of a row share one power of two X, stored as
+ * its exponent + 127 in a byte (E8M0, 255 = NaN); the conversion is that of the
+ * OCP Microscaling Formats specification v1.0, section 6.3:
+ *   X = 2^max(floor(log2(amax of the block)) - emax, -127),
+ *   element = x / X rounded to nearest, ties to the even code, saturating;
+ * emax is 2 and the largest element 6 for E2M1 (codes packed two per byte, element
+ * 2i in the low nibble), 8 and 448 for E4M3. A block of zeros has byte 0; a
+ * negative value that rounds to 0 keeps its sign. A block with an infinity or a NaN has
+ * byte 255 and zero codes, and reads back as NaN. Rows are contiguous, their
+ * length n a multiple of 32: codes [rows, n/2] (E4M3: [rows, n]), scales [rows, n/32].
+ */
+#define PMOE_MX_E2M1 0
+#define PMOE_MX_E4M3 1
+
+/* x BF16 or FP32 [rows, n] -> codes, scales. Codes and scales share no memory with
+ * each other or x. 0 <= rows, n <= 2^30, rows*n < 2^40. Alignment: x and codes 16 bytes. */
+int pmoe_mx_quantize(const void* x, int type, int format, long long rows, int n, void* codes, void* scales,
+                     void* stream);
+
+/* The values that codes and scales stand for, rounded once to BF16 or FP32 (exact but where
+ * they exceed the type). Sizes and alignment as above; out shares no memory with the inputs. */
+int pmoe_mx_dequantize(const void* codes, const void* scales, int format, long long rows, int n, int type,
+                       void* out, void* stream);
+
+/*
+ * Grouped product of expert-sorted MXFP4 rows with MXFP4 matrices:
+ *   out[r] = W[e] a[src(r)],  e the expert of row r:  expert_offsets[e] <= r < expert_offsets[e+1]
+ * with src(r) = route_of_row[r] / topk (a holds tokens), or r without route_of_row
+ * (a holds the rows). E = 1 is one plain product.
+ *   a_codes, a_sf  : E2M1 codes and scales of [a_rows, Kd]; a_rows >= R without route_of_row
+ *   route_of_row   : int32 [R] or NULL; a row whose source is outside [0, a_rows) gets zeros
+ *   expert_offsets : int32 [E+1] on the device, ascending, within [0, R]; rows of no
+ *                    expert (behind the last, say) are left as they were
+ *   w_codes, w_sf  : E2M1 codes [E, N, Kd/2] and scales [E, N, Kd/32] (pmoe_mx_quantize of [E*N, Kd])
+ *   out            : BF16 or FP32 (out_type) [R, N]
+ * Products are exact, sums FP32; each output is one chain of sums whose order
+ * depends on Kd alone, so that a row's bits do not depend on the other rows. A
+ * block that reads as NaN makes every output that it enters NaN.
+ * 1 <= E <= 1024, 0 <= R <= PMOE_MX_MAX_ROWS, N a multiple of 16 up to 32768, Kd a multiple of
+ * 32 up to 16384, topk >= 1; with route_of_row a_rows * Kd < 2^32 - 512. out shares no memory
+ * with an input. Alignment: codes and out 16 bytes, scales 4 where Kd is a multiple of 128, others 4.
+ */
+#define PMOE_MX_MAX_ROWS (1 << 23)
+int pmoe_mx_grouped_gemm(const void* a_codes, const void* a_sf, int a_rows, const int32_t* route_of_row,
+                         int topk, const int32_t* expert_offsets, int R, int E, const void* w_codes,
+                         const void* w_sf, int N, int Kd, void* out, int out_type, void* stream);
+
+/*
+ * Gradient of the rows of that product, the quantization of the rows passed
+ * through: dx[r] = W[e]^T dy[r], dy BF16 [R, N], dx BF16 [R, Kd], FP32 sums rounded once.
+ * Other arguments, limits and rows of no expert as above (for the tokens of a
+ * gathered product: pmoe_permute_tokens_backward of dx).
+ */
+int pmoe_mx_grouped_gemm_backward(const void* dy, const int32_t* expert_offsets, int R, int E,
+                                  const void* w_codes, const void* w_sf, int N, int Kd, void* dx,
+                                  void* stream);
+
+/*
+ * The activation between two such products, with an 8-bit checkpoint of its input
+ * for the backward pass.
+ *   y         : BF16 [R, I] (act PMOE_ACT_RELU2: h = max(y, 0)^2) or [R, 2I], gate then up
+ *               (PMOE_ACT_SWIGLU: h = silu(gate) * up; with swiglu_limit L > 0 on
+ *               gate <= L and -L <= up <= L)
+ *   row_count : int32 on the device, or NULL: only rows below it are read and written
+ *               (expert_offsets + E, say)
+ *   hq, h_sf  : E2M1 codes [R, I/2] and scales [R, I/32] of h. They are those of the exact h,
+ *               not of its FP32 rounding; h beyond FP32's largest counts as infinite
+ *   y8, y8_sf : E4M3 codes and scales of y, rows as y's, or both NULL: no checkpoint
+ * swiglu_limit is 0 (none) or positive, 0 for squared ReLU. 0 <= R <= PMOE_MX_MAX_ROWS, I a
+ * multiple of 32 up to 16384. Outputs share no memory with each other or an input.
+ * Alignment: y, hq and y8 16 bytes, row_count 4.
+ */
+int pmoe_mx_activation(const void* y, int R, int I, int act, float swiglu_limit, const int32_t* row_count,
+                       void* hq, void* h_sf, void* y8, void* y8_sf, void* stream);
+
+/*
+ * Gradient of y at the values that its checkpoint stands for, the quantization of
+ * h passed through: dy from dh BF16 [R, I], in FP32, rounded to BF16 once. Where the clamp
+ * cuts gate or up off, their gradient is 0 (at the limit itself it is not).
+ */
+int pmoe_mx_activation_backward(const void* dh, const void* y8, const void* y8_sf, int R, int I, int act,
+                                float swiglu_limit, const int32_t* row_count, void* dy, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

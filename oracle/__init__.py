@@ -29,6 +29,9 @@ Modules:
              the fused (order-free) finalize.
   train   -- the router's balance loss and gradients, the gradients of the
              finalize, and low-rank adapters with theirs.
+  mx      -- microscaled formats, the grouped product of MXFP4 operands and its
+             gradient, the activation with its 8-bit checkpoint, and tokens
+             sorted by expert.
 
 Parity pins: every function here is pinned by a CPU test against something
 other than itself (hand enumerations, a library cast, brute force, closed

@@ -19,6 +19,8 @@ ACT_RELU2, ACT_SWIGLU = 0, 1
 IDS_INT32, IDS_INT64 = 0, 1
 RECIPE_PER_TOKEN, RECIPE_PER_TENSOR, RECIPE_W4A16 = 0, 1, 2
 FINALIZE_ORDERED, FINALIZE_FUSED = 0, 1
+MX_E2M1, MX_E4M3 = 0, 1
+_MX_FORMATS = {"e2m1": MX_E2M1, "e4m3": MX_E4M3}
 _RECIPES = {"per_token": RECIPE_PER_TOKEN, "per_tensor": RECIPE_PER_TENSOR, "w4a16": RECIPE_W4A16}
 _FINALIZE = {"ordered": FINALIZE_ORDERED, "fused": FINALIZE_FUSED}
 WS_FIELDS = ("row_of_route", "route_of_row", "expert_offsets", "counters", "h", "hq", "h_sf",
@@ -78,6 +80,16 @@ _SIGNATURES = {
                                   ctypes.c_size_t, _vp]),
     "pmoe_adapter_backward": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp,
                                    _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "pmoe_permute_workspace_bytes": (ctypes.c_size_t, [_i, _i, _i]),
+    "pmoe_permute_tokens": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t,
+                                 _vp]),
+    "pmoe_permute_tokens_backward": (_i, [_vp, _i, _vp, _i, _i, _i, _i, _vp, _vp]),
+    "pmoe_mx_quantize": (_i, [_vp, _i, _i, ctypes.c_longlong, _i, _vp, _vp, _vp]),
+    "pmoe_mx_dequantize": (_i, [_vp, _vp, _i, ctypes.c_longlong, _i, _i, _vp, _vp]),
+    "pmoe_mx_grouped_gemm": (_i, [_vp, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _vp, _i, _i, _vp, _i, _vp]),
+    "pmoe_mx_grouped_gemm_backward": (_i, [_vp, _vp, _i, _i, _vp, _vp, _i, _i, _vp, _vp]),
+    "pmoe_mx_activation": (_i, [_vp, _i, _i, _i, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "pmoe_mx_activation_backward": (_i, [_vp, _vp, _vp, _i, _i, _i, ctypes.c_float, _vp, _vp, _vp]),
 }
 STEP_ROUTE, STEP_FC1, STEP_REQUANT, STEP_FC2, STEP_FINALIZE = range(5)
 
@@ -779,3 +791,224 @@ def adapter_backward(dy, x, v, adapter_ids, down, up, scale, base=None, need_dx=
         _ptr(base), _ptr(dx), _ptr(d_down), _ptr(d_up), _ptr(ws), ws.numel(),
         _stream(stream, dy, x, v, ids, down, up, scale, base, dx, d_down, d_up, ws)))
     return dx, d_down, d_up
+
+
+# ----------------------------------------------------------------------------- tokens sorted by expert
+PermutedTokens = namedtuple("PermutedTokens", "rows row_of_route route_of_row expert_offsets")
+
+
+def _type(dtype, name):
+    """PMOE_BF16 or PMOE_F32."""
+    import torch
+    if dtype is torch.bfloat16:
+        return 0
+    if dtype is torch.float32:
+        return 1
+    raise TypeError(f"{name} must be bfloat16 or float32")
+
+
+def permute_workspace_bytes(T, K, E):
+    size = lib().pmoe_permute_workspace_bytes(T, K, E)
+    if size == 0:
+        raise PmoeError(3, lib().pmoe_last_error().decode())
+    return int(size)
+
+
+def permute_tokens(x, topk_ids, E, expert_offset=0, out=None, workspace=None, stream=None):
+    """Routes sorted by expert, and each token copied to its routes' rows (pmoe_permute_tokens).
+
+    x [T, H], of any type whose rows are a multiple of 16 bytes, or None for the order alone;
+    topk_ids [T, K] int32 or int64, ids outside [expert_offset, expert_offset + E) have no row.
+    Returns PermutedTokens(rows [T*K, H] or None, row_of_route int32 [T*K] (-1: no row), route_of_row
+    int32 [T*K], expert_offsets int32 [E+1]); rows and route_of_row behind row expert_offsets[E]
+    are left as they were, in fresh tensors uninitialised. out, a PermutedTokens or 4-tuple, any of
+    its entries None, is written in place."""
+    import torch
+    if topk_ids.dim() != 2 or (x is not None and (x.dim() != 2 or x.shape[0] != topk_ids.shape[0])):
+        raise ValueError("topk_ids must be [T, K] and x [T, H]")
+    T, K = topk_ids.shape
+    ids, ids_type = _ids(topk_ids, "topk_ids")
+    rows, row, route, offsets = out if out is not None else (None,) * 4
+    if x is not None:
+        x = x.contiguous()
+        rows = _out(rows, "rows", x.dtype, (T * K, x.shape[1]), x)
+    elif rows is not None:
+        raise ValueError("rows needs x")
+    i32 = torch.int32
+    res = PermutedTokens(rows, _out(row, "row_of_route", i32, (T * K,), ids),
+                         _out(route, "route_of_row", i32, (T * K,), ids),
+                         _out(offsets, "expert_offsets", i32, (E + 1,), ids))
+    ws = _scratch(lib().pmoe_permute_workspace_bytes(T, K, E), workspace, ids)
+    _check(lib().pmoe_permute_tokens(
+        _ptr(ids), ids_type, T, K, E, expert_offset, _ptr(x), 0 if x is None else x.shape[1] * x.element_size(),
+        *(_ptr(t) for t in res), _ptr(ws), ws.numel(), _stream(stream, ids, x, ws, *res)))
+    return res
+
+
+def permute_tokens_backward(d_rows, row_of_route, K, out=None, stream=None):
+    """Gradient of permute_tokens (pmoe_permute_tokens_backward): dx [T, H], the FP32 sum of d_rows
+    [R, H] (BF16 or FP32, dx too) over the K slots of each token; row_of_route int32 [T*K], values
+    outside [0, R) are no rows."""
+    import torch
+    if d_rows.dim() != 2 or K < 1 or row_of_route.numel() % K:
+        raise ValueError("d_rows must be [R, H] and row_of_route [T*K]")
+    R, H = d_rows.shape
+    T = row_of_route.numel() // K
+    kind = _type(d_rows.dtype, "d_rows")
+    d_rows = d_rows.contiguous()
+    row = _is(row_of_route.reshape(-1), "row_of_route", torch.int32, (T * K,))
+    out = _out(out, "out", d_rows.dtype, (T, H), d_rows)
+    _check(lib().pmoe_permute_tokens_backward(_ptr(d_rows), kind, _ptr(row), T, K, R, H, _ptr(out),
+                                              _stream(stream, d_rows, row, out)))
+    return out
+
+
+# ----------------------------------------------------------------------------- microscaled formats
+def _mx_format(format):
+    if format not in _MX_FORMATS:
+        raise ValueError("format must be 'e2m1' or 'e4m3'")
+    return _MX_FORMATS[format]
+
+
+def _mx_pair(codes, scales, name, shape, fmt=MX_E2M1):
+    """Codes and scales of a tensor of `shape`, checked."""
+    import torch
+    *lead, n = shape
+    per = 2 if fmt == MX_E2M1 else 1
+    return (_is(codes, f"codes of {name}", torch.uint8, (*lead, n // per)),
+            _is(scales, f"scales of {name}", torch.uint8, (*lead, n // 32)))
+
+
+def mx_quantize(x, format="e2m1", out=None, stream=None):
+    """Microscaled quantization (pmoe_mx_quantize) of x BF16 or FP32 [..., n], n a multiple of 32:
+    (codes uint8 [..., n/2] packed E2M1 or [..., n] E4M3, scales uint8 [..., n/32], E8M0)."""
+    import torch
+    fmt, kind = _mx_format(format), _type(x.dtype, "x")
+    if x.dim() < 1 or x.shape[-1] % 32:
+        raise ValueError("the last dimension of x must be a multiple of 32")
+    x = x.contiguous()
+    *lead, n = x.shape
+    codes, scales = out if out is not None else (None, None)
+    codes = _out(codes, "codes", torch.uint8, (*lead, n // 2 if fmt == MX_E2M1 else n), x)
+    scales = _out(scales, "scales", torch.uint8, (*lead, n // 32), x)
+    _check(lib().pmoe_mx_quantize(_ptr(x), kind, fmt, x.numel() // n if n else 0, n, _ptr(codes), _ptr(scales),
+                                  _stream(stream, x, codes, scales)))
+    return codes, scales
+
+
+def mx_dequantize(codes, scales, format="e2m1", dtype=None, out=None, stream=None):
+    """The values of microscaled codes and scales (pmoe_mx_dequantize), BF16 unless dtype is
+    torch.float32."""
+    import torch
+    fmt = _mx_format(format)
+    dtype = torch.bfloat16 if dtype is None else dtype
+    kind = _type(dtype, "dtype")
+    if codes.dim() < 1:
+        raise ValueError("codes must be [..., n/2] (E4M3: [..., n])")
+    n = codes.shape[-1] * (2 if fmt == MX_E2M1 else 1)
+    shape = (*codes.shape[:-1], n)
+    codes, scales = _mx_pair(codes, scales, "the input", shape, fmt)
+    out = _out(out, "out", dtype, shape, codes)
+    _check(lib().pmoe_mx_dequantize(_ptr(codes), _ptr(scales), fmt, out.numel() // n if n else 0, n, kind, _ptr(out),
+                                    _stream(stream, codes, scales, out)))
+    return out
+
+
+def _mx_matrices(w, w_sf, expert_offsets):
+    """(w, w_sf, offsets, E, N, Kd) of quantized expert matrices [E, N, Kd], checked."""
+    import torch
+    if w.dim() != 3:
+        raise ValueError("w must be [E, N, Kd/2]")
+    E, N, Kd = w.shape[0], w.shape[1], 2 * w.shape[2]
+    w, w_sf = _mx_pair(w, w_sf, "w", (E, N, Kd))
+    return w, w_sf, _is(expert_offsets, "expert_offsets", torch.int32, (E + 1,)), E, N, Kd
+
+
+def mx_grouped_gemm(a, a_sf, w, w_sf, expert_offsets, route_of_row=None, topk=1, dtype=None, out=None, stream=None):
+    """Grouped product of MXFP4 rows with MXFP4 expert matrices (pmoe_mx_grouped_gemm): out [R, N] BF16
+    (or dtype torch.float32), row r of expert e (expert_offsets int32 [E+1]) times w[e].
+
+    a uint8 [rows, Kd/2], a_sf uint8 [rows, Kd/32]: the rows themselves (R = rows), or, with
+    route_of_row int32 [R] and topk, tokens, of which row r reads number route_of_row[r] // topk.
+    w uint8 [E, N, Kd/2], w_sf uint8 [E, N, Kd/32], as mx_quantize gives them. Rows of no expert are
+    left as they were (in a fresh out uninitialised)."""
+    import torch
+    w, w_sf, offsets, E, N, Kd = _mx_matrices(w, w_sf, expert_offsets)
+    if a.dim() != 2:
+        raise ValueError("a must be [rows, Kd/2]")
+    a, a_sf = _mx_pair(a, a_sf, "a", (a.shape[0], Kd))
+    if route_of_row is None:
+        route, R = None, a.shape[0]
+    else:
+        route = _is(route_of_row, "route_of_row", torch.int32, (route_of_row.numel(),))
+        R = route.shape[0]
+    dtype = (out.dtype if out is not None else torch.bfloat16) if dtype is None else dtype
+    kind = _type(dtype, "out")
+    out = _out(out, "out", dtype, (R, N), a)
+    _check(lib().pmoe_mx_grouped_gemm(
+        _ptr(a), _ptr(a_sf), a.shape[0], _ptr(route), topk, _ptr(offsets), R, E, _ptr(w), _ptr(w_sf), N, Kd, _ptr(out),
+        kind, _stream(stream, a, a_sf, route, offsets, w, w_sf, out)))
+    return out
+
+
+def mx_grouped_gemm_backward(dy, w, w_sf, expert_offsets, out=None, stream=None):
+    """Gradient of the rows of mx_grouped_gemm (pmoe_mx_grouped_gemm_backward): dx BF16 [R, Kd] from dy
+    BF16 [R, N]; rows of no expert are left as they were. For the tokens of a gathered product:
+    permute_tokens_backward of dx."""
+    import torch
+    w, w_sf, offsets, E, N, Kd = _mx_matrices(w, w_sf, expert_offsets)
+    if dy.dim() != 2:
+        raise ValueError("dy must be [R, N]")
+    R = dy.shape[0]
+    dy = _bf16(dy, "dy", (R, N))
+    out = _out(out, "out", torch.bfloat16, (R, Kd), dy)
+    _check(lib().pmoe_mx_grouped_gemm_backward(_ptr(dy), _ptr(offsets), R, E, _ptr(w), _ptr(w_sf), N, Kd, _ptr(out),
+                                               _stream(stream, dy, offsets, w, w_sf, out)))
+    return out
+
+
+def _row_count(t):
+    import torch
+    return None if t is None else _is(t.reshape(-1), "row_count", torch.int32, (1,))
+
+
+def mx_activation(y, act, swiglu_limit=0.0, checkpoint=False, row_count=None, out=None, stream=None):
+    """Squared ReLU or SwiGLU of y BF16 [R, I] (SwiGLU: [R, 2I], gate then up) into MXFP4, with an 8-bit
+    checkpoint of y (pmoe_mx_activation): (hq uint8 [R, I/2], h_sf uint8 [R, I/32], y8 uint8 as y (E4M3),
+    y8_sf uint8 [R, .../32]); the last two are None without `checkpoint`. row_count: a device int32
+    (expert_offsets[-1:], say), only rows below it are read and written. out = (hq, h_sf, y8, y8_sf),
+    any of them None, is written in place."""
+    import torch
+    if y.dim() != 2:
+        raise ValueError("y must be [R, I] or [R, 2I]")
+    R, W = y.shape
+    if act == ACT_SWIGLU and W % 2:
+        raise ValueError("SwiGLU needs y [R, 2I]")
+    I = W // 2 if act == ACT_SWIGLU else W
+    y = _bf16(y, "y", (R, W))
+    count = _row_count(row_count)
+    hq, h_sf, y8, y8_sf = out if out is not None else (None,) * 4
+    u8 = torch.uint8
+    hq, h_sf = _out(hq, "hq", u8, (R, I // 2), y), _out(h_sf, "h_sf", u8, (R, I // 32), y)
+    y8 = _out(y8, "y8", u8, (R, W), y) if checkpoint else None
+    y8_sf = _out(y8_sf, "y8_sf", u8, (R, W // 32), y) if checkpoint else None
+    _check(lib().pmoe_mx_activation(_ptr(y), R, I, act, float(swiglu_limit), _ptr(count), _ptr(hq), _ptr(h_sf),
+                                    _ptr(y8), _ptr(y8_sf), _stream(stream, y, count, hq, h_sf, y8, y8_sf)))
+    return hq, h_sf, y8, y8_sf
+
+
+def mx_activation_backward(dh, y8, y8_sf, act, swiglu_limit=0.0, row_count=None, out=None, stream=None):
+    """Gradient dy BF16 [R, I or 2I] of mx_activation from dh BF16 [R, I] and the checkpoint
+    (pmoe_mx_activation_backward)."""
+    import torch
+    if dh.dim() != 2:
+        raise ValueError("dh must be [R, I]")
+    R, I = dh.shape
+    W = 2 * I if act == ACT_SWIGLU else I
+    dh = _bf16(dh, "dh", (R, I))
+    y8, y8_sf = _mx_pair(y8, y8_sf, "the checkpoint", (R, W), MX_E4M3)
+    count = _row_count(row_count)
+    out = _out(out, "out", torch.bfloat16, (R, W), dh)
+    _check(lib().pmoe_mx_activation_backward(_ptr(dh), _ptr(y8), _ptr(y8_sf), R, I, act, float(swiglu_limit),
+                                             _ptr(count), _ptr(out), _stream(stream, dh, y8, y8_sf, count, out)))
+    return out

@@ -14,7 +14,7 @@ BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libpmoe.so")
 SOURCES = ["api.hip", "quantize.hip", "weights.hip", "route.hip", "gemm.hip", "finalize.hip",
-           "router.hip", "balance.hip", "adapter.hip"]
+           "router.hip", "balance.hip", "adapter.hip", "permute.hip", "mx_quantize.hip", "mx_gemm.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -1141,3 +1141,291 @@ PMOE_EXPORT int pmoe_finalize(const void* z, const int32_t* row_of_route, const 
                            static_cast<uint16_t*>(out), static_cast<hipStream_t>(stream)));
   return ok();
 }
+
+// ------------------------------------------------------------------ tokens sorted by expert
+namespace {
+
+int check_permute_shape(int T, int K, int E) {
+  if (T < 0) return fail(PMOE_ERR_SHAPE, "T must be >= 0");
+  if (E < 1 || E > kMaxExperts) return fail(PMOE_ERR_SHAPE, "E must be in [1, 1024]");
+  if (K < 1 || K > 32 || K > E) return fail(PMOE_ERR_SHAPE, "K must be in [1, min(32, E)]");
+  if ((long long)T * K >= (1LL << 31) / 2) return fail(PMOE_ERR_SHAPE, "T*K too large");
+  return PMOE_OK;
+}
+
+// The routing's own buffers; its M-tile list and counters are not used outside the grouped GEMMs.
+struct PermuteLayout {
+  size_t rank_local, block_counts, tiles, counters, total;
+};
+PermuteLayout permute_layout(int T, int K, int E) {
+  const size_t TK = (size_t)T * K;
+  PermuteLayout L;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align_up(bytes);
+    return at;
+  };
+  L.rank_local = take(TK * 4);
+  L.block_counts = take((size_t)route_blocks((int)TK) * E * 4);
+  L.tiles = take(((TK + kTileM - 1) / kTileM + E) * 16);
+  L.counters = take(16);
+  L.total = o;
+  return L;
+}
+
+int check_type(int type) {
+  if (type != PMOE_BF16 && type != PMOE_F32) return fail(PMOE_ERR_ARG, "type must be PMOE_BF16 or PMOE_F32");
+  return PMOE_OK;
+}
+size_t type_bytes(int type) { return type == PMOE_F32 ? 4 : 2; }
+
+}  // namespace
+
+PMOE_EXPORT size_t pmoe_permute_workspace_bytes(int T, int K, int E) {
+  if (check_permute_shape(T, K, E) != PMOE_OK) return 0;
+  ok();
+  return permute_layout(T, K, E).total;
+}
+
+PMOE_EXPORT int pmoe_permute_tokens(const void* topk_ids, int ids_type, int T, int K, int E, int expert_offset,
+                                    const void* x, int row_bytes, void* rows, int32_t* row_of_route,
+                                    int32_t* route_of_row, int32_t* expert_offsets, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  PMOE_TRY(check_permute_shape(T, K, E));
+  if (ids_type != PMOE_IDS_INT32 && ids_type != PMOE_IDS_INT64)
+    return fail(PMOE_ERR_ARG, "ids_type must be PMOE_IDS_INT32 or PMOE_IDS_INT64");
+  if (T > 0 && (x == nullptr) != (rows == nullptr)) return fail(PMOE_ERR_ARG, "x and rows are wanted both or neither");
+  const bool copy = T > 0 && x;
+  if (copy && (row_bytes <= 0 || row_bytes % 16 != 0 || row_bytes > 1 << 20))
+    return fail(PMOE_ERR_SHAPE, "row_bytes must be a positive multiple of 16, at most 2^20");
+  PMOE_TRY(check_device());
+  if (T > 0) {
+    PMOE_TRY(check_ids(topk_ids, ids_type, "topk_ids"));
+    PMOE_TRY(check_ptr_here(row_of_route, 4, "row_of_route"));
+    PMOE_TRY(check_ptr_here(route_of_row, 4, "route_of_row"));
+  }
+  if (copy) {
+    PMOE_TRY(check_ptr_here(x, 16, "x"));
+    PMOE_TRY(check_ptr_here(rows, 16, "rows"));
+  }
+  PMOE_TRY(check_ptr_here(expert_offsets, 4, "expert_offsets"));
+  PMOE_TRY(check_ptr_here(ws, 256, "ws"));
+  const PermuteLayout L = permute_layout(T, K, E);
+  if (ws_bytes < L.total)
+    return fail(PMOE_ERR_WORKSPACE, "workspace too small: need " + std::to_string(L.total) + " bytes");
+  const size_t routes = (size_t)T * K, bytes = copy ? row_bytes : 0;
+  PMOE_TRY(check_apart({{"rows", rows, routes * bytes},
+                        {"row_of_route", row_of_route, routes * 4},
+                        {"route_of_row", route_of_row, routes * 4},
+                        {"expert_offsets", expert_offsets, (size_t)(E + 1) * 4},
+                        {"ws", ws, L.total}},
+                       {{"topk_ids", topk_ids, routes * ids_bytes(ids_type)}, {"x", x, T * bytes}}));
+  char* base = static_cast<char*>(ws);
+  RouteBuffers b;
+  b.rank_local = reinterpret_cast<int*>(base + L.rank_local);
+  b.block_counts = reinterpret_cast<int*>(base + L.block_counts);
+  b.tiles = reinterpret_cast<int*>(base + L.tiles);
+  b.counters = reinterpret_cast<int*>(base + L.counters);
+  b.expert_offsets = expert_offsets;
+  b.row_of_route = row_of_route;
+  b.route_of_row = route_of_row;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  PMOE_HIP(launch_route(topk_ids, ids_type == PMOE_IDS_INT64, T * K, E, expert_offset, b, s));
+  if (copy) PMOE_HIP(launch_permute(x, row_of_route, T, K, row_bytes, rows, s));
+  return ok();
+}
+
+PMOE_EXPORT int pmoe_permute_tokens_backward(const void* d_rows, int type, const int32_t* row_of_route, int T, int K,
+                                             int R, int H, void* dx, void* stream) {
+  if (T < 0 || K < 1 || K > 32) return fail(PMOE_ERR_SHAPE, "need T >= 0 and 1 <= K <= 32");
+  if ((long long)T * K >= (1LL << 31) / 2) return fail(PMOE_ERR_SHAPE, "T*K too large");
+  if (R < 0) return fail(PMOE_ERR_SHAPE, "R must be >= 0");
+  PMOE_TRY(check_type(type));
+  if (H <= 0 || H > 1 << 18 || H % (type == PMOE_F32 ? 4 : 8) != 0)
+    return fail(PMOE_ERR_SHAPE, "H must be a positive multiple of 8 (FP32: 4), at most 2^18");
+  if (T == 0) return ok();
+  PMOE_TRY(check_device());
+  if (R > 0) PMOE_TRY(check_ptr_here(d_rows, 16, "d_rows"));
+  PMOE_TRY(check_ptr_here(row_of_route, 4, "row_of_route"));
+  PMOE_TRY(check_ptr_here(dx, 16, "dx"));
+  const size_t row = (size_t)H * type_bytes(type);
+  PMOE_TRY(check_apart({{"dx", dx, T * row}},
+                       {{"d_rows", d_rows, R * row}, {"row_of_route", row_of_route, (size_t)T * K * 4}}));
+  PMOE_HIP(launch_permute_backward(d_rows, type == PMOE_F32, row_of_route, T, K, R, H, dx,
+                                   static_cast<hipStream_t>(stream)));
+  return ok();
+}
+
+// ------------------------------------------------------------------ microscaled formats
+namespace {
+
+// Bytes of codes and scales of n elements.
+size_t mx_code_bytes(int format, size_t n) { return format == PMOE_MX_E2M1 ? n / 2 : n; }
+size_t mx_scale_bytes(size_t n) { return n / 32; }
+
+int check_mx_shape(int format, long long rows, int n) {
+  if (format != PMOE_MX_E2M1 && format != PMOE_MX_E4M3)
+    return fail(PMOE_ERR_ARG, "format must be PMOE_MX_E2M1 or PMOE_MX_E4M3");
+  if (n <= 0 || n % 32 != 0 || n > 1 << 30) return fail(PMOE_ERR_SHAPE, "n must be a positive multiple of 32, at most 2^30");
+  if (rows < 0 || rows >= (1LL << 40) / n) return fail(PMOE_ERR_SHAPE, "need 0 <= rows and rows*n < 2^40");
+  return PMOE_OK;
+}
+
+int check_mx_gemm_shape(int R, int E, int N, int Kd) {
+  if (E < 1 || E > kMaxExperts) return fail(PMOE_ERR_SHAPE, "E must be in [1, 1024]");
+  if (R < 0 || R > PMOE_MX_MAX_ROWS) return fail(PMOE_ERR_SHAPE, "R must be in [0, 2^23]");
+  if (N <= 0 || N % 16 != 0 || N > 2 * kMaxRow) return fail(PMOE_ERR_SHAPE, "N must be a multiple of 16 in [16, 32768]");
+  if (Kd <= 0 || Kd % 32 != 0 || Kd > kMaxRow) return fail(PMOE_ERR_SHAPE, "Kd must be a multiple of 32 in [32, 16384]");
+  return PMOE_OK;
+}
+
+// Rows of whole dwords are read as dwords.
+size_t mx_scale_align(int Kd) { return Kd % 128 == 0 ? 4 : 1; }
+
+int check_mx_activation_shape(int R, int I, int act, float limit) {
+  if (R < 0 || R > PMOE_MX_MAX_ROWS) return fail(PMOE_ERR_SHAPE, "R must be in [0, 2^23]");
+  if (I <= 0 || I % 32 != 0 || I > kMaxRow) return fail(PMOE_ERR_SHAPE, "I must be a multiple of 32 in [32, 16384]");
+  if (act != PMOE_ACT_RELU2 && act != PMOE_ACT_SWIGLU) return fail(PMOE_ERR_ACT, "unknown activation kind");
+  if (!(limit >= 0.0f)) return fail(PMOE_ERR_ARG, "swiglu_limit must be >= 0");
+  if (limit != 0.0f && act != PMOE_ACT_SWIGLU) return fail(PMOE_ERR_ARG, "swiglu_limit needs the SwiGLU activation");
+  return PMOE_OK;
+}
+
+}  // namespace
+
+PMOE_EXPORT int pmoe_mx_quantize(const void* x, int type, int format, long long rows, int n, void* codes,
+                                 void* scales, void* stream) {
+  PMOE_TRY(check_type(type));
+  PMOE_TRY(check_mx_shape(format, rows, n));
+  if (rows == 0) return ok();
+  PMOE_TRY(check_device());
+  PMOE_TRY(check_ptr_here(x, 16, "x"));
+  PMOE_TRY(check_ptr_here(codes, 16, "codes"));
+  PMOE_TRY(check_ptr_here(scales, 1, "scales"));
+  const size_t all = (size_t)rows * n;
+  PMOE_TRY(check_apart({{"codes", codes, mx_code_bytes(format, all)}, {"scales", scales, mx_scale_bytes(all)}},
+                       {{"x", x, all * type_bytes(type)}}));
+  PMOE_HIP(launch_mx_quantize(x, type == PMOE_F32, format == PMOE_MX_E4M3, (long)all, static_cast<uint8_t*>(codes),
+                              static_cast<uint8_t*>(scales), static_cast<hipStream_t>(stream)));
+  return ok();
+}
+
+PMOE_EXPORT int pmoe_mx_dequantize(const void* codes, const void* scales, int format, long long rows, int n, int type,
+                                   void* out, void* stream) {
+  PMOE_TRY(check_type(type));
+  PMOE_TRY(check_mx_shape(format, rows, n));
+  if (rows == 0) return ok();
+  PMOE_TRY(check_device());
+  PMOE_TRY(check_ptr_here(codes, 16, "codes"));
+  PMOE_TRY(check_ptr_here(scales, 1, "scales"));
+  PMOE_TRY(check_ptr_here(out, 16, "out"));
+  const size_t all = (size_t)rows * n;
+  PMOE_TRY(check_apart({{"out", out, all * type_bytes(type)}},
+                       {{"codes", codes, mx_code_bytes(format, all)}, {"scales", scales, mx_scale_bytes(all)}}));
+  PMOE_HIP(launch_mx_dequantize(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales),
+                                format == PMOE_MX_E4M3, (long)all, type == PMOE_F32, out,
+                                static_cast<hipStream_t>(stream)));
+  return ok();
+}
+
+PMOE_EXPORT int pmoe_mx_grouped_gemm(const void* a_codes, const void* a_sf, int a_rows, const int32_t* route_of_row,
+                                     int topk, const int32_t* expert_offsets, int R, int E, const void* w_codes,
+                                     const void* w_sf, int N, int Kd, void* out, int out_type, void* stream) {
+  PMOE_TRY(check_mx_gemm_shape(R, E, N, Kd));
+  PMOE_TRY(check_type(out_type));
+  if (a_rows < 0 || (!route_of_row && a_rows < R)) return fail(PMOE_ERR_SHAPE, "a has fewer rows than R");
+  if (topk < 1) return fail(PMOE_ERR_ARG, "topk must be at least 1");
+  if (route_of_row && (long long)a_rows * Kd >= (1LL << 32) - 512)
+    return fail(PMOE_ERR_SHAPE, "a gathered a_rows*Kd must stay below 2^32 - 512");
+  if (R == 0) return ok();
+  PMOE_TRY(check_device());
+  if (a_rows > 0) {
+    PMOE_TRY(check_ptr_here(a_codes, 16, "a_codes"));
+    PMOE_TRY(check_ptr_here(a_sf, mx_scale_align(Kd), "a_sf"));
+  }
+  if (route_of_row) PMOE_TRY(check_ptr_here(route_of_row, 4, "route_of_row"));
+  PMOE_TRY(check_ptr_here(expert_offsets, 4, "expert_offsets"));
+  PMOE_TRY(check_ptr_here(w_codes, 16, "w_codes"));
+  PMOE_TRY(check_ptr_here(w_sf, mx_scale_align(Kd), "w_sf"));
+  PMOE_TRY(check_ptr_here(out, 16, "out"));
+  const size_t a = (size_t)a_rows * Kd, w = (size_t)E * N * Kd;
+  PMOE_TRY(check_apart({{"out", out, (size_t)R * N * type_bytes(out_type)}},
+                       {{"a_codes", a_codes, a / 2},
+                        {"a_sf", a_sf, a / 32},
+                        {"route_of_row", route_of_row, (size_t)R * 4},
+                        {"expert_offsets", expert_offsets, (size_t)(E + 1) * 4},
+                        {"w_codes", w_codes, w / 2},
+                        {"w_sf", w_sf, w / 32}}));
+  MxGemmParams p{static_cast<const uint8_t*>(a_codes), static_cast<const uint8_t*>(a_sf), a_rows, route_of_row, topk,
+                 expert_offsets, R, E, static_cast<const uint8_t*>(w_codes), static_cast<const uint8_t*>(w_sf), N, Kd,
+                 out, out_type == PMOE_F32};
+  PMOE_HIP(launch_mx_gemm(p, static_cast<hipStream_t>(stream)));
+  return ok();
+}
+
+PMOE_EXPORT int pmoe_mx_grouped_gemm_backward(const void* dy, const int32_t* expert_offsets, int R, int E,
+                                              const void* w_codes, const void* w_sf, int N, int Kd, void* dx,
+                                              void* stream) {
+  PMOE_TRY(check_mx_gemm_shape(R, E, N, Kd));
+  if (R == 0) return ok();
+  PMOE_TRY(check_device());
+  PMOE_TRY(check_ptr_here(dy, 16, "dy"));
+  PMOE_TRY(check_ptr_here(expert_offsets, 4, "expert_offsets"));
+  PMOE_TRY(check_ptr_here(w_codes, 16, "w_codes"));
+  PMOE_TRY(check_ptr_here(w_sf, mx_scale_align(Kd), "w_sf"));
+  PMOE_TRY(check_ptr_here(dx, 16, "dx"));
+  const size_t w = (size_t)E * N * Kd;
+  PMOE_TRY(check_apart({{"dx", dx, (size_t)R * Kd * 2}},
+                       {{"dy", dy, (size_t)R * N * 2},
+                        {"expert_offsets", expert_offsets, (size_t)(E + 1) * 4},
+                        {"w_codes", w_codes, w / 2},
+                        {"w_sf", w_sf, w / 32}}));
+  MxGemmParams p{static_cast<const uint8_t*>(dy), nullptr, R, nullptr, 1, expert_offsets, R, E,
+                 static_cast<const uint8_t*>(w_codes), static_cast<const uint8_t*>(w_sf), N, Kd, dx, false};
+  PMOE_HIP(launch_mx_gemm_backward(p, static_cast<hipStream_t>(stream)));
+  return ok();
+}
+
+PMOE_EXPORT int pmoe_mx_activation(const void* y, int R, int I, int act, float swiglu_limit, const int32_t* row_count,
+                                   void* hq, void* h_sf, void* y8, void* y8_sf, void* stream) {
+  PMOE_TRY(check_mx_activation_shape(R, I, act, swiglu_limit));
+  if ((y8 == nullptr) != (y8_sf == nullptr)) return fail(PMOE_ERR_ARG, "y8 and y8_sf are wanted both or neither");
+  if (R == 0) return ok();
+  PMOE_TRY(check_device());
+  PMOE_TRY(check_ptr_here(y, 16, "y"));
+  if (row_count) PMOE_TRY(check_ptr_here(row_count, 4, "row_count"));
+  PMOE_TRY(check_ptr_here(hq, 16, "hq"));
+  PMOE_TRY(check_ptr_here(h_sf, 1, "h_sf"));
+  if (y8) {
+    PMOE_TRY(check_ptr_here(y8, 16, "y8"));
+    PMOE_TRY(check_ptr_here(y8_sf, 1, "y8_sf"));
+  }
+  const size_t h = (size_t)R * I, w = act == PMOE_ACT_SWIGLU ? 2 * h : h;
+  PMOE_TRY(check_apart({{"hq", hq, h / 2}, {"h_sf", h_sf, h / 32}, {"y8", y8, w}, {"y8_sf", y8_sf, w / 32}},
+                       {{"y", y, 2 * w}, {"row_count", row_count, 4}}));
+  MxActivationParams p{y, R, I, act == PMOE_ACT_SWIGLU, swiglu_limit, row_count, static_cast<uint8_t*>(hq),
+                       static_cast<uint8_t*>(h_sf), static_cast<uint8_t*>(y8), static_cast<uint8_t*>(y8_sf)};
+  PMOE_HIP(launch_mx_activation(p, static_cast<hipStream_t>(stream)));
+  return ok();
+}
+
+PMOE_EXPORT int pmoe_mx_activation_backward(const void* dh, const void* y8, const void* y8_sf, int R, int I, int act,
+                                            float swiglu_limit, const int32_t* row_count, void* dy, void* stream) {
+  PMOE_TRY(check_mx_activation_shape(R, I, act, swiglu_limit));
+  if (R == 0) return ok();
+  PMOE_TRY(check_device());
+  PMOE_TRY(check_ptr_here(dh, 16, "dh"));
+  PMOE_TRY(check_ptr_here(y8, 16, "y8"));
+  PMOE_TRY(check_ptr_here(y8_sf, 1, "y8_sf"));
+  if (row_count) PMOE_TRY(check_ptr_here(row_count, 4, "row_count"));
+  PMOE_TRY(check_ptr_here(dy, 16, "dy"));
+  const size_t h = (size_t)R * I, w = act == PMOE_ACT_SWIGLU ? 2 * h : h;
+  PMOE_TRY(check_apart({{"dy", dy, 2 * w}},
+                       {{"dh", dh, 2 * h}, {"y8", y8, w}, {"y8_sf", y8_sf, w / 32}, {"row_count", row_count, 4}}));
+  MxActivationParams p{nullptr, R, I, act == PMOE_ACT_SWIGLU, swiglu_limit, row_count, nullptr, nullptr,
+                       const_cast<uint8_t*>(static_cast<const uint8_t*>(y8)),
+                       const_cast<uint8_t*>(static_cast<const uint8_t*>(y8_sf))};
+  PMOE_HIP(launch_mx_activation_backward(p, dh, dy, static_cast<hipStream_t>(stream)));
+  return ok();
+}

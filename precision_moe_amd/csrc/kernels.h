@@ -174,4 +174,48 @@ size_t adapter_backward_ws_bytes(int T, int n, int H, int N, int R);
 hipError_t launch_adapter_forward(const AdapterParams& p, hipStream_t s);
 hipError_t launch_adapter_backward(const AdapterParams& p, hipStream_t s);
 
+// ---------------------------------------------------------------- permutation of tokens
+// rows[row(t, j)] = x[t], rows and x of row_bytes (a multiple of 16), and its gradient.
+hipError_t launch_permute(const void* x, const int* row_of_route, int T, int K, long row_bytes, void* rows,
+                          hipStream_t s);
+hipError_t launch_permute_backward(const void* d_rows, bool f32, const int* row_of_route, int T, int K, int R, int H,
+                                   void* dx, hipStream_t s);
+
+// ---------------------------------------------------------------- microscaled formats
+// n elements, a multiple of 32: blocks of 32 consecutive ones.
+hipError_t launch_mx_quantize(const void* x, bool f32, bool e4m3, long n, uint8_t* codes, uint8_t* scales,
+                              hipStream_t s);
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, bool e4m3, long n, bool f32, void* out,
+                                hipStream_t s);
+struct MxActivationParams {
+  const void* y;         // forward: BF16 [R][I or 2I]
+  long R;
+  int I;
+  bool swiglu;
+  float limit;           // SwiGLU clamp, 0 = none
+  const int* row_count;  // rows that are read and written, at most R; null: R
+  uint8_t* hq;           // forward: E2M1 [R][I/2]
+  uint8_t* h_sf;         // forward: [R][I/32]
+  uint8_t* y8;           // E4M3 checkpoint of y; forward: null: not kept
+  uint8_t* y8_sf;
+};
+hipError_t launch_mx_activation(const MxActivationParams& p, hipStream_t s);
+hipError_t launch_mx_activation_backward(const MxActivationParams& p, const void* dh, void* dy, hipStream_t s);
+struct MxGemmParams {
+  const uint8_t* a_codes;   // forward: rows of Kd/2 bytes; backward: dy, rows of N BF16
+  const uint8_t* a_sf;      // forward: rows of Kd/32 bytes
+  int a_rows;               // rows of a, with route_of_row
+  const int* route_of_row;  // forward: row r reads a's row route / topk; null: row r
+  int topk;
+  const int* offsets;       // [E+1]
+  int R, E;
+  const uint8_t* w_codes;   // [E][N][Kd/2]
+  const uint8_t* w_sf;      // [E][N][Kd/32]
+  int N, Kd;
+  void* out;                // forward [R][N], backward BF16 [R][Kd]
+  bool out_f32;
+};
+hipError_t launch_mx_gemm(const MxGemmParams& p, hipStream_t s);
+hipError_t launch_mx_gemm_backward(const MxGemmParams& p, hipStream_t s);
+
 }  // namespace pmoe
