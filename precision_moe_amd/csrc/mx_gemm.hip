@@ -37,15 +37,15 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // Lane l's 16 bytes at `offset` go to lds + 16 l (4 bytes to lds + 4 l; one byte, extended
 // with zeros to 4, to lds + 4 l). The loads are counted by vmcnt, in order.
 __device__ __forceinline__ void load_lds16(intx4 buf, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buf)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(buf)
                : "memory");
 }
 __device__ __forceinline__ void load_lds4(intx4 buf, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buf)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(buf)
                : "memory");
 }
 __device__ __forceinline__ void load_lds1(intx4 buf, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buf)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(buf)
                : "memory");
 }
 template <int kLeft>
@@ -62,6 +62,12 @@ __device__ __forceinline__ void wait_loads() {  // until at most kLeft of the wa
 struct MxItem {
   int e, row0, rows, col;  // rows: of this tile, 1 .. BM
 };
+// Tile m of n of an expert with `rows` rows from `first`: the rows' groups of 32 are shared out evenly.
+__device__ __forceinline__ MxItem mx_tile(int e, int first, int rows, int m, int n, int col) {
+  const int groups = (rows + 31) / 32;
+  const int from = (int)((long)m * groups / n) * 32, to = (int)((long)(m + 1) * groups / n) * 32;
+  return MxItem{e, first + from, min(rows, to) - from, col};
+}
 __device__ __forceinline__ int wave_scan(int v, int lane) {  // inclusive sum over the lanes
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
@@ -104,11 +110,8 @@ __device__ __forceinline__ bool mx_item(const int* offsets, int E, int R, int co
       const int n = __builtin_amdgcn_readlane(tiles, who);
       const int start = __builtin_amdgcn_readlane(upto, who) - n;
       const int local = (int)(item - (long)start * col_tiles);
-      const int m = local % n;
-      it.e = e0 + who;
-      it.col = local / n;
-      it.row0 = __builtin_amdgcn_readlane(first, who) + m * BM;
-      it.rows = min(__builtin_amdgcn_readlane(rows, who) - m * BM, BM);
+      it = mx_tile(e0 + who, __builtin_amdgcn_readlane(first, who), __builtin_amdgcn_readlane(rows, who), local % n, n,
+                   local / n);
       return true;
     }
     before = __builtin_amdgcn_readlane(upto, 63);
@@ -121,30 +124,36 @@ __device__ __forceinline__ bool mx_item(const int* offsets, int E, int R, int co
 // block, of row lane % 32 of either operand, and that block's scale byte. The
 // matrix is the first operand, so that a lane's results are consecutive
 // columns of one row. A stage is 256 elements of the reduction (128 bytes of
-// codes, 8 scales a row); which blocks meet in one instruction is free as long as
-// both operands agree: half h of the wave takes blocks 4h + j in step j, whose
-// four scales are then one aligned dword, read once a stage, and the step selects the byte.
+// codes, 8 scales a row: whole lines, as loads of half lines reach half the rate);
+// which blocks meet in one instruction is free as long as both operands agree: half
+// h of the wave takes blocks 4h + j in step j, whose four scales are then one
+// dword, read once a stage, and the step selects the byte.
 //
-// In LDS a row of a stage is 8 slots of 16 bytes; piece p is in slot p ^ (row %
-// 8), so the 8 lanes that one LDS access serves (8 rows, one piece) hit 8 slots.
-// Loads write LDS in lane order, so the lanes' addresses carry the permutation.
+// In LDS a row of a stage is 8 slots of 16 bytes; piece p is in slot p ^ (row /
+// 2 % 8), so that the 16 lanes that one cycle serves (16 rows, one piece) meet
+// the 16 slots of 64 banks. Loads write LDS in lane order, so the lanes'
+// addresses carry the permutation: eight rows a load, the halves of 64 bytes
+// exchanged in every second load.
 template <int NW_, int MW_, int WN_, int WM_, int S_, bool kBytes_>
 struct MxTile {
   static constexpr int NW = NW_, MW = MW_, WN = WN_, WM = WM_, S = S_;
   static constexpr bool kBytes = kBytes_;  // rows of scales are not whole dwords: loaded byte by byte
   static constexpr int kWaves = WN * WM, BN = 32 * NW * WN, BM = 32 * MW * WM, kRows = BN + BM;
   static constexpr int kScaleRow = kBytes ? 32 : 8;
-  static constexpr int kStage = kRows * (128 + kScaleRow);
-  static constexpr int kLoadW = BN / 8 / kWaves, kLoadX = BM / 8 / kWaves;  // 1 KB loads of a wave
-  static constexpr int kScaleLoads = kRows / (kBytes ? 8 : 32);
+  static constexpr int kLoadW = BN / 8 / kWaves, kLoadX = (BM / 8 + kWaves - 1) / kWaves;  // 1 KB loads of a wave
+  static constexpr int kScaleRows = kBytes ? 8 : 32;                                      // rows of one load of scales
+  static constexpr int kScaleLoads = kRows / kScaleRows;
   static constexpr int kLoadS = (kScaleLoads + kWaves - 1) / kWaves;
   static constexpr int kLoads = kLoadW + kLoadX + kLoadS;
-  static_assert(BN % (8 * kWaves) == 0 && BM % (8 * kWaves) == 0, "whole loads");
+  static constexpr int kStage = kRows * (128 + kScaleRow);
+  static constexpr int kOutRow = 64 * NW + 8;  // bytes of a row of the epilogue's LDS (BF16): banks 2 apart
+  static constexpr int kLds = S * kStage > kWaves * 32 * kOutRow ? S * kStage : kWaves * 32 * kOutRow;
+  static_assert(BN % (8 * kWaves) == 0 && BN % 32 == 0 && BM % 32 == 0, "whole loads");
 };
 
 template <class C>
 __global__ __launch_bounds__(C::kWaves * 64) void mx_gemm_kernel(MxGemmParams P) {
-  __shared__ __attribute__((aligned(128))) uint8_t lds[C::S * C::kStage];
+  __shared__ __attribute__((aligned(128))) uint8_t lds[C::kLds];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   MxItem it;
@@ -165,52 +174,51 @@ __global__ __launch_bounds__(C::kWaves * 64) void mx_gemm_kernel(MxGemmParams P)
     return f >= 0 && f / P.topk < P.a_rows ? f / P.topk : -1;
   };
 
-  // Loads of this lane: of a row of codes 16 bytes, of a row of scales one dword or byte.
-  const int lr = lane >> 3;                              // row of the eight
-  const uint32_t piece = ((lane & 7) ^ lr) * 16;         // its bytes within the stage's 128
+  // Loads of this lane: 16 bytes of a row of codes, a dword or byte of a row of
+  // scales. A load past the operand's last one repeats the last (same bytes, same place).
+  const int lr = lane >> 3;                        // row of the eight
+  const uint32_t piece = ((lane & 7) ^ lr >> 1) * 16;  // its bytes within the stage's 128; ^ 64 in odd loads
   const uint32_t w_row = (uint32_t)(n0 + 8 * wave * C::kLoadW + lr) * krow;
+  auto x_load = [&](int i) { return min(wave * C::kLoadX + i, C::BM / 8 - 1); };
   uint32_t x_row[C::kLoadX];
 #pragma unroll
   for (int i = 0; i < C::kLoadX; ++i) {
-    const int r = source(8 * (wave * C::kLoadX + i) + lr);
+    const int r = source(8 * x_load(i) + lr);
     x_row[i] = r < 0 ? kNoRow : (uint32_t)r * krow;
   }
-  constexpr int kSRows = C::kBytes ? 8 : 32;             // rows of one load of scales
   const int sr = C::kBytes ? lane >> 3 : lane >> 1;
   const uint32_t s_at = C::kBytes ? lane & 7 : (lane & 1) * 4;
+  auto s_load = [&](int i) { return min(wave * C::kLoadS + i, C::kScaleLoads - 1); };
   uint32_t s_row[C::kLoadS];
+  bool s_is_w[C::kLoadS];
 #pragma unroll
   for (int i = 0; i < C::kLoadS; ++i) {
-    const int q = min(wave * C::kLoadS + i, C::kScaleLoads - 1) * kSRows;
-    if (q < C::BN) {
-      s_row[i] = (uint32_t)(n0 + q + sr) * srow;
-    } else {
-      const int r = source(q - C::BN + sr);
-      s_row[i] = r < 0 ? kNoRow : (uint32_t)r * srow;
-    }
+    const int q = s_load(i) * C::kScaleRows;
+    s_is_w[i] = q < C::BN;
+    const int r = s_is_w[i] ? n0 + q + sr : source(q - C::BN + sr);
+    s_row[i] = r < 0 ? kNoRow : (uint32_t)r * srow;
   }
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(lds));
   auto issue = [&](int st, int slot) {
     const uint32_t to = lds0 + slot * C::kStage;
-    const uint32_t kb = (uint32_t)st * 128 + piece;
-    const uint32_t k = kb < krow ? kb : kPast;
-#pragma unroll
-    for (int i = 0; i < C::kLoadW; ++i)
-      load_lds16(wq, w_row + i * 8 * krow + k, to + (wave * C::kLoadW + i) * 1024);
-#pragma unroll
-    for (int i = 0; i < C::kLoadX; ++i)
-      load_lds16(aq, x_row[i] + k, to + C::BN * 128 + (wave * C::kLoadX + i) * 1024);
+    auto k_of = [&](int load) {
+      const uint32_t kb = (uint32_t)st * 128 + (piece ^ (load & 1) * 64);
+      return kb < krow ? kb : kPast;
+    };
     const uint32_t sb = (uint32_t)st * 8 + s_at;
     const uint32_t sk = sb < srow ? sb : kPast;
 #pragma unroll
     for (int i = 0; i < C::kLoadS; ++i) {
-      const int q = min(wave * C::kLoadS + i, C::kScaleLoads - 1);
-      const intx4 buf = q * kSRows < C::BN ? ws : as;
       if constexpr (C::kBytes)
-        load_lds1(buf, s_row[i] + sk, to + C::kRows * 128 + q * 256);
+        load_lds1(s_is_w[i] ? ws : as, s_row[i] + sk, to + C::kRows * 128 + s_load(i) * 256);
       else
-        load_lds4(buf, s_row[i] + sk, to + C::kRows * 128 + q * 256);
+        load_lds4(s_is_w[i] ? ws : as, s_row[i] + sk, to + C::kRows * 128 + s_load(i) * 256);
     }
+#pragma unroll
+    for (int i = 0; i < C::kLoadX; ++i) load_lds16(aq, x_row[i] + k_of(x_load(i)), to + C::BN * 128 + x_load(i) * 1024);
+#pragma unroll
+    for (int i = 0; i < C::kLoadW; ++i)
+      load_lds16(wq, w_row + i * 8 * krow + k_of(wave * C::kLoadW + i), to + (wave * C::kLoadW + i) * 1024);
   };
 
   floatx16 acc[C::NW][C::MW];
@@ -224,82 +232,452 @@ __global__ __launch_bounds__(C::kWaves * 64) void mx_gemm_kernel(MxGemmParams P)
   const int wn = wave % C::WN, wm = wave / C::WN;
   const int half = lane >> 5, r32 = lane & 31;
   const int w_at = wn * C::NW * 32 + r32, x_at = C::BN + wm * C::MW * 32 + r32;  // rows of the stage
-  auto compute = [&](int slot) {
-    const uint8_t* b = lds + slot * C::kStage;
-    const uint8_t* sc = b + C::kRows * 128;
-    intx4 ws4[C::NW], xs4[C::MW];  // scales of the four steps: bytes of [0], or the words' low bytes
-    auto scales = [&](int row) {
-      if constexpr (C::kBytes) return *reinterpret_cast<const intx4*>(sc + row * 32 + half * 16);
-      else return intx4{*reinterpret_cast<const int*>(sc + row * 8 + half * 4), 0, 0, 0};
-    };
-#pragma unroll
-    for (int f = 0; f < C::NW; ++f) ws4[f] = scales(w_at + 32 * f);
-#pragma unroll
-    for (int g = 0; g < C::MW; ++g) xs4[g] = scales(x_at + 32 * g);
-    auto step = [&](auto J) {
-      constexpr int j = decltype(J)::value;
-      const int at = ((4 * half + j) ^ (lane & 7)) * 16;
-      auto frag = [&](int row) {
-        const intx4 v = *reinterpret_cast<const intx4*>(b + row * 128 + at);
-        return intx8{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
-      };
-      intx8 x[C::MW];
-#pragma unroll
-      for (int g = 0; g < C::MW; ++g) x[g] = frag(x_at + 32 * g);
-#pragma unroll
-      for (int f = 0; f < C::NW; ++f) {
-        const intx8 w = frag(w_at + 32 * f);
-#pragma unroll
-        for (int g = 0; g < C::MW; ++g) {
-          if constexpr (C::kBytes)
-            acc[f][g] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x[g], acc[f][g], 4, 4, 0, ws4[f][j], 0, xs4[g][j]);
-          else
-            acc[f][g] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x[g], acc[f][g], 4, 4, j, ws4[f][0], j, xs4[g][0]);
-        }
-      }
-    };
-    step(std::integral_constant<int, 0>{});
-    step(std::integral_constant<int, 1>{});
-    step(std::integral_constant<int, 2>{});
-    step(std::integral_constant<int, 3>{});
+  struct Frags {
+    intx4 w[C::NW], x[C::MW];
   };
-
-  // Stage st is in slot st % S. At its barrier every wave's loads of it have landed
-  // and every wave is done with stage st - 1, whose slot the next loads take.
-  const int stages = (P.Kd + 255) / 256;
+  // Scales of the four steps: the bytes of one word, or (kBytes) the low bytes of four.
+  using Scale = std::conditional_t<C::kBytes, intx4, int>;
+  struct Scales {
+    Scale w[C::NW], x[C::MW];
+  };
+  auto read = [&](Frags& v, int slot, int j) {
+    const uint8_t* b = lds + slot * C::kStage + ((4 * half + j) ^ (lane >> 1 & 7)) * 16;
 #pragma unroll
-  for (int s = 0; s < C::S - 1; ++s) issue(s, s);  // past the last stage: zeros
-  int slot = 0;
-  for (int st = 0; st < stages; ++st) {
-    wait_loads<(C::S - 2) * C::kLoads>();
-    lds_barrier();
-    issue(st + C::S - 1, slot == 0 ? C::S - 1 : slot - 1);
-    compute(slot);
-    slot = slot == C::S - 1 ? 0 : slot + 1;
-  }
-  wait_loads<0>();  // no load may land in LDS after the workgroup's end
-
-  // acc[f][g][i] is column 32 f + 8 (i / 4) + 4 half + i % 4 of row 32 g + r32 of the wave's part.
+    for (int g = 0; g < C::MW; ++g) v.x[g] = *reinterpret_cast<const intx4*>(b + (x_at + 32 * g) * 128);
 #pragma unroll
-  for (int g = 0; g < C::MW; ++g) {
-    const int m = (wm * C::MW + g) * 32 + r32;
-    if (m >= it.rows) continue;
-    const long row = (long)(it.row0 + m) * P.N;
+    for (int f = 0; f < C::NW; ++f) v.w[f] = *reinterpret_cast<const intx4*>(b + (w_at + 32 * f) * 128);
+  };
+  auto read_scales = [&](Scales& v, int slot) {
+    const uint8_t* b = lds + slot * C::kStage + C::kRows * 128 + half * (C::kScaleRow / 2);
+#pragma unroll
+    for (int g = 0; g < C::MW; ++g) v.x[g] = *reinterpret_cast<const Scale*>(b + (x_at + 32 * g) * C::kScaleRow);
+#pragma unroll
+    for (int f = 0; f < C::NW; ++f) v.w[f] = *reinterpret_cast<const Scale*>(b + (w_at + 32 * f) * C::kScaleRow);
+  };
+  auto multiply = [&](const Frags& v, const Scales& s, auto J) {
+    constexpr int j = decltype(J)::value;
+    auto wide = [](intx4 t) { return intx8{t[0], t[1], t[2], t[3], 0, 0, 0, 0}; };
 #pragma unroll
     for (int f = 0; f < C::NW; ++f)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = n0 + (wn * C::NW + f) * 32 + 8 * q + 4 * half;
-        if (n >= P.N) continue;
-        const floatx16& a = acc[f][g];
-        if (P.out_f32)
-          *reinterpret_cast<float4*>(static_cast<float*>(P.out) + row + n) =
-              make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+      for (int g = 0; g < C::MW; ++g) {
+        if constexpr (C::kBytes)
+          acc[f][g] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(v.w[f]), wide(v.x[g]), acc[f][g], 4, 4, 0,
+                                                                      s.w[f][j], 0, s.x[g][j]);
         else
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + row + n) =
-              make_uint2(f32x2_to_bf16x2(a[4 * q], a[4 * q + 1]), f32x2_to_bf16x2(a[4 * q + 2], a[4 * q + 3]));
+          acc[f][g] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(v.w[f]), wide(v.x[g]), acc[f][g], 4, 4, j,
+                                                                      s.w[f], j, s.x[g]);
       }
+  };
+
+  // Stage st is in slot st % S. Fragments are read one step ahead of their
+  // products, the first of a stage during the last step of the one before. The
+  // barrier is there: every wave has then read all of stage st, whose slot the
+  // loads of stage st + S may take, and its loads of stage st + 1 have landed.
+  const int stages = (P.Kd + 255) / 256;
+#pragma unroll
+  for (int s = 0; s < C::S; ++s) issue(s, s);  // past the last stage: zeros
+  wait_loads<(C::S - 1) * C::kLoads>();
+  lds_barrier();
+  Frags even, odd;
+  Scales sc;
+  read_scales(sc, 0);
+  read(even, 0, 0);
+  int slot = 0;
+  for (int st = 0; st < stages; ++st) {
+    const int next = slot == C::S - 1 ? 0 : slot + 1;
+    read(odd, slot, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(even, sc, std::integral_constant<int, 0>{});
+    __builtin_amdgcn_sched_barrier(0);
+    read(even, slot, 2);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(odd, sc, std::integral_constant<int, 1>{});
+    __builtin_amdgcn_sched_barrier(0);
+    read(odd, slot, 3);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(even, sc, std::integral_constant<int, 2>{});
+    __builtin_amdgcn_sched_barrier(0);
+    wait_loads<(C::S - 2) * C::kLoads>();
+    lds_barrier();
+    Scales sn;
+    read(even, next, 0);
+    read_scales(sn, next);
+    issue(st + C::S, slot);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(odd, sc, std::integral_constant<int, 3>{});
+    __builtin_amdgcn_sched_barrier(0);
+    sc = sn;
+    slot = next;
   }
+  wait_loads<0>();  // no load may land in LDS after the workgroup's end, nor in what follows
+  lds_barrier();
+
+  // acc[f][g][i] is column 32 f + 8 (i / 4) + 4 half + i % 4 of row 32 g + r32 of
+  // the wave's part. 32 rows at a time (FP32: in two halves of the columns) go
+  // through this wave's own piece of LDS, so that a store covers whole rows of it.
+  uint8_t* mine = lds + wave * 32 * C::kOutRow;
+  const int cols = min(P.N - n0 - wn * C::NW * 32, C::NW * 32);  // of this wave's part that exist
+#pragma unroll
+  for (int g = 0; g < C::MW; ++g) {
+    const int m0 = (wm * C::MW + g) * 32;
+    const int rows = min(it.rows - m0, 32);
+    const long out = (long)(it.row0 + m0) * P.N + n0 + wn * C::NW * 32;
+    auto copy = [&](int size, int c0, int width) {  // columns c0 .. c0 + width of the 32 rows, 16 bytes a lane
+      const int per = width * size / 16;            // lanes of a row: a power of two
+      const int have = min(max(cols - c0, 0), width) * size;
+      for (int i = lane; i < 32 * per; i += 64) {
+        const int r = i / per, at = i % per * 16;
+        const uint2* from = reinterpret_cast<const uint2*>(mine + r * C::kOutRow + at);
+        const uint2 a = from[0], b = from[1];
+        if (r < rows && at < have)
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(P.out) + (out + (long)r * P.N + c0) * size + at) =
+              make_uint4(a.x, a.y, b.x, b.y);
+      }
+    };
+    if (P.out_f32) {
+      constexpr int kF = C::NW > 1 ? C::NW / 2 : 1;  // fragments of a half
+#pragma unroll
+      for (int h = 0; h < (C::NW > 1 ? 2 : 1) * (C::NW > 1 ? 1 : 2); ++h) {
+        // NW > 1: fragments h * kF ..; NW = 1: quarters 2h, 2h + 1 of the one fragment
+#pragma unroll
+        for (int f = 0; f < kF; ++f)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (C::NW == 1 && q / 2 != h) continue;
+            const floatx16& a = acc[C::NW > 1 ? h * kF + f : 0][g];
+            const int at = (C::NW > 1 ? 32 * f + 8 * q : 8 * (q & 1)) + 4 * half;
+            uint2* to = reinterpret_cast<uint2*>(mine + r32 * C::kOutRow + at * 4);
+            to[0] = make_uint2(__float_as_uint(a[4 * q]), __float_as_uint(a[4 * q + 1]));
+            to[1] = make_uint2(__float_as_uint(a[4 * q + 2]), __float_as_uint(a[4 * q + 3]));
+          }
+        copy(4, h * C::NW * 16, C::NW * 16);
+      }
+    } else {
+#pragma unroll
+      for (int f = 0; f < C::NW; ++f)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const floatx16& a = acc[f][g];
+          *reinterpret_cast<uint2*>(mine + r32 * C::kOutRow + (32 * f + 8 * q + 4 * half) * 2) =
+              make_uint2(f32x2_to_bf16x2(a[4 * q], a[4 * q + 1]), f32x2_to_bf16x2(a[4 * q + 2], a[4 * q + 3]));
+        }
+      copy(2, 0, C::NW * 32);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- forward, many rows
+// The same products in the same order by workgroups that stay: 256 x 256 tiles
+// by eight waves (two a SIMD, each 64 columns by 128 rows), one workgroup a CU,
+// which takes every 32nd tile of its XCD. Loads run ahead across tiles: while the last
+// stages of one are multiplied, the first of the next are under way, so that
+// only the epilogue stands between two tiles. Scales are loaded for two
+// stages at once, 16 bytes of a row: a load moves whole lines whatever it uses of them,
+// and two dwords of every row each stage cost as much as the codes.
+// An expert's rows are shared out evenly over its tiles in groups of 32, and a wave
+// multiplies the groups that its tile has.
+struct MxWide {
+  static constexpr int NW = 2, MW = 4, WN = 4, WM = 2, kWaves = 8, BN = 256, BM = 256, kRows = BN + BM;
+  static constexpr int kStage = kRows * 128, kScales = kRows * 16, kLoad = 4;  // 1 KB loads of a wave and operand
+  static constexpr int kOutRow = 64 * NW + 8;
+  static constexpr int kTable = 2 * kStage + 2 * kScales, kLds = kTable + kMaxExperts * 4;
+};
+
+template <bool kF32>
+__global__ __launch_bounds__(512) void mx_gemm_wide_kernel(MxGemmParams P) {
+  using C = MxWide;
+  __shared__ __attribute__((aligned(128))) uint8_t lds[C::kLds];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t krow = P.Kd / 2, srow = P.Kd / kMxBlock;
+  const int col_tiles = (P.N + C::BN - 1) / C::BN;
+
+  // Row tiles up to and with each expert, by wave 0.
+  int* table = reinterpret_cast<int*>(lds + C::kTable);
+  auto first_row = [&](int e) { return min(max(P.offsets[e], 0), P.R); };
+  auto rows_of = [&](int e, int first) { return max(min(P.offsets[e + 1], P.R) - first, 0); };
+  if (wave == 0) {
+    int before = 0;
+    for (int e0 = 0; e0 < P.E; e0 += 64) {
+      const int e = e0 + lane;
+      const int tiles = e < P.E ? (rows_of(e, first_row(e)) + C::BM - 1) / C::BM : 0;
+      const int upto = before + wave_scan(tiles, lane);
+      if (e < P.E) table[e] = upto;
+      before = __builtin_amdgcn_readlane(upto, 63);
+    }
+  }
+  __syncthreads();
+  const int items = __builtin_amdgcn_readfirstlane(table[P.E - 1]) * col_tiles;  // below 2^23 by the launch's check
+  const int per = (items + 7) >> 3;
+  const int last_item = min((int)(blockIdx.x & 7) * per + per, items);
+  int item = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (item >= last_item) return;
+  const int step = gridDim.x >> 3;
+
+  auto find = [&](int i) {
+    const int tile = i / col_tiles;
+    int e = 0;
+    for (int e0 = 0; e0 < P.E; e0 += 64) {
+      const int upto = table[min(e0 + lane, P.E - 1)];
+      const uint64_t past = __ballot(upto > tile);
+      if (past) {
+        e = e0 + __builtin_ctzll(past);
+        break;
+      }
+    }
+    const int first = __builtin_amdgcn_readfirstlane(first_row(e));
+    const int rows = __builtin_amdgcn_readfirstlane(rows_of(e, first));
+    const int n = (rows + C::BM - 1) / C::BM;
+    const int start = __builtin_amdgcn_readfirstlane(table[e]) - n;
+    const int local = i - start * col_tiles;
+    return mx_tile(e, first, rows, local % n, n, local / n);
+  };
+
+  // What a tile's loads need: where its operands begin, its column, and this lane's rows of A (-1: none).
+  const int lr = lane >> 3;
+  const uint32_t piece = ((lane & 7) ^ lr >> 1) * 16;
+  const uint32_t a_rows = P.route_of_row ? P.a_rows : C::BM;  // rows past a tile's end are not asked for
+  struct Source {
+    const uint8_t *wq, *ws, *aq, *as;
+    int n0, x[C::kLoad];
+  };
+  auto source = [&](const MxItem& it, Source& s) {
+    s.n0 = it.col * C::BN;
+    s.wq = P.w_codes + (long)it.e * P.N * krow;
+    s.ws = P.w_sf + (long)it.e * P.N * srow;
+    const long base = P.route_of_row ? 0 : it.row0;
+    s.aq = P.a_codes + base * krow;
+    s.as = P.a_sf + base * srow;
+#pragma unroll
+    for (int i = 0; i < C::kLoad; ++i) {
+      const int m = 8 * (wave * C::kLoad + i) + lr;
+      s.x[i] = m < it.rows ? m : -1;
+      if (P.route_of_row && m < it.rows) {
+        const int f = P.route_of_row[it.row0 + m];
+        s.x[i] = f >= 0 && f / P.topk < P.a_rows ? f / P.topk : -1;
+      }
+    }
+  };
+  // The rows' offsets are computed at each load: kept, they would not fit in registers.
+  auto opaque = [](int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+  };
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(lds));
+  auto load_codes = [&](const Source& s, int st, int slot, bool any) {  // any: else zeros
+    const uint32_t to = lds0 + slot * C::kStage + wave * C::kLoad * 1024;
+    const uint32_t kb = (uint32_t)st * 128 + piece, kx = kb ^ 64;
+    const uint32_t k[2] = {any && kb < krow ? kb : kPast, any && kx < krow ? kx : kPast};
+    const uint32_t w = (uint32_t)opaque(s.n0 + 8 * wave * C::kLoad + lr) * krow;
+    const intx4 wq = raw_buffer(s.wq, (uint32_t)P.N * krow), aq = raw_buffer(s.aq, a_rows * krow);
+#pragma unroll
+    for (int i = 0; i < C::kLoad; ++i) {
+      const int x = opaque(s.x[i]);
+      load_lds16(aq, (x < 0 ? kNoRow : (uint32_t)x * krow) + k[i & 1], to + C::BN * 128 + i * 1024);
+      load_lds16(wq, w + i * 8 * krow + k[i & 1], to + i * 1024);
+    }
+  };
+  // Scales of two stages: 4 dwords of a row, 16 rows a load. Lane l's row of A is the one
+  // that lanes 8 (l / 4 % 8) of the codes' loads 2i + l / 32 have.
+  auto load_scales = [&](const Source& s, int pair, int buf, bool any) {
+    const uint32_t to = lds0 + 2 * C::kStage + buf * C::kScales + wave * C::kLoad * 128;
+    const uint32_t kb = (uint32_t)pair * 16 + (lane & 3) * 4;
+    const uint32_t k = any && kb < srow ? kb : kPast;
+    const uint32_t w = (uint32_t)opaque(s.n0 + 8 * wave * C::kLoad + (lane >> 2)) * srow + k;
+    const intx4 ws = raw_buffer(s.ws, (uint32_t)P.N * srow), as = raw_buffer(s.as, a_rows * srow);
+#pragma unroll
+    for (int i = 0; i < C::kLoad / 2; ++i) {
+      const int from = (lane >> 2 & 7) * 8;
+      const int lo = __shfl(s.x[2 * i], from, 64), hi = __shfl(s.x[2 * i + 1], from, 64);
+      const int x = lane < 32 ? lo : hi;
+      load_lds4(as, (x < 0 ? kNoRow : (uint32_t)x * srow) + k, to + C::BN * 16 + i * 256);
+      load_lds4(ws, w + i * 16 * srow, to + i * 256);
+    }
+  };
+
+  const int wn = wave % C::WN, wm = wave / C::WN;
+  const int half = lane >> 5, r32 = lane & 31;
+  // Row groups of 32 alternate between the waves that share columns.
+  const int w_at = wn * C::NW * 32 + r32, x_at = C::BN + wm * 32 + r32;
+  struct Frags {
+    intx4 w[C::NW], x[C::MW];
+  };
+  struct Scales {
+    int w[C::NW], x[C::MW];  // of the four steps of a stage
+  };
+  auto read = [&](Frags& v, int slot, int j) {
+    const uint8_t* b = lds + slot * C::kStage + ((4 * half + j) ^ (lane >> 1 & 7)) * 16;
+#pragma unroll
+    for (int g = 0; g < C::MW; ++g) v.x[g] = *reinterpret_cast<const intx4*>(b + (x_at + 64 * g) * 128);
+#pragma unroll
+    for (int f = 0; f < C::NW; ++f) v.w[f] = *reinterpret_cast<const intx4*>(b + (w_at + 32 * f) * 128);
+  };
+  auto read_scales = [&](Scales& v, int buf, int odd_stage) {
+    const uint8_t* b = lds + 2 * C::kStage + buf * C::kScales + odd_stage * 8 + half * 4;
+#pragma unroll
+    for (int g = 0; g < C::MW; ++g) v.x[g] = *reinterpret_cast<const int*>(b + (x_at + 64 * g) * 16);
+#pragma unroll
+    for (int f = 0; f < C::NW; ++f) v.w[f] = *reinterpret_cast<const int*>(b + (w_at + 32 * f) * 16);
+  };
+
+  // Stages come in pairs: stage st is in slot st % 2, its scales in the buffer of its pair.
+  const int pairs = (P.Kd + 511) / 512;
+  MxItem it = find(item);
+  Source src, nxt;
+  source(it, src);
+  load_scales(src, 0, 0, true);
+  load_codes(src, 0, 0, true);
+  load_codes(src, 1, 1, true);
+  wait_loads<2 * C::kLoad>();
+  lds_barrier();
+  Frags even, odd;
+  Scales sc;
+  read_scales(sc, 0, 0);
+  read(even, 0, 0);
+  int buf = 0;
+  bool more = false;
+
+  // One tile, of which this wave multiplies kG groups of 32 rows.
+  auto tile = [&](auto G) {
+    constexpr int kG = decltype(G)::value;
+    floatx16 acc[C::NW][kG];
+#pragma unroll
+    for (int f = 0; f < C::NW; ++f)
+#pragma unroll
+      for (int g = 0; g < kG; ++g)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[f][g][i] = 0.0f;
+    auto multiply = [&](const Frags& v, const Scales& t, auto J) {
+      constexpr int j = decltype(J)::value;
+      auto wide = [](intx4 u) { return intx8{u[0], u[1], u[2], u[3], 0, 0, 0, 0}; };
+#pragma unroll
+      for (int g = 0; g < kG; ++g)
+#pragma unroll
+        for (int f = 0; f < C::NW; ++f)
+          acc[f][g] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(v.w[f]), wide(v.x[g]), acc[f][g], 4, 4, j,
+                                                                      t.w[f], j, t.x[g]);
+    };
+    // The stage in slot `slot`, the odd or the even one of its pair. At its barrier
+    // every wave has read all of it, and the loads of the stage behind it have
+    // landed; `load` may then fill its slot and, in an even stage, the other pair's scales.
+    auto stage = [&](auto Slot, auto load) {
+      constexpr int slot = decltype(Slot)::value;
+      read(odd, slot, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(even, sc, std::integral_constant<int, 0>{});
+      __builtin_amdgcn_sched_barrier(0);
+      read(even, slot, 2);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(odd, sc, std::integral_constant<int, 1>{});
+      __builtin_amdgcn_sched_barrier(0);
+      read(odd, slot, 3);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(even, sc, std::integral_constant<int, 2>{});
+      __builtin_amdgcn_sched_barrier(0);
+      wait_loads<0>();
+      lds_barrier();
+      Scales next;
+      read(even, slot ^ 1, 0);
+      if constexpr (slot == 1) buf ^= 1;
+      read_scales(next, buf, slot ^ 1);
+      load();
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(odd, sc, std::integral_constant<int, 3>{});
+      __builtin_amdgcn_sched_barrier(0);
+      sc = next;
+    };
+    constexpr auto slot0 = std::integral_constant<int, 0>{};
+    constexpr auto slot1 = std::integral_constant<int, 1>{};
+    for (int p = 0; p < pairs - 1; ++p) {
+      stage(slot0, [&] {
+        load_codes(src, 2 * p + 2, 0, true);
+        load_scales(src, p + 1, buf ^ 1, true);
+      });
+      stage(slot1, [&] { load_codes(src, 2 * p + 3, 1, true); });
+    }
+    stage(slot0, [&] {
+      load_codes(nxt, 0, 0, more);
+      load_scales(nxt, 0, buf ^ 1, more);
+    });
+    stage(slot1, [&] {});
+    // All products are issued before the epilogue: left to the compiler, some move into its branches.
+#pragma unroll
+    for (int f = 0; f < C::NW; ++f)
+#pragma unroll
+      for (int g = 0; g < kG; ++g) asm volatile("" : "+v"(acc[f][g]));
+
+    // The second slot is free until the next tile's second stage. acc[f][g][i] is
+    // column 32 f + 8 (i / 4) + 4 half + i % 4 of row r32 of group g; a group's rows
+    // go through this wave's own piece of the slot, so that a store covers whole rows of it.
+    uint8_t* mine = lds + C::kStage + wave * 32 * C::kOutRow;
+    const int n0 = it.col * C::BN + wn * C::NW * 32;
+    const int cols = min(P.N - n0, C::NW * 32);
+    constexpr int kSize = kF32 ? 4 : 2, kPasses = kF32 ? 2 : 1, kWidth = C::NW * 32 / kPasses;
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      const int m0 = (g * C::WM + wm) * 32;
+      const int rows = min(it.rows - m0, 32);
+      uint8_t* out = static_cast<uint8_t*>(P.out) + ((long)(it.row0 + m0) * P.N + n0) * kSize;
+#pragma unroll
+      for (int h = 0; h < kPasses; ++h) {
+#pragma unroll
+        for (int f = 0; f < C::NW; ++f) {
+          if (kF32 && f != h) continue;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const floatx16& a = acc[f][g];
+            uint2* to = reinterpret_cast<uint2*>(mine + r32 * C::kOutRow + ((kF32 ? 0 : 32 * f) + 8 * q + 4 * half) * kSize);
+            if constexpr (kF32) {
+              to[0] = make_uint2(__float_as_uint(a[4 * q]), __float_as_uint(a[4 * q + 1]));
+              to[1] = make_uint2(__float_as_uint(a[4 * q + 2]), __float_as_uint(a[4 * q + 3]));
+            } else {
+              *to = make_uint2(f32x2_to_bf16x2(a[4 * q], a[4 * q + 1]), f32x2_to_bf16x2(a[4 * q + 2], a[4 * q + 3]));
+            }
+          }
+        }
+        const int have = min(max(cols - h * kWidth, 0), kWidth) * kSize;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // 8 lanes to a row of 128 bytes
+          const int r = 8 * i + lr, at = (lane & 7) * 16;
+          const uint2* from = reinterpret_cast<const uint2*>(mine + r * C::kOutRow + at);
+          const uint2 a = from[0], b = from[1];
+          if (r < rows && at < have)
+            *reinterpret_cast<uint4*>(out + (long)r * P.N * kSize + h * kWidth * kSize + at) = make_uint4(a.x, a.y, b.x, b.y);
+        }
+      }
+    }
+  };
+
+  for (;;) {
+    const int next_item = item + step;
+    more = next_item < last_item;
+    MxItem ahead = it;
+    if (more) ahead = find(next_item);
+    source(ahead, nxt);
+    switch (((it.rows + 31) / 32 - wm + 1) / 2) {
+      case 0:  // no row for this wave; it still loads, and meets the others at the barriers
+      case 1: tile(std::integral_constant<int, 1>{}); break;
+      case 2: tile(std::integral_constant<int, 2>{}); break;
+      case 3: tile(std::integral_constant<int, 3>{}); break;
+      default: tile(std::integral_constant<int, 4>{}); break;
+    }
+    if (!more) break;
+    lds_barrier();
+    load_codes(nxt, 1, 1, true);
+    src = nxt;
+    it = ahead;
+    item = next_item;
+  }
+  wait_loads<0>();  // no load may land in LDS after the workgroup's end
+}
+
+static hipError_t run_gemm_wide(const MxGemmParams& p, hipStream_t s) {
+  if (p.out_f32)
+    mx_gemm_wide_kernel<true><<<256, 512, 0, s>>>(p);
+  else
+    mx_gemm_wide_kernel<false><<<256, 512, 0, s>>>(p);
+  return hipGetLastError();
 }
 
 template <class C>
@@ -314,7 +692,7 @@ hipError_t launch_mx_gemm(const MxGemmParams& p, hipStream_t s) {
   const bool bytes = p.Kd % 128 != 0;
   const long mean = (long)p.R / p.E;
   if (mean <= 48) return bytes ? run_gemm<MxTile<1, 1, 4, 1, 3, true>>(p, s) : run_gemm<MxTile<1, 1, 4, 1, 3, false>>(p, s);
-  return bytes ? run_gemm<MxTile<4, 2, 2, 2, 2, true>>(p, s) : run_gemm<MxTile<4, 2, 2, 2, 3, false>>(p, s);
+  return bytes ? run_gemm<MxTile<4, 2, 2, 2, 2, true>>(p, s) : run_gemm_wide(p, s);
 }
 
 // ---------------------------------------------------------------- backward
@@ -326,51 +704,50 @@ hipError_t launch_mx_gemm(const MxGemmParams& p, hipStream_t s) {
 // through LDS. A wave owns 128 columns and every row of the tile, so a matrix tile
 // is converted once a workgroup.
 //
-// A stage is 64 rows n of the matrix (512 columns: 256 bytes a row, 16 scales)
-// and 64 columns of dy. Matrix rows with (n / 8) odd have their two halves of
-// each 128 bytes exchanged, so that the two halves of a wave, 8 rows apart, read
-// different banks.
-template <int MW_, int S_, bool kBytes_>
+// A stage is 64 rows n of the matrix (KW * 128 columns: KW * 64 bytes a row, KW
+// * 4 scales) and 64 columns of dy, four steps of 16. The codes of a step are read two steps
+// ahead and converted one step ahead, between the products of the step before:
+// products and conversions run in different pipes, but a wave issues in order.
+// Matrix rows with (n / 8) odd have the halves of each 128 bytes exchanged, so
+// that the two halves of a wave, 8 rows apart, read different banks.
+template <int MW_, int KW_, int S_, bool kBytes_>
 struct MxBackTile {
-  static constexpr int MW = MW_, S = S_;
+  static constexpr int MW = MW_, KW = KW_, S = S_;
   static constexpr bool kBytes = kBytes_;
-  static constexpr int kWaves = 4, BK = 128 * kWaves, BM = 32 * MW, kN = 64;
-  static constexpr int kScaleRow = kBytes ? 64 : 16;
-  static constexpr int kW = kN * BK / 2, kS = kN * kScaleRow, kStage = kW + kS + BM * kN * 2;
+  static constexpr int kWaves = KW, BK = 128 * KW, BM = 32 * MW, kN = 64, kRow = BK / 2;
+  static constexpr int kScaleRow = kBytes ? 16 * KW : 4 * KW;
+  static constexpr int kW = kN * kRow, kS = kN * kScaleRow, kStage = kW + kS + BM * kN * 2;
   static constexpr int kLoadW = kW / 1024 / kWaves, kLoadS = kS / 256 / kWaves, kLoadY = BM / 8 / kWaves;
   static constexpr int kLoads = kLoadW + kLoadS + kLoadY;
+  static_assert(BM % (8 * kWaves) == 0 && (S - 2) * kLoads < 64, "whole loads, counted in 6 bits");
 };
 
-template <class C>
-__global__ __launch_bounds__(256) void mx_gemm_backward_kernel(MxGemmParams P) {
-  __shared__ __attribute__((aligned(128))) uint8_t lds[C::S * C::kStage];
+// One tile of G groups of 32 rows.
+template <class C, int G>
+__device__ __forceinline__ void mx_back_tile(const MxGemmParams& P, uint8_t* lds, const MxItem& it) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  MxItem it;
-  if (!mx_item<C::BM>(P.offsets, P.E, P.R, (P.Kd + C::BK - 1) / C::BK, it)) return;
   const int k0 = it.col * C::BK;
   const uint32_t krow = P.Kd / 2, srow = P.Kd / kMxBlock, yrow = (uint32_t)P.N * 2;
   const intx4 wq = raw_buffer(P.w_codes + (long)it.e * P.N * krow, (uint32_t)P.N * krow);
   const intx4 ws = raw_buffer(P.w_sf + (long)it.e * P.N * srow, (uint32_t)P.N * srow);
   const intx4 dy = raw_buffer(P.a_codes + (long)it.row0 * yrow, (uint32_t)it.rows * yrow);
 
-  // Loads of this lane: 16 bytes of codes of 1 in 4 rows, a dword (byte) of scales, 16 bytes of dy of 1 in 8 rows.
-  const int wr = lane >> 4, slot16 = lane & 15;
-  const int sr = C::kBytes ? lane >> 4 : lane >> 2;
-  constexpr int kSRows = C::kBytes ? 4 : 16;
-  const uint32_t s_k = k0 / kMxBlock + (C::kBytes ? lane & 15 : (lane & 3) * 4);
-  const int yr = lane >> 3;
-  const uint32_t y_piece = ((lane & 7) ^ yr) * 16;
+  // Loads of this lane: 16 bytes of codes, a dword (byte) of scales, 16 bytes of dy.
+  constexpr int kPer = C::kRow / 16, kWRows = 64 / kPer;            // lanes of a matrix row, rows of a load
+  constexpr int kSPer = C::kBytes ? 4 * C::KW : C::KW, kSRows = 64 / kSPer;
+  const int wr = lane / kPer, sr = lane / kSPer, yr = lane >> 3;
+  const uint32_t s_k = k0 / kMxBlock + lane % kSPer * (C::kBytes ? 1 : 4);
+  const uint32_t y_piece = ((lane & 7) ^ yr >> 1) * 16;  // ^ 64 in odd loads
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(lds));
   auto issue = [&](int st, int slot) {
     const uint32_t to = lds0 + slot * C::kStage;
     const uint32_t n0 = (uint32_t)st * C::kN;
 #pragma unroll
     for (int i = 0; i < C::kLoadW; ++i) {
-      const int q = wave * C::kLoadW + i;                    // rows 4q .. 4q + 3
-      const uint32_t k = k0 / 2 + ((slot16 ^ ((q >> 1 & 1) << 2)) * 16);
-      const uint32_t n = n0 + 4 * q + wr;
-      load_lds16(wq, n < (uint32_t)P.N && k < krow ? n * krow + k : kNoRow, to + q * 1024);
+      const int q = wave * C::kLoadW + i, row = kWRows * q + wr;
+      const uint32_t k = k0 / 2 + ((lane % kPer) ^ (C::KW > 1 ? (row >> 3 & 1) << 2 : 0)) * 16;
+      load_lds16(wq, n0 + row < (uint32_t)P.N && k < krow ? (n0 + row) * krow + k : kNoRow, to + q * 1024);
     }
 #pragma unroll
     for (int i = 0; i < C::kLoadS; ++i) {
@@ -382,78 +759,116 @@ __global__ __launch_bounds__(256) void mx_gemm_backward_kernel(MxGemmParams P) {
       else
         load_lds4(ws, at, to + C::kW + q * 256);
     }
-    const uint32_t yb = n0 * 2 + y_piece;
 #pragma unroll
     for (int i = 0; i < C::kLoadY; ++i) {
       const int q = wave * C::kLoadY + i;
-      const uint32_t m = 8 * q + yr;
+      const uint32_t m = 8 * q + yr, yb = n0 * 2 + (y_piece ^ (q & 1) * 64);
       load_lds16(dy, m < (uint32_t)it.rows && yb < yrow ? m * yrow + yb : kNoRow, to + C::kW + C::kS + q * 1024);
     }
   };
 
-  floatx16 acc[4][C::MW];
+  floatx16 acc[4][G];
 #pragma unroll
   for (int f = 0; f < 4; ++f)
 #pragma unroll
-    for (int g = 0; g < C::MW; ++g)
+    for (int g = 0; g < G; ++g)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[f][g][i] = 0.0f;
 
   const int half = lane >> 5, c = lane & 31;
-  const int w_at = half * 8 * (C::BK / 2) + ((wave * 64 + c * 2) ^ (half << 6));
-  const int s_at = C::kBytes ? half * 8 * 64 + (wave * 4 + (c >> 3)) * 4 : half * 8 * 16 + wave * 4 + (c >> 3);
-  auto compute = [&](int slot) {
+  const int w_at = half * 8 * C::kRow + ((wave * 64 + c * 2) ^ (C::KW > 1 ? half << 6 : 0));
+  const int s_at = half * 8 * C::kScaleRow + (wave * 4 + (c >> 3)) * (C::kBytes ? 4 : 1);
+  struct Raw {
+    uint16_t q[8];   // codes of columns 4c .. 4c + 3 of 8 rows
+    uint8_t s[8];    // their scales
+    bf16x8_t x[G];
+  };
+  auto read = [&](Raw& v, int slot, int j) {
     const uint8_t* b = lds + slot * C::kStage;
-    const uint8_t* sc = b + C::kW + s_at;
-    const uint8_t* y = b + C::kW + C::kS;
 #pragma unroll
-    for (int st = 0; st < C::kN / 16; ++st) {
-      uint32_t lo[8], hi[8];  // columns 0, 1 and 2, 3 of each of 8 rows
+    for (int i = 0; i < 8; ++i) v.q[i] = *reinterpret_cast<const uint16_t*>(b + (16 * j + i) * C::kRow + w_at);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t q = *reinterpret_cast<const uint16_t*>(b + (16 * st + i) * (C::BK / 2) + w_at);
-        const float s = mx_scale(sc[(16 * st + i) * C::kScaleRow]);
-        lo[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0));
-        hi[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1));
-      }
-      bf16x8_t w[4];
-      auto regroup = [](const uint32_t(&v)[8], uint32_t sel) {
-        const uint32_t p[4] = {__builtin_amdgcn_perm(v[1], v[0], sel), __builtin_amdgcn_perm(v[3], v[2], sel),
-                               __builtin_amdgcn_perm(v[5], v[4], sel), __builtin_amdgcn_perm(v[7], v[6], sel)};
-        bf16x8_t r;
-        __builtin_memcpy(&r, p, 16);
-        return r;
-      };
-      w[0] = regroup(lo, 0x05040100u);
-      w[1] = regroup(lo, 0x07060302u);
-      w[2] = regroup(hi, 0x05040100u);
-      w[3] = regroup(hi, 0x07060302u);
+    for (int i = 0; i < 8; ++i) v.s[i] = b[C::kW + (16 * j + i) * C::kScaleRow + s_at];
 #pragma unroll
-      for (int g = 0; g < C::MW; ++g) {
-        const int m = 32 * g + c;
-        const bf16x8_t x = *reinterpret_cast<const bf16x8_t*>(y + m * 128 + (((2 * st + half) ^ (lane & 7)) * 16));
+    for (int g = 0; g < G; ++g)
+      v.x[g] = *reinterpret_cast<const bf16x8_t*>(b + C::kW + C::kS + (32 * g + c) * 128 +
+                                                  (((2 * j + half) ^ (lane >> 1 & 7)) * 16));
+  };
+  // Conversion in 16 pieces: piece i < 8 converts row i, piece 8 + i makes two words of the fragments.
+  struct Frags {
+    uint32_t lo[8], hi[8];  // columns 0, 1 and 2, 3 of each row
+    uint32_t w[4][4];
+  };
+  auto convert = [&](const Raw& v, Frags& f, int piece) {
+    if (piece < 8) {
+      const float s = mx_scale(v.s[piece]);
+      f.lo[piece] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((uint32_t)v.q[piece], s, 0));
+      f.hi[piece] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((uint32_t)v.q[piece], s, 1));
+    } else {
+      const int p = piece - 8, pair = p & 3, h = p >> 2;
+      const uint32_t a = h ? f.hi[2 * pair] : f.lo[2 * pair], b = h ? f.hi[2 * pair + 1] : f.lo[2 * pair + 1];
+      f.w[2 * h][pair] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+      f.w[2 * h + 1][pair] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+    }
+  };
+  // The products of one step, and between them the conversion of the next.
+  auto step = [&](const Frags& f, const Raw& v, const Raw& next, Frags& nf) {
+    constexpr int kProducts = 4 * G;
 #pragma unroll
-        for (int f = 0; f < 4; ++f) acc[f][g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[f], x, acc[f][g], 0, 0, 0);
-      }
+    for (int i = 0; i < kProducts; ++i) {
+      const int g = i / 4, k = i % 4;
+      bf16x8_t w;
+      __builtin_memcpy(&w, f.w[k], 16);
+      acc[k][g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, v.x[g], acc[k][g], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int p = 16 * i / kProducts; p < 16 * (i + 1) / kProducts; ++p) convert(next, nf, p);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
+  // Stage st is in slot st % S. Its last codes are read in its second step; the barrier
+  // behind that also says that stage st + 1 has landed for every wave.
   const int stages = (P.N + C::kN - 1) / C::kN;
 #pragma unroll
-  for (int s = 0; s < C::S - 1; ++s) issue(s, s);
+  for (int s = 0; s < C::S; ++s) issue(s, s);
+  wait_loads<(C::S - 1) * C::kLoads>();
+  lds_barrier();
+  Raw r0, r1, r2, r3;
+  Frags even, odd;
+  read(r0, 0, 0);
+  read(r1, 0, 1);
+#pragma unroll
+  for (int p = 0; p < 16; ++p) convert(r0, even, p);
   int slot = 0;
   for (int st = 0; st < stages; ++st) {
+    const int next = slot == C::S - 1 ? 0 : slot + 1;
+    read(r2, slot, 2);
+    __builtin_amdgcn_sched_barrier(0);
+    step(even, r0, r1, odd);
+    read(r3, slot, 3);
+    __builtin_amdgcn_sched_barrier(0);
+    step(odd, r1, r2, even);
     wait_loads<(C::S - 2) * C::kLoads>();
     lds_barrier();
-    issue(st + C::S - 1, slot == 0 ? C::S - 1 : slot - 1);
-    compute(slot);
-    slot = slot == C::S - 1 ? 0 : slot + 1;
+    read(r0, next, 0);
+    issue(st + C::S, slot);
+    __builtin_amdgcn_sched_barrier(0);
+    step(even, r2, r3, odd);
+    read(r1, next, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    step(odd, r3, r0, even);
+    slot = next;
   }
   wait_loads<0>();
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int g = 0; g < G; ++g) asm volatile("" : "+v"(acc[f][g]));  // no product moves into the branches below
 
   // acc[f][g][i] is column 4 (8 (i / 4) + 4 half + i % 4) + f of the wave's 128, row 32 g + c.
 #pragma unroll
-  for (int g = 0; g < C::MW; ++g) {
+  for (int g = 0; g < G; ++g) {
     const int m = 32 * g + c;
     if (m >= it.rows) continue;
     uint16_t* out = static_cast<uint16_t*>(P.out) + (long)(it.row0 + m) * P.Kd;
@@ -472,10 +887,23 @@ __global__ __launch_bounds__(256) void mx_gemm_backward_kernel(MxGemmParams P) {
 }
 
 template <class C>
+__global__ __launch_bounds__(C::kWaves * 64) void mx_gemm_backward_kernel(MxGemmParams P) {
+  __shared__ __attribute__((aligned(128))) uint8_t lds[C::S * C::kStage];
+  MxItem it;
+  if (!mx_item<C::BM>(P.offsets, P.E, P.R, (P.Kd + C::BK - 1) / C::BK, it)) return;
+  switch ((it.rows + 31) / 32) {
+    case 1: mx_back_tile<C, 1>(P, lds, it); break;
+    case 2: mx_back_tile<C, C::MW < 2 ? C::MW : 2>(P, lds, it); break;
+    case 3: mx_back_tile<C, C::MW < 3 ? C::MW : 3>(P, lds, it); break;
+    default: mx_back_tile<C, C::MW>(P, lds, it); break;
+  }
+}
+
+template <class C>
 static hipError_t run_gemm_backward(const MxGemmParams& p, hipStream_t s) {
   const long tiles = (long)p.R / C::BM + (p.E < p.R ? p.E : p.R);
   const long grid = (tiles * ((p.Kd + C::BK - 1) / C::BK) + 7) / 8 * 8;
-  mx_gemm_backward_kernel<C><<<(unsigned)grid, 256, 0, s>>>(p);
+  mx_gemm_backward_kernel<C><<<(unsigned)grid, C::kWaves * 64, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -483,8 +911,8 @@ hipError_t launch_mx_gemm_backward(const MxGemmParams& p, hipStream_t s) {
   const bool bytes = p.Kd % 128 != 0;
   const long mean = (long)p.R / p.E;
   if (mean <= 48)
-    return bytes ? run_gemm_backward<MxBackTile<1, 3, true>>(p, s) : run_gemm_backward<MxBackTile<1, 3, false>>(p, s);
-  return bytes ? run_gemm_backward<MxBackTile<4, 3, true>>(p, s) : run_gemm_backward<MxBackTile<4, 4, false>>(p, s);
+    return bytes ? run_gemm_backward<MxBackTile<1, 4, 3, true>>(p, s) : run_gemm_backward<MxBackTile<1, 4, 3, false>>(p, s);
+  return bytes ? run_gemm_backward<MxBackTile<4, 4, 3, true>>(p, s) : run_gemm_backward<MxBackTile<4, 4, 4, false>>(p, s);
 }
 
 }  // namespace pmoe
