@@ -377,16 +377,22 @@ __global__ __launch_bounds__(C::kWaves * 64) void mx_gemm_kernel(MxGemmParams P)
 // and two dwords of every row each stage cost as much as the codes.
 // An expert's rows are shared out evenly over its tiles in groups of 32, and a wave
 // multiplies the groups that its tile has.
+// Where Kd is not a multiple of 128, rows of scales are not whole dwords: they are loaded
+// byte by byte, each stage its own, 4 bytes of LDS a scale, beside tiles of 192 rows.
+template <int MW_, bool kBytes_>
 struct MxWide {
-  static constexpr int NW = 2, MW = 4, WN = 4, WM = 2, kWaves = 8, BN = 256, BM = 256, kRows = BN + BM;
-  static constexpr int kStage = kRows * 128, kScales = kRows * 16, kLoad = 4;  // 1 KB loads of a wave and operand
+  static constexpr int NW = 2, MW = MW_, WN = 4, WM = 2, kWaves = WN * WM, BN = 32 * NW * WN, BM = 32 * MW * WM;
+  static constexpr bool kBytes = kBytes_;
+  static constexpr int kRows = BN + BM, kStage = kRows * 128;
+  static constexpr int kScaleRow = kBytes ? 32 : 16, kScales = kRows * kScaleRow;  // of a stage, of a pair of stages
+  static constexpr int kLoadW = BN / 8 / kWaves, kLoadX = BM / 8 / kWaves, kLoads = kLoadW + kLoadX;  // 1 KB loads of a wave
   static constexpr int kOutRow = 64 * NW + 8;
   static constexpr int kTable = 2 * kStage + 2 * kScales, kLds = kTable + kMaxExperts * 4;
+  static_assert(kWaves * 32 * kOutRow <= kStage && kLds <= 163840 && (kBytes || kLoadX % 2 == 0), "room and whole loads");
 };
 
-template <bool kF32>
-__global__ __launch_bounds__(512) void mx_gemm_wide_kernel(MxGemmParams P) {
-  using C = MxWide;
+template <class C, bool kF32>
+__global__ __launch_bounds__(C::kWaves * 64) void mx_gemm_wide_kernel(MxGemmParams P) {
   __shared__ __attribute__((aligned(128))) uint8_t lds[C::kLds];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -440,7 +446,7 @@ __global__ __launch_bounds__(512) void mx_gemm_wide_kernel(MxGemmParams P) {
   const uint32_t a_rows = P.route_of_row ? P.a_rows : C::BM;  // rows past a tile's end are not asked for
   struct Source {
     const uint8_t *wq, *ws, *aq, *as;
-    int n0, x[C::kLoad];
+    int n0, x[C::kLoadX];
   };
   auto source = [&](const MxItem& it, Source& s) {
     s.n0 = it.col * C::BN;
@@ -450,8 +456,8 @@ __global__ __launch_bounds__(512) void mx_gemm_wide_kernel(MxGemmParams P) {
     s.aq = P.a_codes + base * krow;
     s.as = P.a_sf + base * srow;
 #pragma unroll
-    for (int i = 0; i < C::kLoad; ++i) {
-      const int m = 8 * (wave * C::kLoad + i) + lr;
+    for (int i = 0; i < C::kLoadX; ++i) {
+      const int m = 8 * (wave * C::kLoadX + i) + lr;
       s.x[i] = m < it.rows ? m : -1;
       if (P.route_of_row && m < it.rows) {
         const int f = P.route_of_row[it.row0 + m];
@@ -465,34 +471,59 @@ __global__ __launch_bounds__(512) void mx_gemm_wide_kernel(MxGemmParams P) {
     return v;
   };
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(lds));
-  auto load_codes = [&](const Source& s, int st, int slot, bool any) {  // any: else zeros
-    const uint32_t to = lds0 + slot * C::kStage + wave * C::kLoad * 1024;
+  // The loads of a stage's codes and of its scales (kBytes) or, in an even stage, of
+  // its pair's, in parts; !any: zeros.
+  auto row_of = [&](const Source& s, int i, uint32_t row) {
+    const int x = opaque(s.x[i]);
+    return x < 0 ? kNoRow : (uint32_t)x * row;
+  };
+  auto load_codes = [&](const Source& s, int st, int slot, bool any, int part, int parts) {
+    const uint32_t to = lds0 + slot * C::kStage;
     const uint32_t kb = (uint32_t)st * 128 + piece, kx = kb ^ 64;
     const uint32_t k[2] = {any && kb < krow ? kb : kPast, any && kx < krow ? kx : kPast};
-    const uint32_t w = (uint32_t)opaque(s.n0 + 8 * wave * C::kLoad + lr) * krow;
+    const uint32_t w = (uint32_t)opaque(s.n0 + 8 * wave * C::kLoadW + lr) * krow;
     const intx4 wq = raw_buffer(s.wq, (uint32_t)P.N * krow), aq = raw_buffer(s.aq, a_rows * krow);
 #pragma unroll
-    for (int i = 0; i < C::kLoad; ++i) {
-      const int x = opaque(s.x[i]);
-      load_lds16(aq, (x < 0 ? kNoRow : (uint32_t)x * krow) + k[i & 1], to + C::BN * 128 + i * 1024);
-      load_lds16(wq, w + i * 8 * krow + k[i & 1], to + i * 1024);
+    for (int l = C::kLoads * part / parts; l < C::kLoads * (part + 1) / parts; ++l) {
+      if (l < C::kLoadX) {
+        const int q = wave * C::kLoadX + l;
+        load_lds16(aq, row_of(s, l, krow) + k[q & 1], to + C::BN * 128 + q * 1024);
+      } else {
+        const int i = l - C::kLoadX;
+        load_lds16(wq, w + i * 8 * krow + k[i & 1], to + (wave * C::kLoadW + i) * 1024);
+      }
     }
   };
-  // Scales of two stages: 4 dwords of a row, 16 rows a load. Lane l's row of A is the one
-  // that lanes 8 (l / 4 % 8) of the codes' loads 2i + l / 32 have.
-  auto load_scales = [&](const Source& s, int pair, int buf, bool any) {
-    const uint32_t to = lds0 + 2 * C::kStage + buf * C::kScales + wave * C::kLoad * 128;
-    const uint32_t kb = (uint32_t)pair * 16 + (lane & 3) * 4;
-    const uint32_t k = any && kb < srow ? kb : kPast;
-    const uint32_t w = (uint32_t)opaque(s.n0 + 8 * wave * C::kLoad + (lane >> 2)) * srow + k;
+  auto load_scales = [&](const Source& s, int at, int buf, bool any, int part, int parts) {
+    const uint32_t to = lds0 + 2 * C::kStage + buf * C::kScales;
     const intx4 ws = raw_buffer(s.ws, (uint32_t)P.N * srow), as = raw_buffer(s.as, a_rows * srow);
+    if constexpr (C::kBytes) {  // 8 scales of 8 rows a load, stage `at`
+      const uint32_t kb = (uint32_t)at * 8 + (lane & 7);
+      const uint32_t k = any && kb < srow ? kb : kPast;
+      const uint32_t w = (uint32_t)opaque(s.n0 + 8 * wave * C::kLoadW + lr) * srow + k;
 #pragma unroll
-    for (int i = 0; i < C::kLoad / 2; ++i) {
-      const int from = (lane >> 2 & 7) * 8;
-      const int lo = __shfl(s.x[2 * i], from, 64), hi = __shfl(s.x[2 * i + 1], from, 64);
-      const int x = lane < 32 ? lo : hi;
-      load_lds4(as, (x < 0 ? kNoRow : (uint32_t)x * srow) + k, to + C::BN * 16 + i * 256);
-      load_lds4(ws, w + i * 16 * srow, to + i * 256);
+      for (int l = C::kLoads * part / parts; l < C::kLoads * (part + 1) / parts; ++l) {
+        if (l < C::kLoadX)
+          load_lds1(as, row_of(s, l, srow) + k, to + C::BN * 32 + (wave * C::kLoadX + l) * 256);
+        else
+          load_lds1(ws, w + (l - C::kLoadX) * 8 * srow, to + (wave * C::kLoadW + l - C::kLoadX) * 256);
+      }
+    } else {  // 4 dwords of 16 rows a load, pair `at`; a lane's row of A is what lanes 8 (l / 4 % 8) have of codes' loads 2i + l / 32
+      const uint32_t kb = (uint32_t)at * 16 + (lane & 3) * 4;
+      const uint32_t k = any && kb < srow ? kb : kPast;
+      const uint32_t w = (uint32_t)opaque(s.n0 + 8 * wave * C::kLoadW + (lane >> 2)) * srow + k;
+      constexpr int kX = C::kLoadX / 2, kAll = kX + C::kLoadW / 2;
+#pragma unroll
+      for (int l = kAll * part / parts; l < kAll * (part + 1) / parts; ++l) {
+        if (l < kX) {
+          const int from = (lane >> 2 & 7) * 8;
+          const int lo = __shfl(s.x[2 * l], from, 64), hi = __shfl(s.x[2 * l + 1 < C::kLoadX ? 2 * l + 1 : 0], from, 64);
+          const int x = lane < 32 ? lo : hi;
+          load_lds4(as, (x < 0 ? kNoRow : (uint32_t)x * srow) + k, to + C::BN * 16 + (wave * kX + l) * 256);
+        } else {
+          load_lds4(ws, w + (l - kX) * 16 * srow, to + (wave * (C::kLoadW / 2) + l - kX) * 256);
+        }
+      }
     }
   };
 
@@ -503,38 +534,47 @@ __global__ __launch_bounds__(512) void mx_gemm_wide_kernel(MxGemmParams P) {
   struct Frags {
     intx4 w[C::NW], x[C::MW];
   };
+  // Scales of the four steps of a stage: the bytes of one word, or (kBytes) the low bytes of four.
+  using Scale = std::conditional_t<C::kBytes, intx4, int>;
   struct Scales {
-    int w[C::NW], x[C::MW];  // of the four steps of a stage
+    Scale w[C::NW], x[C::MW];
   };
-  auto read = [&](Frags& v, int slot, int j) {
+  // Part `part` of `parts` of a step's fragments.
+  auto read = [&](Frags& v, int slot, int j, int part, int parts) {
+    constexpr int kAll = C::MW + C::NW;
     const uint8_t* b = lds + slot * C::kStage + ((4 * half + j) ^ (lane >> 1 & 7)) * 16;
 #pragma unroll
-    for (int g = 0; g < C::MW; ++g) v.x[g] = *reinterpret_cast<const intx4*>(b + (x_at + 64 * g) * 128);
-#pragma unroll
-    for (int f = 0; f < C::NW; ++f) v.w[f] = *reinterpret_cast<const intx4*>(b + (w_at + 32 * f) * 128);
+    for (int i = kAll * part / parts; i < kAll * (part + 1) / parts; ++i) {
+      if (i < C::MW)
+        v.x[i] = *reinterpret_cast<const intx4*>(b + (x_at + 64 * i) * 128);
+      else
+        v.w[i - C::MW] = *reinterpret_cast<const intx4*>(b + (w_at + 32 * (i - C::MW)) * 128);
+    }
   };
   auto read_scales = [&](Scales& v, int buf, int odd_stage) {
-    const uint8_t* b = lds + 2 * C::kStage + buf * C::kScales + odd_stage * 8 + half * 4;
+    const uint8_t* b = lds + 2 * C::kStage + buf * C::kScales + (C::kBytes ? half * 16 : odd_stage * 8 + half * 4);
 #pragma unroll
-    for (int g = 0; g < C::MW; ++g) v.x[g] = *reinterpret_cast<const int*>(b + (x_at + 64 * g) * 16);
+    for (int g = 0; g < C::MW; ++g) v.x[g] = *reinterpret_cast<const Scale*>(b + (x_at + 64 * g) * C::kScaleRow);
 #pragma unroll
-    for (int f = 0; f < C::NW; ++f) v.w[f] = *reinterpret_cast<const int*>(b + (w_at + 32 * f) * 16);
+    for (int f = 0; f < C::NW; ++f) v.w[f] = *reinterpret_cast<const Scale*>(b + (w_at + 32 * f) * C::kScaleRow);
   };
 
-  // Stages come in pairs: stage st is in slot st % 2, its scales in the buffer of its pair.
+  // Stages come in pairs: stage st is in slot st % 2, its scales in the buffer of its pair,
+  // or (kBytes) in buffer st % 2.
   const int pairs = (P.Kd + 511) / 512;
   MxItem it = find(item);
   Source src, nxt;
   source(it, src);
-  load_scales(src, 0, 0, true);
-  load_codes(src, 0, 0, true);
-  load_codes(src, 1, 1, true);
-  wait_loads<2 * C::kLoad>();
+  load_scales(src, 0, 0, true, 0, 1);
+  load_codes(src, 0, 0, true, 0, 1);
+  load_codes(src, 1, 1, true, 0, 1);
+  if constexpr (C::kBytes) load_scales(src, 1, 1, true, 0, 1);
+  wait_loads<(C::kBytes ? 2 : 1) * C::kLoads>();
   lds_barrier();
   Frags even, odd;
   Scales sc;
   read_scales(sc, 0, 0);
-  read(even, 0, 0);
+  read(even, 0, 0, 0, 1);
   int buf = 0;
   bool more = false;
 
@@ -548,59 +588,61 @@ __global__ __launch_bounds__(512) void mx_gemm_wide_kernel(MxGemmParams P) {
       for (int g = 0; g < kG; ++g)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[f][g][i] = 0.0f;
-    auto multiply = [&](const Frags& v, const Scales& t, auto J) {
+    // The products of step J, and between them what `behind` does in parts.
+    auto multiply = [&](const Frags& v, auto J, auto behind) {
       constexpr int j = decltype(J)::value;
       auto wide = [](intx4 u) { return intx8{u[0], u[1], u[2], u[3], 0, 0, 0, 0}; };
 #pragma unroll
       for (int g = 0; g < kG; ++g)
 #pragma unroll
-        for (int f = 0; f < C::NW; ++f)
-          acc[f][g] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(v.w[f]), wide(v.x[g]), acc[f][g], 4, 4, j,
-                                                                      t.w[f], j, t.x[g]);
+        for (int f = 0; f < C::NW; ++f) {
+          if constexpr (C::kBytes)
+            acc[f][g] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(v.w[f]), wide(v.x[g]), acc[f][g], 4, 4, 0,
+                                                                        sc.w[f][j], 0, sc.x[g][j]);
+          else
+            acc[f][g] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(v.w[f]), wide(v.x[g]), acc[f][g], 4, 4, j,
+                                                                        sc.w[f], j, sc.x[g]);
+          __builtin_amdgcn_sched_barrier(0);
+          behind(g * C::NW + f, kG * C::NW);
+          __builtin_amdgcn_sched_barrier(0);
+        }
     };
     // The stage in slot `slot`, the odd or the even one of its pair. At its barrier
     // every wave has read all of it, and the loads of the stage behind it have
     // landed; `load` may then fill its slot and, in an even stage, the other pair's scales.
     auto stage = [&](auto Slot, auto load) {
       constexpr int slot = decltype(Slot)::value;
-      read(odd, slot, 1);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(even, sc, std::integral_constant<int, 0>{});
-      __builtin_amdgcn_sched_barrier(0);
-      read(even, slot, 2);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(odd, sc, std::integral_constant<int, 1>{});
-      __builtin_amdgcn_sched_barrier(0);
-      read(odd, slot, 3);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(even, sc, std::integral_constant<int, 2>{});
-      __builtin_amdgcn_sched_barrier(0);
+      multiply(even, std::integral_constant<int, 0>{}, [&](int part, int parts) { read(odd, slot, 1, part, parts); });
+      multiply(odd, std::integral_constant<int, 1>{}, [&](int part, int parts) { read(even, slot, 2, part, parts); });
+      multiply(even, std::integral_constant<int, 2>{}, [&](int part, int parts) { read(odd, slot, 3, part, parts); });
       wait_loads<0>();
       lds_barrier();
       Scales next;
-      read(even, slot ^ 1, 0);
-      if constexpr (slot == 1) buf ^= 1;
-      read_scales(next, buf, slot ^ 1);
-      load();
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(odd, sc, std::integral_constant<int, 3>{});
-      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (slot == 1 && !C::kBytes) buf ^= 1;
+      read_scales(next, C::kBytes ? slot ^ 1 : buf, slot ^ 1);
+      multiply(odd, std::integral_constant<int, 3>{}, [&](int part, int parts) {
+        read(even, slot ^ 1, 0, part, parts);
+        load(part, parts);
+      });
       sc = next;
     };
     constexpr auto slot0 = std::integral_constant<int, 0>{};
     constexpr auto slot1 = std::integral_constant<int, 1>{};
     for (int p = 0; p < pairs - 1; ++p) {
-      stage(slot0, [&] {
-        load_codes(src, 2 * p + 2, 0, true);
-        load_scales(src, p + 1, buf ^ 1, true);
+      stage(slot0, [&](int part, int parts) {
+        load_codes(src, 2 * p + 2, 0, true, part, parts);
+        load_scales(src, C::kBytes ? 2 * p + 2 : p + 1, C::kBytes ? 0 : buf ^ 1, true, part, parts);
       });
-      stage(slot1, [&] { load_codes(src, 2 * p + 3, 1, true); });
+      stage(slot1, [&](int part, int parts) {
+        load_codes(src, 2 * p + 3, 1, true, part, parts);
+        if constexpr (C::kBytes) load_scales(src, 2 * p + 3, 1, true, part, parts);
+      });
     }
-    stage(slot0, [&] {
-      load_codes(nxt, 0, 0, more);
-      load_scales(nxt, 0, buf ^ 1, more);
+    stage(slot0, [&](int part, int parts) {
+      load_codes(nxt, 0, 0, more, part, parts);
+      load_scales(nxt, 0, C::kBytes ? 0 : buf ^ 1, more, part, parts);
     });
-    stage(slot1, [&] {});
+    stage(slot1, [](int, int) {});
     // All products are issued before the epilogue: left to the compiler, some move into its branches.
 #pragma unroll
     for (int f = 0; f < C::NW; ++f)
@@ -623,11 +665,11 @@ __global__ __launch_bounds__(512) void mx_gemm_wide_kernel(MxGemmParams P) {
       for (int h = 0; h < kPasses; ++h) {
 #pragma unroll
         for (int f = 0; f < C::NW; ++f) {
-          if (kF32 && f != h) continue;
+          if (f / (C::NW / kPasses) != h) continue;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const floatx16& a = acc[f][g];
-            uint2* to = reinterpret_cast<uint2*>(mine + r32 * C::kOutRow + ((kF32 ? 0 : 32 * f) + 8 * q + 4 * half) * kSize);
+            uint2* to = reinterpret_cast<uint2*>(mine + r32 * C::kOutRow + (32 * (f % (C::NW / kPasses)) + 8 * q + 4 * half) * kSize);
             if constexpr (kF32) {
               to[0] = make_uint2(__float_as_uint(a[4 * q]), __float_as_uint(a[4 * q + 1]));
               to[1] = make_uint2(__float_as_uint(a[4 * q + 2]), __float_as_uint(a[4 * q + 3]));
@@ -638,8 +680,9 @@ __global__ __launch_bounds__(512) void mx_gemm_wide_kernel(MxGemmParams P) {
         }
         const int have = min(max(cols - h * kWidth, 0), kWidth) * kSize;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // 8 lanes to a row of 128 bytes
-          const int r = 8 * i + lr, at = (lane & 7) * 16;
+        for (int i = 0; i < kWidth * kSize / 32; ++i) {  // a row's 16 bytes a lane
+          constexpr int kPer = kWidth * kSize / 16;
+          const int r = 64 / kPer * i + lane / kPer, at = lane % kPer * 16;
           const uint2* from = reinterpret_cast<const uint2*>(mine + r * C::kOutRow + at);
           const uint2 a = from[0], b = from[1];
           if (r < rows && at < have)
@@ -660,11 +703,12 @@ __global__ __launch_bounds__(512) void mx_gemm_wide_kernel(MxGemmParams P) {
       case 1: tile(std::integral_constant<int, 1>{}); break;
       case 2: tile(std::integral_constant<int, 2>{}); break;
       case 3: tile(std::integral_constant<int, 3>{}); break;
-      default: tile(std::integral_constant<int, 4>{}); break;
+      default: tile(std::integral_constant<int, C::MW>{}); break;
     }
     if (!more) break;
     lds_barrier();
-    load_codes(nxt, 1, 1, true);
+    load_codes(nxt, 1, 1, true, 0, 1);
+    if constexpr (C::kBytes) load_scales(nxt, 1, 1, true, 0, 1);
     src = nxt;
     it = ahead;
     item = next_item;
@@ -672,11 +716,12 @@ __global__ __launch_bounds__(512) void mx_gemm_wide_kernel(MxGemmParams P) {
   wait_loads<0>();  // no load may land in LDS after the workgroup's end
 }
 
+template <class C>
 static hipError_t run_gemm_wide(const MxGemmParams& p, hipStream_t s) {
   if (p.out_f32)
-    mx_gemm_wide_kernel<true><<<256, 512, 0, s>>>(p);
+    mx_gemm_wide_kernel<C, true><<<256, C::kWaves * 64, 0, s>>>(p);
   else
-    mx_gemm_wide_kernel<false><<<256, 512, 0, s>>>(p);
+    mx_gemm_wide_kernel<C, false><<<256, C::kWaves * 64, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -688,11 +733,25 @@ static hipError_t run_gemm(const MxGemmParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Which tile: the largest that the rows of an expert fill to some part and that gives the
+// chip enough workgroups (m: rows of an expert if all have alike). Measured at N = Kd =
+// 4096: 64 experts, m = 1: 128 x 32 tiles 101 us, 256 x 128 109, 256 x 256 133; m = 32:
+// 153, 126, 145; m = 192: 443, 265, 212. One expert, 1024 rows: 33, 23, 29, and 18
+// with 128 x 128; 64 rows: 10, 18, 18, and 8 with 64 x 32.
+template <bool kBytes>
+static hipError_t run_gemm_any(const MxGemmParams& p, hipStream_t s) {
+  const long experts = p.E < p.R ? p.E : p.R, m = (p.R + experts - 1) / experts;
+  auto items = [&](int bm, int bn) { return experts * ((m + bm - 1) / bm) * ((p.N + bn - 1) / bn); };
+  using Wide = MxWide<kBytes ? 3 : 4, kBytes>;
+  if (m > 112 && items(Wide::BM, Wide::BN) >= (kBytes ? 512 : 160)) return run_gemm_wide<Wide>(p, s);
+  if (m > 8 && items(128, 256) >= 128) return run_gemm<MxTile<2, 2, 4, 2, 2, kBytes>>(p, s);
+  if (m > 8 && items(128, 128) >= 128) return run_gemm<MxTile<2, 2, 2, 2, 2, kBytes>>(p, s);
+  if (items(32, 128) >= 256) return run_gemm<MxTile<1, 1, 4, 1, 3, kBytes>>(p, s);
+  return run_gemm<MxTile<1, 1, 2, 1, 4, kBytes>>(p, s);
+}
+
 hipError_t launch_mx_gemm(const MxGemmParams& p, hipStream_t s) {
-  const bool bytes = p.Kd % 128 != 0;
-  const long mean = (long)p.R / p.E;
-  if (mean <= 48) return bytes ? run_gemm<MxTile<1, 1, 4, 1, 3, true>>(p, s) : run_gemm<MxTile<1, 1, 4, 1, 3, false>>(p, s);
-  return bytes ? run_gemm<MxTile<4, 2, 2, 2, 2, true>>(p, s) : run_gemm_wide(p, s);
+  return p.Kd % 128 != 0 ? run_gemm_any<true>(p, s) : run_gemm_any<false>(p, s);
 }
 
 // ---------------------------------------------------------------- backward
@@ -740,30 +799,29 @@ __device__ __forceinline__ void mx_back_tile(const MxGemmParams& P, uint8_t* lds
   const uint32_t s_k = k0 / kMxBlock + lane % kSPer * (C::kBytes ? 1 : 4);
   const uint32_t y_piece = ((lane & 7) ^ yr >> 1) * 16;  // ^ 64 in odd loads
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(lds));
-  auto issue = [&](int st, int slot) {
+  // Part `part` of `parts` of this wave's loads of stage st.
+  auto issue = [&](int st, int slot, int part, int parts) {
     const uint32_t to = lds0 + slot * C::kStage;
     const uint32_t n0 = (uint32_t)st * C::kN;
 #pragma unroll
-    for (int i = 0; i < C::kLoadW; ++i) {
-      const int q = wave * C::kLoadW + i, row = kWRows * q + wr;
-      const uint32_t k = k0 / 2 + ((lane % kPer) ^ (C::KW > 1 ? (row >> 3 & 1) << 2 : 0)) * 16;
-      load_lds16(wq, n0 + row < (uint32_t)P.N && k < krow ? (n0 + row) * krow + k : kNoRow, to + q * 1024);
-    }
-#pragma unroll
-    for (int i = 0; i < C::kLoadS; ++i) {
-      const int q = wave * C::kLoadS + i;
-      const uint32_t n = n0 + kSRows * q + sr;
-      const uint32_t at = n < (uint32_t)P.N && s_k < srow ? n * srow + s_k : kNoRow;
-      if constexpr (C::kBytes)
-        load_lds1(ws, at, to + C::kW + q * 256);
-      else
-        load_lds4(ws, at, to + C::kW + q * 256);
-    }
-#pragma unroll
-    for (int i = 0; i < C::kLoadY; ++i) {
-      const int q = wave * C::kLoadY + i;
-      const uint32_t m = 8 * q + yr, yb = n0 * 2 + (y_piece ^ (q & 1) * 64);
-      load_lds16(dy, m < (uint32_t)it.rows && yb < yrow ? m * yrow + yb : kNoRow, to + C::kW + C::kS + q * 1024);
+    for (int l = C::kLoads * part / parts; l < C::kLoads * (part + 1) / parts; ++l) {
+      if (l < C::kLoadW) {
+        const int q = wave * C::kLoadW + l, row = kWRows * q + wr;
+        const uint32_t k = k0 / 2 + ((lane % kPer) ^ (C::KW > 1 ? (row >> 3 & 1) << 2 : 0)) * 16;
+        load_lds16(wq, n0 + row < (uint32_t)P.N && k < krow ? (n0 + row) * krow + k : kNoRow, to + q * 1024);
+      } else if (l < C::kLoadW + C::kLoadS) {
+        const int q = wave * C::kLoadS + l - C::kLoadW;
+        const uint32_t n = n0 + kSRows * q + sr;
+        const uint32_t at = n < (uint32_t)P.N && s_k < srow ? n * srow + s_k : kNoRow;
+        if constexpr (C::kBytes)
+          load_lds1(ws, at, to + C::kW + q * 256);
+        else
+          load_lds4(ws, at, to + C::kW + q * 256);
+      } else {
+        const int q = wave * C::kLoadY + l - C::kLoadW - C::kLoadS;
+        const uint32_t m = 8 * q + yr, yb = n0 * 2 + (y_piece ^ (q & 1) * 64);
+        load_lds16(dy, m < (uint32_t)it.rows && yb < yrow ? m * yrow + yb : kNoRow, to + C::kW + C::kS + q * 1024);
+      }
     }
   };
 
@@ -779,20 +837,20 @@ __device__ __forceinline__ void mx_back_tile(const MxGemmParams& P, uint8_t* lds
   const int w_at = half * 8 * C::kRow + ((wave * 64 + c * 2) ^ (C::KW > 1 ? half << 6 : 0));
   const int s_at = half * 8 * C::kScaleRow + (wave * 4 + (c >> 3)) * (C::kBytes ? 4 : 1);
   struct Raw {
-    uint16_t q[8];   // codes of columns 4c .. 4c + 3 of 8 rows
-    uint8_t s[8];    // their scales
+    uint32_t q[8];   // codes of columns 4c .. 4c + 3 of 8 rows
+    uint32_t s[8];   // their scales
     bf16x8_t x[G];
   };
-  auto read = [&](Raw& v, int slot, int j) {
+  // In 16 pieces: piece i < 8 reads row i, the others dy.
+  auto read = [&](Raw& v, int slot, int j, int piece) {
     const uint8_t* b = lds + slot * C::kStage;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v.q[i] = *reinterpret_cast<const uint16_t*>(b + (16 * j + i) * C::kRow + w_at);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v.s[i] = b[C::kW + (16 * j + i) * C::kScaleRow + s_at];
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-      v.x[g] = *reinterpret_cast<const bf16x8_t*>(b + C::kW + C::kS + (32 * g + c) * 128 +
-                                                  (((2 * j + half) ^ (lane >> 1 & 7)) * 16));
+    if (piece < 8) {
+      v.q[piece] = *reinterpret_cast<const uint16_t*>(b + (16 * j + piece) * C::kRow + w_at);
+      v.s[piece] = b[C::kW + (16 * j + piece) * C::kScaleRow + s_at];
+    } else if (piece - 8 < G) {
+      v.x[piece - 8] = *reinterpret_cast<const bf16x8_t*>(b + C::kW + C::kS + (32 * (piece - 8) + c) * 128 +
+                                                          (((2 * j + half) ^ (lane >> 1 & 7)) * 16));
+    }
   };
   // Conversion in 16 pieces: piece i < 8 converts row i, piece 8 + i makes two words of the fragments.
   struct Frags {
@@ -802,8 +860,8 @@ __device__ __forceinline__ void mx_back_tile(const MxGemmParams& P, uint8_t* lds
   auto convert = [&](const Raw& v, Frags& f, int piece) {
     if (piece < 8) {
       const float s = mx_scale(v.s[piece]);
-      f.lo[piece] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((uint32_t)v.q[piece], s, 0));
-      f.hi[piece] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((uint32_t)v.q[piece], s, 1));
+      f.lo[piece] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v.q[piece], s, 0));
+      f.hi[piece] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v.q[piece], s, 1));
     } else {
       const int p = piece - 8, pair = p & 3, h = p >> 2;
       const uint32_t a = h ? f.hi[2 * pair] : f.lo[2 * pair], b = h ? f.hi[2 * pair + 1] : f.lo[2 * pair + 1];
@@ -811,8 +869,9 @@ __device__ __forceinline__ void mx_back_tile(const MxGemmParams& P, uint8_t* lds
       f.w[2 * h + 1][pair] = __builtin_amdgcn_perm(b, a, 0x07060302u);
     }
   };
-  // The products of one step, and between them the conversion of the next.
-  auto step = [&](const Frags& f, const Raw& v, const Raw& next, Frags& nf) {
+  // The products of one step, and between them the conversion of the next, the reads
+  // of the one behind that, and, in one step of a stage, its loads.
+  auto step = [&](const Frags& f, const Raw& v, const Raw& next, Frags& nf, auto behind) {
     constexpr int kProducts = 4 * G;
 #pragma unroll
     for (int i = 0; i < kProducts; ++i) {
@@ -822,7 +881,10 @@ __device__ __forceinline__ void mx_back_tile(const MxGemmParams& P, uint8_t* lds
       acc[k][g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, v.x[g], acc[k][g], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int p = 16 * i / kProducts; p < 16 * (i + 1) / kProducts; ++p) convert(next, nf, p);
+      for (int p = 16 * i / kProducts; p < 16 * (i + 1) / kProducts; ++p) {
+        convert(next, nf, p);
+        behind(p);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -831,40 +893,37 @@ __device__ __forceinline__ void mx_back_tile(const MxGemmParams& P, uint8_t* lds
   // behind that also says that stage st + 1 has landed for every wave.
   const int stages = (P.N + C::kN - 1) / C::kN;
 #pragma unroll
-  for (int s = 0; s < C::S; ++s) issue(s, s);
+  for (int s = 0; s < C::S; ++s) issue(s, s, 0, 1);
   wait_loads<(C::S - 1) * C::kLoads>();
   lds_barrier();
   Raw r0, r1, r2, r3;
   Frags even, odd;
-  read(r0, 0, 0);
-  read(r1, 0, 1);
+#pragma unroll
+  for (int p = 0; p < 16; ++p) {
+    read(r0, 0, 0, p);
+    read(r1, 0, 1, p);
+  }
 #pragma unroll
   for (int p = 0; p < 16; ++p) convert(r0, even, p);
   int slot = 0;
   for (int st = 0; st < stages; ++st) {
     const int next = slot == C::S - 1 ? 0 : slot + 1;
-    read(r2, slot, 2);
-    __builtin_amdgcn_sched_barrier(0);
-    step(even, r0, r1, odd);
-    read(r3, slot, 3);
-    __builtin_amdgcn_sched_barrier(0);
-    step(odd, r1, r2, even);
+    step(even, r0, r1, odd, [&](int p) { read(r2, slot, 2, p); });
+    step(odd, r1, r2, even, [&](int p) { read(r3, slot, 3, p); });
     wait_loads<(C::S - 2) * C::kLoads>();
     lds_barrier();
-    read(r0, next, 0);
-    issue(st + C::S, slot);
-    __builtin_amdgcn_sched_barrier(0);
-    step(even, r2, r3, odd);
-    read(r1, next, 1);
-    __builtin_amdgcn_sched_barrier(0);
-    step(odd, r3, r0, even);
+    step(even, r2, r3, odd, [&](int p) {
+      read(r0, next, 0, p);
+      issue(st + C::S, slot, p, 16);
+    });
+    step(odd, r3, r0, even, [&](int p) { read(r1, next, 1, p); });
     slot = next;
   }
   wait_loads<0>();
 #pragma unroll
   for (int f = 0; f < 4; ++f)
 #pragma unroll
-    for (int g = 0; g < G; ++g) asm volatile("" : "+v"(acc[f][g]));  // no product moves into the branches below
+    for (int g = 0; g < G; ++g) asm volatile("" : "+a"(acc[f][g]));  // no product moves into the branches below
 
   // acc[f][g][i] is column 4 (8 (i / 4) + 4 half + i % 4) + f of the wave's 128, row 32 g + c.
 #pragma unroll
@@ -907,12 +966,22 @@ static hipError_t run_gemm_backward(const MxGemmParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Which tile, as for the forward product. Measured at N = Kd = 4096: 64 experts, m = 1:
+// 32 x 512 tiles 104 us, 128 x 512 122; m = 48: 218, 169; m = 192: 584, 436. One expert,
+// 1024 rows: 61, 84, and 58 with 32 x 128; 4096 rows: 183, 107, 228. Eight experts of 256 rows,
+// N = Kd = 2048: 47, 48, 61, and 37 with 64 x 256.
+template <bool kBytes>
+static hipError_t run_gemm_backward_any(const MxGemmParams& p, hipStream_t s) {
+  const long experts = p.E < p.R ? p.E : p.R, m = (p.R + experts - 1) / experts;
+  auto items = [&](int bm, int bk) { return experts * ((m + bm - 1) / bm) * ((p.Kd + bk - 1) / bk); };
+  if (m > 24 && items(128, 512) >= 200) return run_gemm_backward<MxBackTile<4, 4, 4, kBytes>>(p, s);
+  if (m > 24 && items(64, 256) >= 256) return run_gemm_backward<MxBackTile<2, 2, 4, kBytes>>(p, s);
+  if (items(32, 512) >= 256) return run_gemm_backward<MxBackTile<1, 4, 3, kBytes>>(p, s);
+  return run_gemm_backward<MxBackTile<1, 1, 4, kBytes>>(p, s);
+}
+
 hipError_t launch_mx_gemm_backward(const MxGemmParams& p, hipStream_t s) {
-  const bool bytes = p.Kd % 128 != 0;
-  const long mean = (long)p.R / p.E;
-  if (mean <= 48)
-    return bytes ? run_gemm_backward<MxBackTile<1, 4, 3, true>>(p, s) : run_gemm_backward<MxBackTile<1, 4, 3, false>>(p, s);
-  return bytes ? run_gemm_backward<MxBackTile<4, 4, 3, true>>(p, s) : run_gemm_backward<MxBackTile<4, 4, 4, false>>(p, s);
+  return p.Kd % 128 != 0 ? run_gemm_backward_any<true>(p, s) : run_gemm_backward_any<false>(p, s);
 }
 
 }  // namespace pmoe

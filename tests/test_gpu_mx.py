@@ -186,7 +186,16 @@ PRODUCTS = [  # E, R, spare, N, Kd, offsets
     (2, 513, 0, 1040, 512, "cuts"), (1024, 1200, 7, 32, 64, "cuts"), (4, 900, 40, 128, 1184, "gaps")]
 
 
-@pytest.mark.parametrize("E,R,spare,N,Kd,kind", PRODUCTS)
+# shapes that reach every tile of the products, forward and back, with rows of scales that are whole dwords and not
+TILES = [(40, 5300, 11, 1040, 640, "cuts"), (40, 5300, 0, 1040, 256, "gaps"), (64, 8100, 9, 2064, 544, "cuts"),
+         (64, 8100, 0, 2064, 96, "gaps"), (16, 800, 5, 4112, 256, "cuts"), (16, 800, 5, 4112, 224, "gaps"),
+         (8, 1000, 3, 2064, 512, "cuts"), (8, 1000, 3, 2064, 480, "one"), (100, 300, 0, 528, 256, "cuts"),
+         (100, 300, 0, 528, 288, "gaps"), (3, 5, 0, 208, 1152, "cuts"), (3, 5, 0, 208, 1120, "cuts"),
+         (24, 2000, 7, 96, 4608, "cuts"), (24, 2000, 0, 112, 4640, "gaps"), (40, 400, 5, 80, 3584, "cuts"),
+         (40, 400, 0, 64, 3616, "cuts"), (16, 1200, 20, 144, 2176, "cuts"), (16, 1200, 0, 144, 2080, "cuts")]
+
+
+@pytest.mark.parametrize("E,R,spare,N,Kd,kind", PRODUCTS + TILES)
 def test_product_exact(pm, E, R, spare, N, Kd, kind):
     """Sums that FP32 holds exactly: every output is checked to the bit, in both types."""
     import torch
@@ -206,7 +215,8 @@ def test_product_exact(pm, E, R, spare, N, Kd, kind):
 
 
 @pytest.mark.parametrize("T,K,E,N,Kd,offset", [(16, 6, 64, 512, 1024, 0), (300, 4, 8, 176, 544, 8), (1, 1, 1, 16, 96, 0),
-                                               (513, 2, 5, 272, 256, 0)])
+                                               (513, 2, 5, 272, 256, 0), (1500, 4, 40, 1040, 640, 0),
+                                               (1700, 5, 64, 2064, 288, 64), (3000, 3, 64, 2064, 544, 0)])
 def test_product_gathers_tokens(pm, T, K, E, N, Kd, offset):
     import torch
     rng = np.random.default_rng(T + E)
@@ -313,7 +323,7 @@ def test_product_with_offsets_that_are_none(pm):
         assert (buf[:20] == 9).all() and (buf[20 + R:] == 9).all()
 
 
-@pytest.mark.parametrize("E,R,spare,N,Kd,kind", PRODUCTS)
+@pytest.mark.parametrize("E,R,spare,N,Kd,kind", PRODUCTS + TILES)
 def test_product_gradient_exact(pm, E, R, spare, N, Kd, kind):
     """dy of small whole numbers: sums that FP32 holds exactly, rounded to BF16 once."""
     import torch
