@@ -1231,8 +1231,13 @@ PMOE_EXPORT int pmoe_permute_tokens(const void* topk_ids, int ids_type, int T, i
   b.row_of_route = row_of_route;
   b.route_of_row = route_of_row;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  PMOE_HIP(launch_route(topk_ids, ids_type == PMOE_IDS_INT64, T * K, E, expert_offset, b, s));
-  if (copy) PMOE_HIP(launch_permute(x, row_of_route, T, K, row_bytes, rows, s));
+  const bool ids64 = ids_type == PMOE_IDS_INT64;
+  if (copy && route_copy_fits(T, K, row_bytes)) {
+    PMOE_HIP(launch_route_copy(topk_ids, ids64, T, K, E, expert_offset, b, x, row_bytes, rows, s));
+  } else {
+    PMOE_HIP(launch_route(topk_ids, ids64, T * K, E, expert_offset, b, s));
+    if (copy) PMOE_HIP(launch_permute(x, row_of_route, T, K, row_bytes, rows, s));
+  }
   return ok();
 }
 

@@ -175,7 +175,12 @@ hipError_t launch_adapter_forward(const AdapterParams& p, hipStream_t s);
 hipError_t launch_adapter_backward(const AdapterParams& p, hipStream_t s);
 
 // ---------------------------------------------------------------- permutation of tokens
-// rows[row(t, j)] = x[t], rows and x of row_bytes (a multiple of 16), and its gradient.
+// The routing (without M-tiles and counters) and the copy rows[row(t, j)] = x[t] in one
+// launch, where route_copy_fits; same results as launch_route + launch_permute.
+bool route_copy_fits(int T, int K, long row_bytes);
+hipError_t launch_route_copy(const void* ids, bool ids64, int T, int K, int E, int expert_offset,
+                             const RouteBuffers& b, const void* x, long row_bytes, void* rows, hipStream_t s);
+// The copy alone, rows and x of row_bytes (a multiple of 16), and its gradient.
 hipError_t launch_permute(const void* x, const int* row_of_route, int T, int K, long row_bytes, void* rows,
                           hipStream_t s);
 hipError_t launch_permute_backward(const void* d_rows, bool f32, const int* row_of_route, int T, int K, int R, int H,

@@ -21,6 +21,8 @@
 //                   writes row_of_route and route_of_row.
 // A route is valid iff expert_offset <= id < expert_offset + E; other ids
 // (the -1 fill of unused slots, other ranks' experts) are skipped.
+#include <algorithm>
+
 #include "rowquant.h"
 
 namespace pmoe {
@@ -128,14 +130,16 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(int* __restrict__ bloc
   const int e = threadIdx.x;
   int total = 0;
   if (e < E) {
-    // exclusive prefix over blocks, in place; eight independent loads per
-    // round so the latency is paid once per eight blocks, not once per block
-    for (int b0 = 0; b0 < NB; b0 += 8) {
-      int c[8];
+    // exclusive prefix over blocks, in place; 32 independent loads per
+    // round so the latency is paid once per 32 blocks, not once per block
+    // (128 blocks of 256 experts: 12.0 us with 8 at a time, 8.6 with 32)
+    constexpr int kLoads = 32;
+    for (int b0 = 0; b0 < NB; b0 += kLoads) {
+      int c[kLoads];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = b0 + i < NB ? block_counts[(long)(b0 + i) * E + e] : 0;
+      for (int i = 0; i < kLoads; ++i) c[i] = b0 + i < NB ? block_counts[(long)(b0 + i) * E + e] : 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kLoads; ++i) {
         if (b0 + i < NB) block_counts[(long)(b0 + i) * E + e] = total;
         total += c[i];
       }
@@ -198,6 +202,7 @@ __global__ __launch_bounds__(256) void route_scatter_kernel(
 // path.
 constexpr int kRouteSmall = 8192;
 constexpr int kRouteSmallPer = kRouteSmall / 1024;
+constexpr long kRouteCopyBytes = 32L << 20;  // of rows, for one launch: 16 waves a CU, fewer than a long copy wants
 
 // LDS of the one-workgroup routing.
 struct RouteSmallLds {
@@ -206,14 +211,17 @@ struct RouteSmallLds {
   int sh[1024];
 };
 
-// The routing body; the caller is a workgroup of 1024 threads.
-template <typename IdT>
+// The routing body; the caller is a workgroup of 1024 threads. Where several
+// workgroups run it on the same routes (kCopy), `write` says which one stores the
+// results, and row_of_route[] is also left in LDS for each.
+template <typename IdT, bool kCopy = false>
 __device__ __forceinline__ void route_small_body(const IdT* __restrict__ ids, int TK, int E,
                                                  int offset, int nbits,
                                                  int* __restrict__ expert_offsets,
                                                  int* __restrict__ tiles, int* __restrict__ counters,
                                                  int* __restrict__ row_of_route,
-                                                 int* __restrict__ route_of_row, RouteSmallLds& lds) {
+                                                 int* __restrict__ route_of_row, RouteSmallLds& lds,
+                                                 bool write = true, int* row_lds = nullptr) {
   int* base = lds.base;
   int(*wcnt)[kMaxExperts] = lds.wcnt;
   int* sh = lds.sh;
@@ -269,29 +277,34 @@ __device__ __forceinline__ void route_small_body(const IdT* __restrict__ ids, in
   const int tstart = tincl - ntiles;
   const int T_tiles = sh[1023];
   if (tid < E) {
-    expert_offsets[tid] = start;
     base[tid] = start;
-    for (int i = 0; i < ntiles; ++i)
-      reinterpret_cast<int4*>(tiles)[tstart + i] = make_int4(tid, start, tstart, total);
+    if (write) expert_offsets[tid] = start;
+    if constexpr (!kCopy) {
+      for (int i = 0; i < ntiles; ++i)
+        reinterpret_cast<int4*>(tiles)[tstart + i] = make_int4(tid, start, tstart, total);
+    }
   }
-  if (tid == 0) {
-    expert_offsets[E] = R;
-    counters[0] = R;
-    counters[1] = T_tiles;
+  if (tid == 0 && write) expert_offsets[E] = R;
+  if constexpr (!kCopy) {
+    if (tid == 0) {
+      counters[0] = R;
+      counters[1] = T_tiles;
+    }
+    write_split(tid < E, tstart, ntiles, start, total, T_tiles, tid == 0, counters);
   }
-  write_split(tid < E, tstart, ntiles, start, total, T_tiles, tid == 0, counters);
   __syncthreads();
 #pragma unroll
   for (int c = 0; c < kRouteSmallPer; ++c) {
     if (c >= seg) break;  // uniform
     const int f = f0 + 64 * c;
     const int e = ev[c];
-    if (e >= 0) {
-      const int row = base[e] + mine[e] + before[c] + rank[c];
-      row_of_route[f] = row;
-      route_of_row[row] = f;
-    } else if (f < TK) {
-      row_of_route[f] = -1;
+    const int row = e >= 0 ? base[e] + mine[e] + before[c] + rank[c] : -1;
+    if (f < TK) {
+      if constexpr (kCopy) row_lds[f] = row;
+      if (write) {
+        row_of_route[f] = row;
+        if (row >= 0) route_of_row[row] = f;
+      }
     }
   }
 }
@@ -331,6 +344,34 @@ __global__ __launch_bounds__(1024) void route_quantize_kernel(
                                     x_scale, reinterpret_cast<float*>(lds.sh) + 4 * grp);
 }
 
+// The routing and the copy of each token to its rows in one launch: every
+// workgroup routes for itself (as route_small_kernel, a few microseconds that the copy
+// would wait for in any case) and copies its share of the tokens, a wave 1 KB
+// of one token at a time. 61 tokens of 8 KB to 366 rows: a call takes
+// 8.4 to 9.6 us, 12.0 in two launches.
+template <typename IdT>
+__global__ __launch_bounds__(1024) void route_copy_kernel(const IdT* __restrict__ ids, int T, int K, int E, int offset,
+                                                          int nbits, int* __restrict__ expert_offsets,
+                                                          int* __restrict__ row_of_route,
+                                                          int* __restrict__ route_of_row, const uint4* __restrict__ x,
+                                                          int P, uint4* __restrict__ rows) {
+  __shared__ RouteSmallLds lds;
+  __shared__ int row_lds[kRouteSmall];
+  route_small_body<IdT, true>(ids, T * K, E, offset, nbits, expert_offsets, nullptr, nullptr, row_of_route,
+                              route_of_row, lds, blockIdx.x == 0, row_lds);
+  __syncthreads();
+  const int lane = threadIdx.x & 63, chunks = (P + 63) / 64;
+  for (int w = blockIdx.x * 16 + (threadIdx.x >> 6); w < T * chunks; w += gridDim.x * 16) {
+    const int t = w / chunks, p = (w - t * chunks) * 64 + lane;
+    if (p >= P) continue;
+    const uint4 v = x[(long)t * P + p];
+    for (int j = 0; j < K; ++j) {
+      const int r = row_lds[t * K + j];
+      if (r >= 0) rows[(long)r * P + p] = v;
+    }
+  }
+}
+
 static int expert_bits(int E) {
   int nbits = 0;
   while ((1 << nbits) < E) ++nbits;
@@ -366,6 +407,27 @@ hipError_t launch_route_quantize(const void* ids, bool ids64, int TK, int E, int
   else
     launch_route_quantize_t(static_cast<const int*>(ids), TK, E, expert_offset, b, x, T, H, Hq,
                             static_a, xq, x_sf, x_scale, s);
+  return hipGetLastError();
+}
+
+bool route_copy_fits(int T, int K, long row_bytes) {
+  return (long)T * K <= kRouteSmall && (long)T * K * row_bytes <= kRouteCopyBytes;
+}
+
+hipError_t launch_route_copy(const void* ids, bool ids64, int T, int K, int E, int expert_offset,
+                             const RouteBuffers& b, const void* x, long row_bytes, void* rows, hipStream_t s) {
+  const int P = (int)(row_bytes / 16);
+  const long waves = (long)T * ((P + 63) / 64);
+  const int grid = (int)std::max<long>(1, std::min<long>(256, (waves + 15) / 16));
+  const auto* xv = static_cast<const uint4*>(x);
+  auto* rv = static_cast<uint4*>(rows);
+  if (ids64)
+    route_copy_kernel<long long><<<grid, 1024, 0, s>>>(static_cast<const long long*>(ids), T, K, E, expert_offset,
+                                                       expert_bits(E), b.expert_offsets, b.row_of_route,
+                                                       b.route_of_row, xv, P, rv);
+  else
+    route_copy_kernel<int><<<grid, 1024, 0, s>>>(static_cast<const int*>(ids), T, K, E, expert_offset, expert_bits(E),
+                                                 b.expert_offsets, b.row_of_route, b.route_of_row, xv, P, rv);
   return hipGetLastError();
 }
 
