@@ -611,8 +611,8 @@ size_t pmoe_permute_workspace_bytes(int T, int K, int E);
  *   row_of_route   : int32 [T*K] out, -1 where the route has no row
  *   route_of_row   : int32 [T*K] out, the valid rows; behind them left as it was
  *   expert_offsets : int32 [E+1] out, first row of each expert; [E] = valid rows
- * T = 0 writes zeros to expert_offsets. 1 <= E <= 1024, 1 <= K <= min(32, E),
- * T*K < 2^30, row_bytes a positive multiple of 16, at most 2^20. Outputs and ws share no
+ * T = 0 writes zeros to expert_offsets. 1 <= E <= 1024, 1 <= K <= 32 (K > E where this
+ * is a share of few experts), T*K < 2^30, row_bytes a positive multiple of 16, at most 2^20. Outputs and ws share no
  * memory with each other or with an input. Alignment: x and rows 16 bytes, ws
  * 256, int64 ids 8, others 4.
  */

@@ -42,14 +42,14 @@ def quantize(x, fmt="e2m1"):
     code = np.where(good[:, None], code, 0).astype(np.uint8).reshape(x.shape)
     if fmt == "e2m1":
         code = code[..., 0::2] | (code[..., 1::2] << 4)
-    return code, np.where(good, byte, 255).astype(np.uint8).reshape(*x.shape[:-1], -1)
+    return code, np.where(good, byte, 255).astype(np.uint8).reshape(*x.shape[:-1], x.shape[-1] // BLOCK)
 
 
 def dequantize(codes, scales, fmt="e2m1"):
     """The float64 values that codes and scales stand for."""
     codes, scales = np.asarray(codes), np.asarray(scales)
     if fmt == "e2m1":
-        c = np.stack([codes & 15, codes >> 4], -1).reshape(*codes.shape[:-1], -1)
+        c = np.stack([codes & 15, codes >> 4], -1).reshape(*codes.shape[:-1], 2 * codes.shape[-1])
         v = E2M1[c & 7] * np.where(c & 8, -1.0, 1.0)
     else:
         c = codes

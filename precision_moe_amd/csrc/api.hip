@@ -1148,7 +1148,7 @@ namespace {
 int check_permute_shape(int T, int K, int E) {
   if (T < 0) return fail(PMOE_ERR_SHAPE, "T must be >= 0");
   if (E < 1 || E > kMaxExperts) return fail(PMOE_ERR_SHAPE, "E must be in [1, 1024]");
-  if (K < 1 || K > 32 || K > E) return fail(PMOE_ERR_SHAPE, "K must be in [1, min(32, E)]");
+  if (K < 1 || K > 32) return fail(PMOE_ERR_SHAPE, "K must be in [1, 32]");
   if ((long long)T * K >= (1LL << 31) / 2) return fail(PMOE_ERR_SHAPE, "T*K too large");
   return PMOE_OK;
 }

@@ -17,7 +17,7 @@ def _permute(T=4, K=2, E=8, ids_type=0, x=None, row_bytes=16, rows=None):
     return _rc("pmoe_permute_tokens", None, ids_type, T, K, E, 0, x, row_bytes, rows, None, None, None, None, 0, None)
 
 
-@pytest.mark.parametrize("kw", [dict(T=-1), dict(E=0), dict(E=1025), dict(K=0), dict(K=9), dict(E=64, K=33),
+@pytest.mark.parametrize("kw", [dict(T=-1), dict(E=0), dict(E=1025), dict(K=0), dict(K=33), dict(E=64, K=33),
                                 dict(T=1 << 29, K=2), dict(x=16, rows=16, row_bytes=0),
                                 dict(x=16, rows=16, row_bytes=24), dict(x=16, rows=16, row_bytes=(1 << 20) + 16)])
 def test_permute_shapes(kw):
@@ -31,8 +31,8 @@ def test_permute_arguments():
     assert _permute(ids_type=2) == ARG
     assert _permute(x=16) == ARG and _permute(rows=16) == ARG          # both or neither
     with pytest.raises(pm.PmoeError):
-        pm.permute_workspace_bytes(4, 9, 8)
-    assert pm.permute_workspace_bytes(0, 2, 8) > 0
+        pm.permute_workspace_bytes(4, 33, 8)
+    assert pm.permute_workspace_bytes(0, 2, 8) > 0 and pm.permute_workspace_bytes(4, 9, 8) > 0
 
     def back(type=0, T=4, K=2, R=8, H=64):
         return _rc("pmoe_permute_tokens_backward", None, type, None, T, K, R, H, None, None)
