@@ -807,7 +807,14 @@ def _type(dtype, name):
     raise TypeError(f"{name} must be bfloat16 or float32")
 
 
+def _c_ints(*values):
+    """Refuses what the C interface's int would cut."""
+    if max(values) > 0x7FFFFFFF or min(values) < -0x80000000:
+        raise ValueError(f"sizes and offsets must fit 32 bits: {values}")
+
+
 def permute_workspace_bytes(T, K, E):
+    _c_ints(T, K, E)
     size = lib().pmoe_permute_workspace_bytes(T, K, E)
     if size == 0:
         raise PmoeError(3, lib().pmoe_last_error().decode())
@@ -827,6 +834,8 @@ def permute_tokens(x, topk_ids, E, expert_offset=0, out=None, workspace=None, st
     if topk_ids.dim() != 2 or (x is not None and (x.dim() != 2 or x.shape[0] != topk_ids.shape[0])):
         raise ValueError("topk_ids must be [T, K] and x [T, H]")
     T, K = topk_ids.shape
+    row_bytes = 0 if x is None else x.shape[1] * x.element_size()
+    _c_ints(T, K, E, expert_offset, row_bytes)
     ids, ids_type = _ids(topk_ids, "topk_ids")
     rows, row, route, offsets = out if out is not None else (None,) * 4
     if x is not None:
@@ -840,7 +849,7 @@ def permute_tokens(x, topk_ids, E, expert_offset=0, out=None, workspace=None, st
                          _out(offsets, "expert_offsets", i32, (E + 1,), ids))
     ws = _scratch(lib().pmoe_permute_workspace_bytes(T, K, E), workspace, ids)
     _check(lib().pmoe_permute_tokens(
-        _ptr(ids), ids_type, T, K, E, expert_offset, _ptr(x), 0 if x is None else x.shape[1] * x.element_size(),
+        _ptr(ids), ids_type, T, K, E, expert_offset, _ptr(x), row_bytes,
         *(_ptr(t) for t in res), _ptr(ws), ws.numel(), _stream(stream, ids, x, ws, *res)))
     return res
 
@@ -854,6 +863,7 @@ def permute_tokens_backward(d_rows, row_of_route, K, out=None, stream=None):
         raise ValueError("d_rows must be [R, H] and row_of_route [T*K]")
     R, H = d_rows.shape
     T = row_of_route.numel() // K
+    _c_ints(T, K, R, H)
     kind = _type(d_rows.dtype, "d_rows")
     d_rows = d_rows.contiguous()
     row = _is(row_of_route.reshape(-1), "row_of_route", torch.int32, (T * K,))
@@ -886,6 +896,7 @@ def mx_quantize(x, format="e2m1", out=None, stream=None):
     fmt, kind = _mx_format(format), _type(x.dtype, "x")
     if x.dim() < 1 or x.shape[-1] % 32:
         raise ValueError("the last dimension of x must be a multiple of 32")
+    _c_ints(x.shape[-1])
     x = x.contiguous()
     *lead, n = x.shape
     codes, scales = out if out is not None else (None, None)
@@ -906,6 +917,7 @@ def mx_dequantize(codes, scales, format="e2m1", dtype=None, out=None, stream=Non
     if codes.dim() < 1:
         raise ValueError("codes must be [..., n/2] (E4M3: [..., n])")
     n = codes.shape[-1] * (2 if fmt == MX_E2M1 else 1)
+    _c_ints(n)
     shape = (*codes.shape[:-1], n)
     codes, scales = _mx_pair(codes, scales, "the input", shape, fmt)
     out = _out(out, "out", dtype, shape, codes)
@@ -942,6 +954,7 @@ def mx_grouped_gemm(a, a_sf, w, w_sf, expert_offsets, route_of_row=None, topk=1,
     else:
         route = _is(route_of_row, "route_of_row", torch.int32, (route_of_row.numel(),))
         R = route.shape[0]
+    _c_ints(a.shape[0], topk, R, E, N, Kd)
     dtype = (out.dtype if out is not None else torch.bfloat16) if dtype is None else dtype
     kind = _type(dtype, "out")
     out = _out(out, "out", dtype, (R, N), a)
@@ -960,6 +973,7 @@ def mx_grouped_gemm_backward(dy, w, w_sf, expert_offsets, out=None, stream=None)
     if dy.dim() != 2:
         raise ValueError("dy must be [R, N]")
     R = dy.shape[0]
+    _c_ints(R, E, N, Kd)
     dy = _bf16(dy, "dy", (R, N))
     out = _out(out, "out", torch.bfloat16, (R, Kd), dy)
     _check(lib().pmoe_mx_grouped_gemm_backward(_ptr(dy), _ptr(offsets), R, E, _ptr(w), _ptr(w_sf), N, Kd, _ptr(out),
@@ -984,10 +998,13 @@ def mx_activation(y, act, swiglu_limit=0.0, checkpoint=False, row_count=None, ou
     R, W = y.shape
     if act == ACT_SWIGLU and W % 2:
         raise ValueError("SwiGLU needs y [R, 2I]")
+    _c_ints(R, W)
     I = W // 2 if act == ACT_SWIGLU else W
     y = _bf16(y, "y", (R, W))
     count = _row_count(row_count)
     hq, h_sf, y8, y8_sf = out if out is not None else (None,) * 4
+    if not checkpoint and (y8 is not None or y8_sf is not None):
+        raise ValueError("y8 and y8_sf need checkpoint")
     u8 = torch.uint8
     hq, h_sf = _out(hq, "hq", u8, (R, I // 2), y), _out(h_sf, "h_sf", u8, (R, I // 32), y)
     y8 = _out(y8, "y8", u8, (R, W), y) if checkpoint else None
@@ -1005,6 +1022,7 @@ def mx_activation_backward(dh, y8, y8_sf, act, swiglu_limit=0.0, row_count=None,
         raise ValueError("dh must be [R, I]")
     R, I = dh.shape
     W = 2 * I if act == ACT_SWIGLU else I
+    _c_ints(R, W)
     dh = _bf16(dh, "dh", (R, I))
     y8, y8_sf = _mx_pair(y8, y8_sf, "the checkpoint", (R, W), MX_E4M3)
     count = _row_count(row_count)

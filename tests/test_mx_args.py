@@ -131,3 +131,27 @@ def test_binding_dtypes_and_shapes():
                       ((dy, y8, y8_sf[:, :1], 1), ValueError), ((dy, y8, y8_sf, 0), ValueError)):
         with pytest.raises(err):
             pm.mx_activation_backward(*args)
+
+
+def test_binding_refuses_what_an_int_would_cut():
+    """Sizes past 32 bits, on tensors without memory: they reach the C interface as 32-bit ints."""
+    def meta(*shape, dtype=BF):
+        return torch.empty(shape, dtype=dtype, device="meta")
+    big, ids, row = 2 ** 32 + 32, torch.zeros(4, 2, dtype=I32), torch.zeros(8, dtype=I32)
+    w, w_sf, off = meta(1, 32, 32, dtype=U8), meta(1, 32, 2, dtype=U8), torch.zeros(2, dtype=I32)
+    for call in (lambda: pm.permute_tokens(meta(4, big), ids, 8), lambda: pm.permute_tokens(None, ids, 8, expert_offset=2 ** 32),
+                 lambda: pm.permute_tokens(None, ids, 2 ** 32 + 8), lambda: pm.permute_tokens(None, meta(big, 1, dtype=I32), 8),
+                 lambda: pm.permute_workspace_bytes(big, 1, 8), lambda: pm.permute_tokens_backward(meta(8, big), row, 2),
+                 lambda: pm.permute_tokens_backward(meta(big, 8), row, 2), lambda: pm.mx_quantize(meta(big)),
+                 lambda: pm.mx_quantize(meta(2, big), format="e4m3"),
+                 lambda: pm.mx_dequantize(meta(big // 2, dtype=U8), meta(big // 32, dtype=U8)),
+                 lambda: pm.mx_grouped_gemm(meta(big, 32, dtype=U8), meta(big, 2, dtype=U8), w, w_sf, off),
+                 lambda: pm.mx_grouped_gemm(meta(8, 32, dtype=U8), meta(8, 2, dtype=U8), w, w_sf, off, route_of_row=row, topk=big),
+                 lambda: pm.mx_grouped_gemm_backward(meta(big, 32), w, w_sf, off), lambda: pm.mx_activation(meta(big, 64), 1),
+                 lambda: pm.mx_activation_backward(meta(big, 32), None, None, 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+    y8, y8_sf = torch.zeros(4, 64, dtype=U8), torch.zeros(4, 2, dtype=U8)
+    for out in ((None, None, y8, None), (None, None, y8, y8_sf)):      # a checkpoint that would not be written
+        with pytest.raises(ValueError, match="need checkpoint"):
+            pm.mx_activation(torch.zeros(4, 64, dtype=BF), 1, out=out)
