@@ -192,7 +192,8 @@ TILES = [(40, 5300, 11, 1040, 640, "cuts"), (40, 5300, 0, 1040, 256, "gaps"), (6
          (8, 1000, 3, 2064, 512, "cuts"), (8, 1000, 3, 2064, 480, "one"), (100, 300, 0, 528, 256, "cuts"),
          (100, 300, 0, 528, 288, "gaps"), (3, 5, 0, 208, 1152, "cuts"), (3, 5, 0, 208, 1120, "cuts"),
          (24, 2000, 7, 96, 4608, "cuts"), (24, 2000, 0, 112, 4640, "gaps"), (40, 400, 5, 80, 3584, "cuts"),
-         (40, 400, 0, 64, 3616, "cuts"), (16, 1200, 20, 144, 2176, "cuts"), (16, 1200, 0, 144, 2080, "cuts")]
+         (40, 400, 0, 64, 3616, "cuts"), (16, 1200, 20, 144, 2176, "cuts"), (16, 1200, 0, 144, 2080, "cuts"),
+         (32, 4400, 10, 1552, 160, "cuts"), (8, 2048, 0, 4112, 1056, "gaps"), (32, 6144, 0, 1552, 96, "cuts")]
 
 
 @pytest.mark.parametrize("E,R,spare,N,Kd,kind", PRODUCTS + TILES)
