@@ -35,19 +35,24 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p);
 }
 // Lane l's 16 bytes at `offset` go to lds + 16 l (4 bytes to lds + 4 l; one byte, extended
-// with zeros to 4, to lds + 4 l). The loads are counted by vmcnt, in order.
+// with zeros to 4, to lds + 4 l). The loads are counted by vmcnt, in order. Each names M0 as
+// overwritten, so that no M0 of the compiler's own is merged across it (the compiler allocates
+// nothing there and warns that such a register is not saved, which nothing asks for).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_lds16(intx4 buf, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(buf)
-               : "memory");
+               : "m0", "memory");
 }
 __device__ __forceinline__ void load_lds4(intx4 buf, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(buf)
-               : "memory");
+               : "m0", "memory");
 }
 __device__ __forceinline__ void load_lds1(intx4 buf, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(buf)
-               : "memory");
+               : "m0", "memory");
 }
+#pragma clang diagnostic pop
 template <int kLeft>
 __device__ __forceinline__ void wait_loads() {  // until at most kLeft of the wave's loads are under way
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLeft) : "memory");
