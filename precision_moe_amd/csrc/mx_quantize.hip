@@ -112,12 +112,13 @@ __device__ __forceinline__ float clamp_up(float u, float L) {
   return L > 0.0f ? (u > L ? L : (u < -L ? -L : u)) : u;
 }
 
+constexpr float kHi = 0x1.715476p+0f, kLo = 0x1.4ae0c0p-26f;  // log2(e) = kHi + kLo
+
 // exp(-g) in FP32 within 3 units in the last place for -87 <= g <= 100 (above: that of
 // 100, which vanishes beside 1): the product with log2(e) is carried in two parts, as
 // its rounding alone would cost |g| units.
 __device__ __forceinline__ float exp_neg(float g) {
   g = g > 100.0f ? 100.0f : g;
-  constexpr float kHi = 0x1.715476p+0f, kLo = 0x1.4ae0c0p-26f;  // log2(e) = kHi + kLo
   const float t = -g * kHi;
   const float r = __builtin_fmaf(-g, kHi, -t) - g * kLo;
   const float e = __builtin_amdgcn_exp2f(t);
@@ -251,6 +252,19 @@ __global__ __launch_bounds__(256) void mx_activation_kernel(const uint16_t* __re
   }
 }
 
+// Both gradients of SwiGLU at a gate below kLowGate, where s = exp(gate) = m 2^n, 1/2 <= m <= 1, beside
+// 1: s alone is below FP32's normal numbers, its product with d h and up need not be, so the power of two
+// is applied to that. What a subnormal loses then is at most 2^-150, times a gate of at most 1000, below
+// half of BF16's smallest step (2^-134). Below -1000 both gradients are 0 whatever the other factors are.
+constexpr float kLowGate = -87.0f;
+__device__ __forceinline__ void swiglu_grad_low(float d, float g, float u, float& dg, float& du) {
+  g = g < -1000.0f ? -1000.0f : g;
+  const float n = __builtin_ceilf(g * kHi);
+  const float m = __builtin_amdgcn_exp2f(__builtin_fmaf(g, kHi, -n) + g * kLo);
+  dg = __builtin_amdgcn_ldexpf(d * u * m, (int)n) * (1.0f + g);
+  du = __builtin_amdgcn_ldexpf(d * m, (int)n) * g;
+}
+
 // Backward from the checkpoint: with y the values that it stands for,
 //   squared ReLU  d y = 2 max(y, 0) d h
 //   SwiGLU        d gate = d h * up * s (1 + gate (1 - s)),  d up = d h * gate * s,  s = 1 / (1 + exp(-gate)),
@@ -271,15 +285,28 @@ __global__ __launch_bounds__(256) void mx_activation_backward_kernel(
     if constexpr (kSwiglu) {
       const long ga = r * 2 * per + c, ua = ga + per;
       float u[8], dg[8], du[8];
+      bool low = false;
       mx_values8(codes[ga], y8_sf[ga >> 2], g);
       mx_values8(codes[ua], y8_sf[ua >> 2], u);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float gc = clamp_gate(g[k], L), uc = clamp_up(u[k], L);
-        const float s = gc < -87.0f ? 0.0f : __builtin_amdgcn_rcpf(1.0f + exp_neg(gc));
+        const float s = __builtin_amdgcn_rcpf(1.0f + exp_neg(gc));
         const float a = d[k] * uc * (s * __builtin_fmaf(gc, 1.0f - s, 1.0f)), b = d[k] * (gc * s);
         dg[k] = gc != g[k] && g[k] == g[k] ? 0.0f : a;
         du[k] = uc != u[k] && u[k] == u[k] ? 0.0f : b;
+        low |= gc < kLowGate;
+      }
+      if (low) {  // a sigmoid of less than FP32's smallest normal: hardly ever
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (!(g[k] < kLowGate)) continue;  // such a gate is not clamped
+          const float uc = clamp_up(u[k], L);
+          float a, b;
+          swiglu_grad_low(d[k], g[k], uc, a, b);
+          dg[k] = a;
+          du[k] = uc != u[k] && u[k] == u[k] ? 0.0f : b;
+        }
       }
       reinterpret_cast<uint4*>(dy)[ga] = pack8(dg);
       reinterpret_cast<uint4*>(dy)[ua] = pack8(du);
