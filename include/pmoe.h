@@ -688,6 +688,9 @@ int pmoe_mx_grouped_gemm(const void* a_codes, const void* a_sf, int a_rows, cons
 /*
  * Gradient of the rows of that product, the quantization of the rows passed
  * through: dx[r] = W[e]^T dy[r], dy BF16 [R, N], dx BF16 [R, Kd], FP32 sums rounded once.
+ * The matrices are multiplied as BF16, which holds every element at scales up to 252, the largest
+ * that pmoe_mx_quantize gives; at scales 253 and 254 (of other origin), elements of 2^128 and
+ * above count as infinite here.
  * Other arguments, limits and rows of no expert as above (for the tokens of a
  * gathered product: pmoe_permute_tokens_backward of dx).
  */

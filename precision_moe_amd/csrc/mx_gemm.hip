@@ -770,7 +770,9 @@ hipError_t launch_mx_gemm(const MxGemmParams& p, hipStream_t s) {
 // v_mfma_f32_32x32x16_bf16 reduces over 16 rows n of the matrix; a lane needs 8
 // consecutive n of one column k, while the codes run along k. So a lane reads
 // the same 4 columns (16 bits) of 8 rows, converts each pair of columns with its
-// row's scale (exact in BF16), and regroups the halves of row pairs: 4 fragments
+// row's scale (exact in BF16 up to the quantizer's largest scale, 252: subnormal values are
+// kept by the convert and the product, and only 4 * 2^126 and 2 * 2^127 on are past its
+// largest), and regroups the halves of row pairs: 4 fragments
 // of 32 columns, columns 4c + i in fragment i for lane c, with no transposition
 // through LDS. A wave owns 128 columns and every row of the tile, so a matrix tile
 // is converted once a workgroup.
