@@ -30,6 +30,23 @@ def _f(t):
     return bf16_to_f32(bf16_bits(t)).astype(np.float64) if t.dtype == torch.bfloat16 else t.cpu().numpy().astype(np.float64)
 
 
+# ----------------------------------------------------------------------------- order of the routes
+@pytest.mark.parametrize("blocks", [33, 36, 40, 41, 48, 49, 56, 57, 64, 65, 72, 80, 81, 96, 104, 113, 130])
+@pytest.mark.parametrize("E", [3, 512, 513, 1024])
+def test_order_of_any_number_of_blocks(pm, blocks, E):
+    """Above 8192 routes the sort counts blocks of 256 and sums the counts in rounds of 8, 16 or 32: ends inside and at each."""
+    rng = np.random.default_rng(blocks + E)
+    ids = rng.integers(-1, E + 1, (blocks * 256 - int(rng.integers(0, 255)), 1)).astype(np.int32)
+    got = pm.permute_tokens(None, dev(ids), E)
+    key = np.where((ids >= 0) & (ids < E), ids, E).reshape(-1)
+    route = np.argsort(key, kind="stable")[:(key < E).sum()]
+    row = np.full(key.size, -1)
+    row[route] = np.arange(len(route))
+    assert np.array_equal(got.row_of_route.cpu().numpy(), row)
+    assert np.array_equal(got.route_of_row.cpu().numpy()[:len(route)], route)
+    assert np.array_equal(got.expert_offsets.cpu().numpy(), np.searchsorted(np.sort(key), np.arange(E + 1)))
+
+
 # ----------------------------------------------------------------------------- activation
 @pytest.mark.parametrize("limit,d_bits,up_bits", [(0.0, (-10, 30), (0, 90)), (7.0, (60, 110), (-2, 2))])
 def test_activation_gradient_of_gates_far_below_zero(pm, limit, d_bits, up_bits):
