@@ -313,7 +313,7 @@ __global__ __launch_bounds__(256) void mx_activation_backward_kernel(
     } else {
       mx_values8(codes[i], y8_sf[i >> 2], g);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) g[k] = (g[k] < 0.0f ? 0.0f : 2.0f * g[k]) * d[k];
+      for (int k = 0; k < 8; ++k) g[k] = 2.0f * ((g[k] < 0.0f ? 0.0f : g[k]) * d[k]);  // 2 y alone may pass FP32's largest
       reinterpret_cast<uint4*>(dy)[i] = pack8(g);
     }
   }

@@ -71,6 +71,19 @@ def test_activation_gradient_of_gates_far_below_zero(pm, limit, d_bits, up_bits)
     assert np.all(np.abs(got - ref) <= slack + 2.0 ** -134 + 2.0 ** -8 * (np.abs(ref) + slack))
 
 
+def test_relu2_gradient_of_the_largest_values(pm):
+    """2 y is past FP32's largest number where y is at least 2^127, 2 y d h is not. The product of a value of 4 bits and
+    one of 8 is exact, so the result is rounded to BF16 once."""
+    rng = np.random.default_rng(22)
+    y = rng.choice([1.0, -1.0, 1.125, 1.5, 1.75], (40, 64)) * 2.0 ** rng.choice([119, 126, 127, 127], (40, 64))
+    codes, scales = mx.quantize(y, "e4m3")
+    v = mx.dequantize(codes, scales, "e4m3")
+    assert np.array_equal(v, y)
+    dh = _bf(rng.standard_normal((40, 64)) * 2.0 ** rng.integers(-40, -4, (40, 1)))
+    got = _f(pm.mx_activation_backward(dev_bf16(dh), dev(codes), dev(scales), pm.ACT_RELU2))
+    assert np.array_equal(got, bf16_to_f32(_bf(mx.activation_backward(bf16_to_f32(dh), v, "relu2"))))
+
+
 # ----------------------------------------------------------------------------- products
 # Experts of 255 or 256 rows, all alike, for which each tile is chosen: with N = 256 and Kd up to 512 (forward), with
 # Kd up to 256 (backward). Every expert's output has to be the first one's.
