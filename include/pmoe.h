@@ -719,7 +719,7 @@ int pmoe_mx_activation(const void* y, int R, int I, int act, float swiglu_limit,
 /*
  * Gradient of y at the values that its checkpoint stands for, the quantization of
  * h passed through: dy from dh BF16 [R, I], in FP32, rounded to BF16 once. Where the clamp
- * cuts gate or up off, their gradient is 0 (at the limit itself it is not).
+ * cuts gate or up off, their gradient is 0 (at the limit itself, and of a NaN, it is not).
  */
 int pmoe_mx_activation_backward(const void* dh, const void* y8, const void* y8_sf, int R, int I, int act,
                                 float swiglu_limit, const int32_t* row_count, void* dy, void* stream);

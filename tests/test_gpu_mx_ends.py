@@ -84,6 +84,23 @@ def test_relu2_gradient_of_the_largest_values(pm):
     assert np.array_equal(got, bf16_to_f32(_bf(mx.activation_backward(bf16_to_f32(dh), v, "relu2"))))
 
 
+def test_activation_gradient_does_not_cut_off_a_nan(pm):
+    """With a clamp, too, a block of up that reads as NaN makes d gate NaN and leaves d up what the gate says, and
+    a NaN gate makes both NaN; other blocks are those of the row without it."""
+    rng = np.random.default_rng(23)
+    y = rng.standard_normal((6, 256)) * 3
+    dh = dev_bf16(_bf(rng.standard_normal((6, 128))))
+    codes, scales = mx.quantize(y, "e4m3")
+    call = lambda s, limit: _f(pm.mx_activation_backward(dh, dev(codes), dev(s), pm.ACT_SWIGLU, swiglu_limit=limit))
+    bad = scales.copy()
+    bad[1, 5] = 255                                    # up 32 .. 63 of row 1
+    bad[4, 2] = 255                                    # gate 64 .. 95 of row 4
+    for limit in (0.0, 20.0):                          # 20: the values are below it
+        got, want = call(bad, limit), call(scales, limit)
+        want[1, 32:64] = want[4, 64:96] = want[4, 192:224] = np.nan
+        assert np.array_equal(got, want, equal_nan=True)
+
+
 # ----------------------------------------------------------------------------- products
 # Experts of 255 or 256 rows, all alike, for which each tile is chosen: with N = 256 and Kd up to 512 (forward), with
 # Kd up to 256 (backward). Every expert's output has to be the first one's.
