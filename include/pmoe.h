@@ -612,9 +612,9 @@ size_t pmoe_permute_workspace_bytes(int T, int K, int E);
  *   route_of_row   : int32 [T*K] out, the valid rows; behind them left as it was
  *   expert_offsets : int32 [E+1] out, first row of each expert; [E] = valid rows
  * T = 0 writes zeros to expert_offsets. 1 <= E <= 1024, 1 <= K <= 32 (K > E where this
- * is a share of few experts), T*K < 2^30, row_bytes a positive multiple of 16, at most 2^20. Outputs and ws share no
- * memory with each other or with an input. Alignment: x and rows 16 bytes, ws
- * 256, int64 ids 8, others 4.
+ * is a share of few experts), T*K < 2^30, row_bytes a positive multiple of 16, at most
+ * 2^20. Outputs and ws share no memory with each other or with an input. Alignment: x
+ * and rows 16 bytes, ws 256, int64 ids 8, others 4.
  */
 int pmoe_permute_tokens(const void* topk_ids, int ids_type, int T, int K, int E, int expert_offset,
                         const void* x, int row_bytes, void* rows, int32_t* row_of_route,
@@ -653,7 +653,8 @@ int pmoe_permute_tokens_backward(const void* d_rows, int type, const int32_t* ro
 #define PMOE_MX_E4M3 1
 
 /* x BF16 or FP32 [rows, n] -> codes, scales. Codes and scales share no memory with
- * each other or x. 0 <= rows, n <= 2^30, rows*n < 2^40. Alignment: x and codes 16 bytes. */
+ * each other or x. rows >= 0, n a positive multiple of 32 up to 2^30, rows*n < 2^40.
+ * Alignment: x and codes 16 bytes. */
 int pmoe_mx_quantize(const void* x, int type, int format, long long rows, int n, void* codes, void* scales,
                      void* stream);
 
@@ -718,7 +719,8 @@ int pmoe_mx_activation(const void* y, int R, int I, int act, float swiglu_limit,
 
 /*
  * Gradient of y at the values that its checkpoint stands for, the quantization of
- * h passed through: dy from dh BF16 [R, I], in FP32, rounded to BF16 once. Where the clamp
+ * h passed through: dy from dh BF16 [R, I], in FP32, rounded to BF16 once (d gate starts
+ * with dh * up, which is infinite past FP32's largest number). Where the clamp
  * cuts gate or up off, their gradient is 0 (at the limit itself, and of a NaN, it is not).
  */
 int pmoe_mx_activation_backward(const void* dh, const void* y8, const void* y8_sf, int R, int I, int act,

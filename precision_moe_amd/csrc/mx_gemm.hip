@@ -139,9 +139,10 @@ __device__ __forceinline__ bool mx_item(const int* offsets, int E, int R, int co
 // the 16 slots of 64 banks. Loads write LDS in lane order, so the lanes'
 // addresses carry the permutation: eight rows a load, the halves of 64 bytes
 // exchanged in every second load.
-// 16 tokens, 96 routes to 64 experts, N = Kd = 4096: 66 us, the 445 MB of the experts that are hit at
-// 6.7 TB/s (reads alone, some of them from the 256 MB cache). 1100 tokens, 4 routes each, 32 experts, N =
-// 1552, Kd = 2080: 33 us, 0.85 PFLOP/s: byte loads of scales and 448 tiles on 256 CUs.
+// 16 tokens, 96 routes to 64 experts, N = Kd = 4096: 67 us, the 445 MB of the experts that are hit at
+// 6.7 TB/s (reads alone, some of them from the 256 MB cache); 32 rows an expert 141 us (FP32 output: 152).
+// 1100 tokens, 4 routes each, 32 experts, N = 1552, Kd = 2080: 33 us (FP32: 37), 0.85 PFLOP/s: byte loads
+// of scales and 448 tiles on 256 CUs.
 template <int NW_, int MW_, int WN_, int WM_, int S_, bool kBytes_>
 struct MxTile {
   static constexpr int NW = NW_, MW = MW_, WN = WN_, WM = WM_, S = S_;
@@ -384,11 +385,13 @@ __global__ __launch_bounds__(C::kWaves * 64) void mx_gemm_kernel(MxGemmParams P)
 // stages at once, 16 bytes of a row: a load moves whole lines whatever it uses of them,
 // and two dwords of every row each stage cost as much as the codes.
 // An expert's rows are shared out evenly over its tiles in groups of 32, and a wave
-// multiplies the groups that its tile has. 49152 gathered rows, 64 experts, N = Kd = 4096: 522 us,
-// 3160 TFLOP/s, the matrix pipes busy for 43 % of it at 1.84 GHz: what bounds it is the power
-// that random codes draw (the instruction alone then runs at 5700 TFLOP/s, 9600 with constant
-// ones) and the loads, 64 KB a stage of 32 products a wave. Three slots of smaller stages, half lines, loads
-// in clumps and a prefetch into L2 measured no better.
+// multiplies the groups that its tile has. 49152 gathered rows, 64 experts, N = Kd = 4096: 536 us
+// (533 to 547; FP32 output 630), 3080 TFLOP/s, the matrix pipes busy for 43 % of it at 1.8 GHz: what
+// bounds it is the power that random codes draw (the instruction alone then runs at 5700 TFLOP/s,
+// 9600 with constant ones) and LDS, into which a stage of 64 products a SIMD loads 64 KB and of
+// which its waves read 192 KB (31 % of the cycles by its counter, which leaves the loads out),
+// with two slots, so that a stage's loads are waited for three quarters of a stage after their
+// issue. Three slots of smaller stages, half lines, loads in clumps and a prefetch into L2 measured no better.
 // Where Kd is not a multiple of 128, rows of scales are not whole dwords: they are loaded
 // byte by byte, each stage its own, 4 bytes of LDS a scale, beside tiles of 192 rows.
 template <int MW_, bool kBytes_>
@@ -750,6 +753,12 @@ static hipError_t run_gemm(const MxGemmParams& p, hipStream_t s) {
 // 4096: 64 experts, m = 1: 128 x 32 tiles 101 us, 256 x 128 109, 256 x 256 133; m = 32:
 // 153, 126, 145; m = 192: 443, 265, 212. One expert, 1024 rows: 33, 23, 29, and 18
 // with 128 x 128; 64 rows: 10, 18, 18, and 8 with 64 x 32.
+// How many tiles the persistent kernel wants (N = 2064, 180 or 200 rows an expert): at 72, 108, 180, 288,
+// 432 tiles, Kd = 4096, it takes 29, 30, 30, 55, 68 us and 256 x 128 tiles, which fill the chip once up
+// to 256 of them, 22, 25, 43, 63, 93; with experts of unlike size (log-normal, 1) 29, 29, 37, 61, 91 and
+// 24, 26, 47, 70, 96. With byte scales, Kd = 2080, at 180, 216, 432, 576: 25, 25, 47, 67 and 32, 32, 63,
+// 81 where experts are alike, 40, 41, 62, 78 and 34, 33, 64, 84 where they are not: below 512 the
+// gain of the first is the loss of the second, and the host cannot tell them apart.
 template <bool kBytes>
 static hipError_t run_gemm_any(const MxGemmParams& p, hipStream_t s) {
   const long experts = p.E < p.R ? p.E : p.R, m = (p.R + experts - 1) / experts;
@@ -783,8 +792,8 @@ hipError_t launch_mx_gemm(const MxGemmParams& p, hipStream_t s) {
 // products and conversions run in different pipes, but a wave issues in order.
 // Matrix rows with (n / 8) odd have the halves of each 128 bytes exchanged, so
 // that the two halves of a wave, 8 rows apart, read different banks.
-// 24576 rows, 64 experts, N = Kd = 4096: 729 us, 1130 TFLOP/s (a large BF16 product of the library: 1266
-// to 1558), the matrix pipes busy for 63 % at 1.8 GHz, the vector ones, which convert, for 40 %. 777
+// 24576 rows, 64 experts, N = Kd = 4096: 755 us (744 to 765), 1090 TFLOP/s (a large BF16 product of the library:
+// 1266 to 1558), the matrix pipes busy for 63 % at 1.7 GHz, the vector ones, which convert, for 40 %. 777
 // rows of 16 experts, N = 1536, Kd = 2048: 26 us, 24 stages of about 1 us in a row whatever the tile (24 to
 // 28 us for five of them): the conversion of 64 x 128 codes by one wave is the chain.
 template <int MW_, int KW_, int S_, bool kBytes_>

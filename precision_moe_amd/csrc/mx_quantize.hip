@@ -2,7 +2,7 @@
 // products with its 8-bit checkpoint. All are bound by memory: one pass, every
 // value read once and written once. A lane holds 8 consecutive elements, four
 // lanes a block of 32, whose largest magnitude is two quad permutations away.
-// Measured, 268M elements: FP32 to E2M1 239 us, E2M1 to BF16 112 to 118 us (5.1 and 5.8 TB/s; a
+// Measured, 268M elements: FP32 to E2M1 240 us, E2M1 to BF16 111 to 118 us (5.1 and 5.8 TB/s; a
 // plain copy reaches 5.1); up to some hundred KB the calls are launches (2.4 us).
 #include "kernels.h"
 #include "mx.h"
@@ -208,7 +208,7 @@ __device__ __forceinline__ long counted_rows(const int* row_count, long R) {
 // 32763 rows, I = 2048, with the checkpoint: 100 to 118 us for 444 MB (the rate of a copy: 87),
 // the vector instructions of the exponential, the two codings and the check of the exact value near
 // their limit; a fifth fewer of them did not shorten a forward and backward call (218 us). Four
-// groups a lane in flight took longer (6.5 instead of 3.5 us at 96 rows). 96 rows: 4.2 us.
+// groups a lane in flight took longer (6.5 instead of 3.5 us at 96 rows). 96 rows: 3.5 to 4.2 us.
 template <bool kSwiglu, bool kKeep>
 __global__ __launch_bounds__(256) void mx_activation_kernel(const uint16_t* __restrict__ y, long R, int I, float L,
                                                             const int* __restrict__ row_count,
@@ -269,7 +269,7 @@ __device__ __forceinline__ void swiglu_grad_low(float d, float g, float u, float
 //   squared ReLU  d y = 2 max(y, 0) d h
 //   SwiGLU        d gate = d h * up * s (1 + gate (1 - s)),  d up = d h * gate * s,  s = 1 / (1 + exp(-gate)),
 // gate and up clamped, and no gradient through what the clamp cut off. 32763 rows, I = 2048:
-// 96 us for 541 MB, 5.6 TB/s, more than a plain copy's 5.1; the vector units are busy throughout too.
+// 95 us for 541 MB, 5.7 TB/s, more than a plain copy's 5.1; the vector units are busy throughout too.
 template <bool kSwiglu>
 __global__ __launch_bounds__(256) void mx_activation_backward_kernel(
     const uint16_t* __restrict__ dh, const uint8_t* __restrict__ y8, const uint8_t* __restrict__ y8_sf, long R, int I,
