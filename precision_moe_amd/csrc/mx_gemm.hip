@@ -386,7 +386,7 @@ __global__ __launch_bounds__(C::kWaves * 64) void mx_gemm_kernel(MxGemmParams P)
 // and two dwords of every row each stage cost as much as the codes.
 // An expert's rows are shared out evenly over its tiles in groups of 32, and a wave
 // multiplies the groups that its tile has. 49152 gathered rows, 64 experts, N = Kd = 4096: 536 us
-// (533 to 547; FP32 output 630), 3080 TFLOP/s, the matrix pipes busy for 43 % of it at 1.8 GHz: what
+// (527 to 547; FP32 output 630), 3080 TFLOP/s, the matrix pipes busy for 43 % of it at 1.8 GHz: what
 // bounds it is the power that random codes draw (the instruction alone then runs at 5700 TFLOP/s,
 // 9600 with constant ones) and LDS, into which a stage of 64 products a SIMD loads 64 KB and of
 // which its waves read 192 KB (31 % of the cycles by its counter, which leaves the loads out),
@@ -792,7 +792,7 @@ hipError_t launch_mx_gemm(const MxGemmParams& p, hipStream_t s) {
 // products and conversions run in different pipes, but a wave issues in order.
 // Matrix rows with (n / 8) odd have the halves of each 128 bytes exchanged, so
 // that the two halves of a wave, 8 rows apart, read different banks.
-// 24576 rows, 64 experts, N = Kd = 4096: 755 us (744 to 765), 1090 TFLOP/s (a large BF16 product of the library:
+// 24576 rows, 64 experts, N = Kd = 4096: 760 us (744 to 765), 1085 TFLOP/s (a large BF16 product of the library:
 // 1266 to 1558), the matrix pipes busy for 63 % at 1.7 GHz, the vector ones, which convert, for 40 %. 777
 // rows of 16 experts, N = 1536, Kd = 2048: 26 us, 24 stages of about 1 us in a row whatever the tile (24 to
 // 28 us for five of them): the conversion of 64 x 128 codes by one wave is the chain.
